@@ -11,6 +11,8 @@ from ._abi import (GDN_BF16, GDN_CP_AUTO, GDN_CP_FORCE, GDN_CP_OFF, GDN_FP32, Gd
                    gdn_recurrent_step, gdn_set_spin_limit, gdn_sync_status)
 from .api import (chunk_gated_delta_rule, chunk_gated_delta_rule_bwd,
                   chunk_gated_delta_rule_fwd, recurrent_step)
+from .layer import (gated_linear_recurrence, gated_linear_recurrence_bwd,
+                    gated_linear_recurrence_fwd, gated_linear_recurrence_step)
 
 _abi.load()
 
@@ -19,4 +21,6 @@ __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_
            "gdn_abi_version", "gdn_fwd_workspace_size", "gdn_fwd_ctx_size", "gdn_chunk_fwd",
            "gdn_bwd_workspace_size", "gdn_chunk_bwd", "gdn_sync_status", "gdn_last_error",
            "gdn_set_spin_limit", "gdn_profile_begin", "gdn_profile_end", "GdnError", "GDN_FP32", "GDN_BF16", "GDN_CP_AUTO",
-           "GDN_CP_OFF", "GDN_CP_FORCE"]
+           "GDN_CP_OFF", "GDN_CP_FORCE",
+           "gated_linear_recurrence", "gated_linear_recurrence_fwd",
+           "gated_linear_recurrence_bwd", "gated_linear_recurrence_step"]

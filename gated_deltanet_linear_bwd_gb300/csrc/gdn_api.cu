@@ -16,6 +16,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_layer_internal.h"
 
 namespace gdn {
 
@@ -26,7 +27,7 @@ static thread_local std::string t_last_error;
 static constexpr long long kDefaultSpinLimit = 1ll << 21;
 static std::atomic<long long> g_spin_limit{kDefaultSpinLimit};
 
-static gdn_status fail(gdn_status code, const char *fmt, ...) {
+gdn_status fail(gdn_status code, const char *fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -36,7 +37,7 @@ static gdn_status fail(gdn_status code, const char *fmt, ...) {
     return code;
 }
 
-static gdn_status cuda_fail(cudaError_t e, const char *what) {
+gdn_status cuda_fail(cudaError_t e, const char *what) {
     return fail(GDN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -71,6 +72,16 @@ static gdn_status device_info(DeviceInfo **out) {
         d.ready = true;
     }
     *out = &d;
+    return GDN_OK;
+}
+
+gdn_status layer_device(LayerDevice *out) {
+    DeviceInfo *d = nullptr;
+    const gdn_status st = device_info(&d);
+    if (st != GDN_OK) return st;
+    out->sms = d->sms;
+    out->status = d->status;
+    out->spin_limit = g_spin_limit.load();
     return GDN_OK;
 }
 
