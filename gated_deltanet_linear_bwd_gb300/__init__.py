@@ -11,8 +11,10 @@ from ._abi import (GDN_BF16, GDN_CP_AUTO, GDN_CP_FORCE, GDN_CP_OFF, GDN_FP32, Gd
                    gdn_recurrent_step, gdn_set_spin_limit, gdn_sync_status)
 from .api import (chunk_gated_delta_rule, chunk_gated_delta_rule_bwd,
                   chunk_gated_delta_rule_fwd, recurrent_step)
-from .layer import (gated_linear_recurrence, gated_linear_recurrence_bwd,
-                    gated_linear_recurrence_fwd, gated_linear_recurrence_step)
+from .layer import (MxTensor, add_rms_norm, add_rms_norm_bwd, add_rms_norm_fwd,
+                    gated_linear_recurrence, gated_linear_recurrence_bwd,
+                    gated_linear_recurrence_fwd, gated_linear_recurrence_step, mx_dequantize,
+                    mx_from_parts, mx_linear, mx_matmul, mx_quantize)
 
 _abi.load()
 
@@ -23,4 +25,6 @@ __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_
            "gdn_set_spin_limit", "gdn_profile_begin", "gdn_profile_end", "GdnError", "GDN_FP32", "GDN_BF16", "GDN_CP_AUTO",
            "GDN_CP_OFF", "GDN_CP_FORCE",
            "gated_linear_recurrence", "gated_linear_recurrence_fwd",
-           "gated_linear_recurrence_bwd", "gated_linear_recurrence_step"]
+           "gated_linear_recurrence_bwd", "gated_linear_recurrence_step",
+           "add_rms_norm", "add_rms_norm_fwd", "add_rms_norm_bwd",
+           "MxTensor", "mx_quantize", "mx_dequantize", "mx_from_parts", "mx_matmul", "mx_linear"]

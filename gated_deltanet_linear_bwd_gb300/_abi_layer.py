@@ -24,9 +24,41 @@ class gdn_linrec_step_args(ctypes.Structure):
                 ("D", _i32), ("dtype", _i32), ("h", _vp), ("out_state", _vp)]
 
 
-STRUCTS = (gdn_linrec_fwd_args, gdn_linrec_bwd_args, gdn_linrec_step_args)
-EXPORTS = ("gdn_linrec_fwd", "gdn_linrec_bwd_workspace_size", "gdn_linrec_bwd",
-           "gdn_linrec_step")
+class gdn_mx_quantize_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("rows", _i32), ("K", _i32), ("dtype", _i32), ("format", _i32),
+                ("data", _vp), ("scales", _vp)]
+
+
+class gdn_mx_dequantize_args(ctypes.Structure):
+    _fields_ = [("data", _vp), ("scales", _vp), ("rows", _i32), ("K", _i32), ("dtype", _i32),
+                ("format", _i32), ("x", _vp)]
+
+
+class gdn_mx_matmul_args(ctypes.Structure):
+    _fields_ = [("a", _vp), ("a_scales", _vp), ("b", _vp), ("b_scales", _vp), ("M", _i32),
+                ("N", _i32), ("K", _i32), ("format", _i32), ("out_dtype", _i32), ("c", _vp)]
+
+
+class gdn_rms_norm_fwd_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("weight", _vp), ("rows", _i32), ("D", _i32),
+                ("dtype", _i32), ("eps", _f32), ("mx", _i32), ("y", _vp), ("scales", _vp),
+                ("sum", _vp), ("rstd", _vp)]
+
+
+class gdn_rms_norm_bwd_args(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("sum", _vp), ("weight", _vp), ("rstd", _vp), ("d_sum", _vp),
+                ("rows", _i32), ("D", _i32), ("dtype", _i32), ("ds", _vp), ("dweight", _vp)]
+
+
+GDN_MXFP8, GDN_MXFP4 = 0, 1
+
+_PLAIN = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_step": gdn_linrec_step_args,
+          "gdn_mx_quantize": gdn_mx_quantize_args, "gdn_mx_dequantize": gdn_mx_dequantize_args,
+          "gdn_mx_matmul": gdn_mx_matmul_args, "gdn_rms_norm_fwd": gdn_rms_norm_fwd_args}
+_WITH_WORKSPACE = {"gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args}
+STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
+EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \
+    tuple(n + "_workspace_size" for n in _WITH_WORKSPACE) + ("gdn_mx_scale_bytes",)
 
 _declared = False
 
@@ -37,15 +69,16 @@ def load():
     lib = _abi.load()
     if not _declared:
         p = ctypes.POINTER
-        for name, args in (("gdn_linrec_fwd", gdn_linrec_fwd_args),
-                           ("gdn_linrec_step", gdn_linrec_step_args)):
+        for name, args in _PLAIN.items():
             getattr(lib, name).restype = _i32
             getattr(lib, name).argtypes = [p(args), _vp]
-        for name, args in (("gdn_linrec_bwd", gdn_linrec_bwd_args),):
+        for name, args in _WITH_WORKSPACE.items():
             getattr(lib, name).restype = _i32
             getattr(lib, name).argtypes = [p(args), _vp, ctypes.c_size_t, _vp]
             getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
             getattr(lib, name + "_workspace_size").argtypes = [p(args)]
+        lib.gdn_mx_scale_bytes.restype = ctypes.c_size_t
+        lib.gdn_mx_scale_bytes.argtypes = [_i32, _i32]
         _declared = True
     return lib
 

@@ -1,0 +1,38 @@
+// gdn_layer_util.cu -- the sum over rows that the layer operators' weight
+// gradients end with.
+#include "gdn_layer_internal.h"
+
+namespace gdn {
+namespace {
+
+// out[d] = sum over rows of partial[row][d], in a fixed order.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, int rows, int D,
+                                                          float *out) {
+    __shared__ float strip[32][33];
+    pdl_enter();
+    const int lane = threadIdx.x & 31, strip_no = threadIdx.x >> 5;
+    const int d = blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (d < D)
+        for (int r = strip_no; r < rows; r += 32) t += partial[(long long)r * D + d];
+    strip[strip_no][lane] = t;
+    __syncthreads();
+    if (strip_no == 0 && d < D) {
+        t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) t += strip[k][lane];
+        out[d] = t;
+    }
+}
+
+}  // namespace
+
+cudaError_t column_sum(const float *partial, int rows, int D, float *out, cudaStream_t s) {
+    prof_before("column_sum", s);
+    const cudaError_t e = launch_pdl(column_sum_kernel, dim3((D + 31) / 32), dim3(1024), 0, s, partial,
+                                     rows, D, out);
+    prof_after(s);
+    return e;
+}
+
+}  // namespace gdn

@@ -321,26 +321,6 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(BwdArgs a, Shape s) {
     }
 }
 
-// out[d] = sum over rows of partial[row][d], in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, int rows, int D,
-                                                          float *out) {
-    __shared__ float strip[32][33];
-    pdl_enter();
-    const int lane = threadIdx.x & 31, strip_no = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + lane;
-    float t = 0.f;
-    if (d < D)
-        for (int r = strip_no; r < rows; r += 32) t += partial[(long long)r * D + d];
-    strip[strip_no][lane] = t;
-    __syncthreads();
-    if (strip_no == 0 && d < D) {
-        t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) t += strip[k][lane];
-        out[d] = t;
-    }
-}
-
 // One token: a channel per thread.
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(256) step_kernel(const T *x, const T *g, const float *scale,
@@ -471,10 +451,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_byte
     cudaStream_t q = (cudaStream_t)stream;
     cudaError_t e = linrec::launch("linrec_bwd", GDN_LINREC_KERNEL(linrec::bwd_kernel), b, s, q);
     if (e == cudaSuccess && sums) {
-        prof_before("linrec_column_sum", q);
-        e = launch_pdl(linrec::column_sum_kernel, dim3((a->D + 31) / 32), dim3(1024), 0, q,
-                       (const float *)ws, s.lanes_n, a->D, a->d_gate_scale);
-        prof_after(q);
+        e = column_sum((const float *)ws, s.lanes_n, a->D, a->d_gate_scale, q);
     }
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear recurrence backward launch");
 }

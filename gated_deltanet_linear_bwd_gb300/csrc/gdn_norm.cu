@@ -1,0 +1,364 @@
+// gdn_norm.cu -- residual addition with the RMS norm, to the input's type or to
+// MXFP8 with its scales, and the backward pass.
+//
+// A row is held in registers, 16 elements to a thread, by `tpr` threads (a power
+// of two): loaded once, reduced by shuffles (and through shared memory where a row
+// spans warps), scaled and written.  Rows of few columns share a CTA.
+#include <algorithm>
+
+#include "gdn_layer_internal.h"
+#include "gdn_mx.cuh"
+
+namespace gdn {
+namespace norm {
+namespace {
+
+constexpr int kPer = 16;           // elements of a row in one thread
+constexpr int kMaxD = 1024 * kPer;
+
+// VEC elements of T as one 16-byte load (or one element where rows do not start
+// on 16 bytes).
+template <typename T, int VEC>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *v) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Chunk<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float *v) {
+        const float4 r = *reinterpret_cast<const float4 *>(p);
+        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float *v) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <typename T>
+struct Chunk<T, 1> {
+    static __device__ __forceinline__ void load(const T *p, float *v) { v[0] = to_f(*p); }
+    static __device__ __forceinline__ void store(T *p, const float *v) { from_f(p, v[0]); }
+};
+
+// Sum over a row's `tpr` threads; every one of them gets it.  `red` holds one
+// float per warp; the whole CTA calls.
+__device__ __forceinline__ float row_sum(float x, int tpr, float *red) {
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (tpr <= 32) return x;
+    const int warp = threadIdx.x >> 5, per = tpr >> 5;
+    __syncthreads();               // the row before is done with `red`
+    if ((threadIdx.x & 31) == 0) red[warp] = x;
+    __syncthreads();
+    x = 0.f;
+    for (int w = warp / per * per, e = w + per; w < e; ++w) x += red[w];
+    return x;
+}
+
+struct FwdArgs {
+    const void *x, *res, *w;
+    void *y, *sum;
+    uint8_t *scales;
+    float *rstd;
+    float eps;
+    int rows, D, tpr, ktiles;
+};
+
+template <typename T, int VEC, bool MX>
+__global__ void __launch_bounds__(1024) fwd_kernel(FwdArgs a) {
+    using C = Chunk<T, VEC>;
+    constexpr int NV = kPer / VEC;
+    __shared__ float red[32];
+    pdl_enter();
+
+    const int tid = threadIdx.x & (a.tpr - 1), per_cta = blockDim.x / a.tpr;
+    const int group = threadIdx.x / a.tpr;
+    float w[kPer];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int col = (v * a.tpr + tid) * VEC;
+        if (col < a.D) C::load(reinterpret_cast<const T *>(a.w) + col, w + v * VEC);
+    }
+    // with MX scales the last tile's rows past the end are walked too: their scales are zeros
+    const long long last = MX ? (a.rows + 127ll) / 128 * 128 : a.rows;
+    for (long long r0 = blockIdx.x * per_cta; r0 < last; r0 += gridDim.x * per_cta) {
+        const long long row = r0 + group;
+        const bool live = row < a.rows;
+        const long long base = row * a.D;
+        float s[kPer], ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = (v * a.tpr + tid) * VEC;
+            const bool in = live && col < a.D;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[v * VEC + i] = 0.f;
+            if (in) C::load(reinterpret_cast<const T *>(a.x) + base + col, s + v * VEC);
+            if (in && a.res) {
+                float r[VEC];
+                C::load(reinterpret_cast<const T *>(a.res) + base + col, r);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) s[v * VEC + i] += r[i];
+                C::store(reinterpret_cast<T *>(a.sum) + base + col, s + v * VEC);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) ss += s[v * VEC + i] * s[v * VEC + i];
+        }
+        const float rstd = rsqrtf(row_sum(ss, a.tpr, red) / (float)a.D + a.eps);
+        if (live && a.rstd && tid == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = (v * a.tpr + tid) * VEC;
+            float y[VEC];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                y[i] = col < a.D ? s[v * VEC + i] * rstd * w[v * VEC + i] : 0.f;
+                if (MX) amax = max(amax, mx::abs_bits(y[i]));
+            }
+            if constexpr (!MX) {
+                if (live && col < a.D) C::store(reinterpret_cast<T *>(a.y) + base + col, y);
+            } else {
+                // a block of 32 columns is 32 / VEC neighbouring lanes
+#pragma unroll
+                for (int o = 1; o < 32 / VEC; o <<= 1)
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const int byte = live && col < a.D ? mx::scale_byte<false>(amax) : 0;
+                if (col < a.ktiles * 128 && col % 32 == 0 && row < last)
+                    a.scales[mx::scale_offset(row, col / 32, a.ktiles)] = (uint8_t)byte;
+                if (live && col < a.D) {
+                    const float f = mx::scale_factor(byte);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) y[i] = byte == 255 ? 0.f : y[i] * f;
+                    uint32_t *o = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(a.y) + base + col);
+                    const uint32_t q0 = mx::e4m3x4(y[0], y[1], y[2], y[3]);
+                    if constexpr (VEC == 8)
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(q0, mx::e4m3x4(y[4], y[5], y[6], y[7]));
+                    else
+                        *o = q0;
+                }
+            }
+        }
+    }
+}
+
+struct BwdArgs {
+    const void *dy, *s, *w, *dsum;
+    const float *rstd;
+    void *ds;
+    float *partial;                // [gridDim.x][D]
+    int rows, D, tpr;
+};
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024) bwd_kernel(BwdArgs a) {
+    using C = Chunk<T, VEC>;
+    constexpr int NV = kPer / VEC;
+    extern __shared__ float sums[];          // [rows per CTA][D], where a CTA holds several rows
+    __shared__ float red[32];
+    pdl_enter();
+
+    const int tid = threadIdx.x & (a.tpr - 1), per_cta = blockDim.x / a.tpr;
+    const int group = threadIdx.x / a.tpr;
+    float w[kPer], dw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = dw[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int col = (v * a.tpr + tid) * VEC;
+        if (col < a.D) C::load(reinterpret_cast<const T *>(a.w) + col, w + v * VEC);
+    }
+    for (long long r0 = blockIdx.x * per_cta; r0 < a.rows; r0 += gridDim.x * per_cta) {
+        const long long row = r0 + group;
+        const bool live = row < a.rows;
+        const long long base = row * a.D;
+        const float rstd = live ? a.rstd[row] : 0.f;
+        float xh[kPer], wdy[kPer], dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = (v * a.tpr + tid) * VEC;
+            const bool in = live && col < a.D;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) xh[v * VEC + i] = wdy[v * VEC + i] = 0.f;
+            if (in) {
+                C::load(reinterpret_cast<const T *>(a.s) + base + col, xh + v * VEC);
+                C::load(reinterpret_cast<const T *>(a.dy) + base + col, wdy + v * VEC);
+            }
+#pragma unroll
+            for (int i = v * VEC; i < (v + 1) * VEC; ++i) {
+                xh[i] *= rstd;
+                dw[i] += wdy[i] * xh[i];
+                wdy[i] *= w[i];
+                dot += wdy[i] * xh[i];
+            }
+        }
+        const float c = row_sum(dot, a.tpr, red) / (float)a.D;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = (v * a.tpr + tid) * VEC;
+            if (!live || col >= a.D) continue;
+            float d[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) d[i] = 0.f;
+            if (a.dsum) C::load(reinterpret_cast<const T *>(a.dsum) + base + col, d);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                d[i] += rstd * (wdy[v * VEC + i] - xh[v * VEC + i] * c);
+            C::store(reinterpret_cast<T *>(a.ds) + base + col, d);
+        }
+    }
+    // the CTA's sum of dy xh over its rows, the row groups added in order
+    if (per_cta > 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int col = (v * a.tpr + tid) * VEC + i;
+                if (col < a.D) sums[group * a.D + col] = dw[v * VEC + i];
+            }
+        __syncthreads();
+        for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
+            float t = 0.f;
+            for (int k = 0; k < per_cta; ++k) t += sums[k * a.D + col];
+            a.partial[(long long)blockIdx.x * a.D + col] = t;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int col = (v * a.tpr + tid) * VEC + i;
+                if (col < a.D) a.partial[(long long)blockIdx.x * a.D + col] = dw[v * VEC + i];
+            }
+    }
+}
+
+// Threads of a row: the least power of two that holds it, 16 elements each (8 at
+// least: two MX blocks of bf16 or one of fp32 in neighbouring lanes).
+int row_threads(int D) {
+    int t = 8;
+    while (t * kPer < D) t *= 2;
+    return t;
+}
+int cta_threads(int tpr) { return std::max(tpr, 256); }
+
+// Whole 16-byte chunks in every row.
+bool vector_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
+
+// CTAs of the backward pass: enough to fill the GPU (4 of 256 threads per SM), as
+// each leaves a row of partial sums of dweight.
+int bwd_ctas(int rows, int D, int sms) {
+    const int tpr = row_threads(D), threads = cta_threads(tpr), per = threads / tpr;
+    return std::max(1, std::min((rows + per - 1) / per, sms * std::max(1, 1024 / threads)));
+}
+
+// The GPU's SM count enters the workspace's size, which is asked for without a
+// device: sized for the most SMs of an sm_103a part.
+constexpr int kMaxSms = 160;
+
+gdn_status check(int rows, int D, int dtype) {
+    if (rows < 0 || D < 1) return fail(GDN_ERR_INVALID_ARG, "bad sizes rows=%d D=%d", rows, D);
+    if (D > kMaxD) return fail(GDN_ERR_UNSUPPORTED, "D = %d (at most %d)", D, kMaxD);
+    if (dtype != GDN_FP32 && dtype != GDN_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", dtype);
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace norm
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_rms_norm_fwd(const gdn_rms_norm_fwd_args *a, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = norm::check(a->rows, a->D, a->dtype);
+    if (st != GDN_OK) return st;
+    if (a->mx != 0 && a->mx != 1) return fail(GDN_ERR_INVALID_ARG, "mx = %d (0 or 1)", a->mx);
+    if (a->mx && a->D % 32 != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "D = %d: MXFP8 output takes multiples of 32", a->D);
+    if (a->rows == 0) return GDN_OK;
+    if (!a->x || !a->weight || !a->y || (a->mx && !a->scales) || (a->residual && !a->sum))
+        return fail(GDN_ERR_INVALID_ARG, "x, weight, y, scales (for MXFP8) and sum (with a residual) are required");
+    if (misaligned(a->x) || misaligned(a->residual) || misaligned(a->weight) || misaligned(a->y) ||
+        misaligned(a->scales) || misaligned(a->sum) || misaligned(a->rstd))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    norm::FwdArgs f{a->x, a->residual, a->weight, a->y, a->sum, a->scales, a->rstd, a->eps,
+                    a->rows, a->D, norm::row_threads(a->D), (a->D + 127) / 128};
+    const int threads = norm::cta_threads(f.tpr), per = threads / f.tpr;
+    const long long rows = a->mx ? (a->rows + 127ll) / 128 * 128 : a->rows;
+    const long long ctas = std::min<long long>((rows + per - 1) / per, (long long)dev.sms * (2048 / threads));
+    const bool vec = norm::vector_rows(a->dtype, a->D);
+    auto k = a->dtype == GDN_BF16
+                 ? (a->mx ? norm::fwd_kernel<__nv_bfloat16, 8, true>
+                    : vec ? norm::fwd_kernel<__nv_bfloat16, 8, false>
+                          : norm::fwd_kernel<__nv_bfloat16, 1, false>)
+                 : (a->mx ? norm::fwd_kernel<float, 4, true>
+                    : vec ? norm::fwd_kernel<float, 4, false> : norm::fwd_kernel<float, 1, false>);
+    cudaStream_t q = (cudaStream_t)stream;
+    prof_before("rms_norm_fwd", q);
+    const cudaError_t e = launch_pdl(k, dim3((unsigned)ctas), dim3(threads), 0, q, f);
+    prof_after(q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "rms norm launch");
+}
+
+size_t gdn_rms_norm_bwd_workspace_size(const gdn_rms_norm_bwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (norm::check(a->rows, a->D, a->dtype) != GDN_OK) return 0;
+    return std::max<size_t>(256, (size_t)norm::bwd_ctas(a->rows, a->D, norm::kMaxSms) * a->D * 4);
+}
+
+gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = norm::check(a->rows, a->D, a->dtype);
+    if (st != GDN_OK) return st;
+    if ((a->rows > 0 && (!a->dy || !a->sum || !a->rstd || !a->ds)) || !a->weight || !a->dweight)
+        return fail(GDN_ERR_INVALID_ARG, "dy, sum, weight, rstd, ds and dweight are required");
+    if (misaligned(a->dy) || misaligned(a->sum) || misaligned(a->weight) || misaligned(a->rstd) ||
+        misaligned(a->d_sum) || misaligned(a->ds) || misaligned(a->dweight))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    const size_t need = gdn_rms_norm_bwd_workspace_size(a);
+    if (!ws || misaligned(ws) || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    const int ctas = norm::bwd_ctas(a->rows, a->D, std::min(dev.sms, norm::kMaxSms));
+    const int tpr = norm::row_threads(a->D), threads = norm::cta_threads(tpr), per = threads / tpr;
+    const norm::BwdArgs b{a->dy, a->sum, a->weight, a->d_sum, a->rstd, a->ds, (float *)ws,
+                          a->rows, a->D, tpr};
+    const bool vec = norm::vector_rows(a->dtype, a->D);
+    auto k = a->dtype == GDN_BF16 ? (vec ? norm::bwd_kernel<__nv_bfloat16, 8> : norm::bwd_kernel<__nv_bfloat16, 1>)
+                                  : (vec ? norm::bwd_kernel<float, 4> : norm::bwd_kernel<float, 1>);
+    // rows that share a CTA: 256 / tpr of at most 16 tpr columns, 16 KB of sums
+    const size_t smem = per > 1 ? (size_t)per * a->D * sizeof(float) : 0;
+    cudaStream_t q = (cudaStream_t)stream;
+    prof_before("rms_norm_bwd", q);
+    cudaError_t e = launch_pdl(k, dim3(ctas), dim3(threads), smem, q, b);
+    prof_after(q);
+    if (e == cudaSuccess) e = column_sum((const float *)ws, ctas, a->D, a->dweight, q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "rms norm backward launch");
+}
+
+}  // extern "C"

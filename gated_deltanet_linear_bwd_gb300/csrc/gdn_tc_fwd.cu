@@ -820,6 +820,21 @@ cudaError_t make_map_tiles(CUtensorMap *m, const void *base, long long rows_tota
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// [rows, bytes] of 8-bit elements (bytes a multiple of 16) viewed as 2-D: boxes of
+// 128 bytes x box_rows rows, past the end reading as zeros.
+cudaError_t make_map_bytes(CUtensorMap *m, const void *base, long long rows, long long bytes,
+                           int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+                                dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 bool supported(const Plan &p) {
     // TMA row coordinates are 32-bit ints: the largest, of the chunk-state tiles
     // (two 128-row halves per (chunk, head)), is 2 (chunk * H + head) * 128 + 128

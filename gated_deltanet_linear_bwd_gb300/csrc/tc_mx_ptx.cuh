@@ -1,0 +1,114 @@
+// tc_mx_ptx.cuh -- inline-PTX wrappers for the block-scaled tcgen05 products:
+// MXFP8 (kind::mxf8f6f4, one scale per 32 elements of K) and MXFP4 (kind::mxf4),
+// their scales copied from shared memory to TMEM, and what clusters need.
+//
+// Operand tiles are K-major rows of 128 bytes in the 128-byte swizzle, as in
+// tc_ptx.cuh: 128 elements of 8 bits or 256 of 4 bits; one MMA takes 32 bytes of a
+// row (K = 32 or 64).
+//
+// Scales of 128 rows x 4 blocks are 512 bytes, the bytes of (row, block) at
+// 16 (row % 32) + 4 (row / 32) + block: 32 rows of 16 bytes, which tcgen05.cp
+// 32x128b.warpx4 puts into 4 TMEM columns of every lane quarter: column row / 32,
+// lane row % 32, a byte per block.  An MMA names its blocks' bytes by the scale id
+// in its instruction descriptor.
+#pragma once
+
+#include "tc_ptx.cuh"
+
+namespace gdn {
+namespace tc {
+
+// Instruction descriptor of the block-scaled kinds: e4m3 (0) or e2m1 (1) A and B,
+// power-of-two scales, N >> 3 in bits 17-22, M >> 4 in bits 24-28; `id` is the
+// scale byte both operands take.
+__host__ __device__ constexpr uint32_t idesc_mx(bool fp4, int M, int N, int id) {
+    return ((uint32_t)id << 4) | ((fp4 ? 1u : 0u) << 7) | ((fp4 ? 1u : 0u) << 10) |
+           ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+           ((uint32_t)id << 29);
+}
+
+// Descriptor of a 512-byte scale tile for tcgen05.cp: no swizzle, 8-row groups of
+// 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// D (+)= A B with scales; warp-collective like mma_bf16.
+template <bool FP4>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                       uint32_t sb, uint32_t accumulate) {
+    if (FP4)
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+}
+
+// A 512-byte scale tile to 4 TMEM columns; in order with the MMAs the same warp
+// issues.  Warp-collective.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile(
+        "{\n"
+        ".reg .pred e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n"
+        "}\n" ::"r"(taddr),
+        "l"(desc)
+        : "memory");
+}
+
+// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster meets; writes before it are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `saddr` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+}  // namespace tc
+}  // namespace gdn

@@ -1,5 +1,6 @@
 """Torch-facing wrappers of the operators around the gated delta rule: the
-per-channel gated linear recurrence.  As in api.py they check arguments,
+residual addition with the RMS norm, microscaled (MX) matrices and their product,
+and the per-channel gated linear recurrence.  As in api.py they check arguments,
 allocate outputs and workspace with torch on the tensors' device and pass raw
 pointers on the current stream; every computation runs in libgdn.so.
 """
@@ -129,3 +130,198 @@ def gated_linear_recurrence_step(x, g, state, gate_scale=None, out_state=None):
     a.h, a.out_state = h.data_ptr(), state.data_ptr() if out_state is None else out_state.data_ptr()
     _abi_layer.call("gdn_linrec_step", a, _stream(dev))
     return h
+
+
+# ------------------------------------------------------------------ microscaled matrices
+_FORMATS = {"mxfp8": _abi_layer.GDN_MXFP8, "mxfp4": _abi_layer.GDN_MXFP4}
+
+
+def _scale_shape(rows, K):
+    """Tiles of 128 rows x 4 blocks, indexed [row tile][K tile][row % 32][row / 32][block]."""
+    return (-(-rows // 128), -(-K // 128), 32, 4, 4)
+
+
+class MxTensor:
+    """A microscaled matrix [rows, K]: `data` (float8_e4m3fn [rows, K] for "mxfp8",
+    uint8 [rows, K / 2] of two e2m1 elements for "mxfp4", the first in the low half)
+    and `scales` (uint8 exponents + 127 for each row and 32 columns, in the product's
+    order: tiles [row / 128][block / 4][row % 32][row % 128 / 32][block % 4])."""
+    __slots__ = ("data", "scales", "fmt", "shape")
+
+    def __init__(self, data, scales, fmt, shape):
+        self.data, self.scales, self.fmt, self.shape = data, scales, fmt, shape
+
+    @classmethod
+    def empty(cls, rows, K, fmt, device):
+        if fmt not in _FORMATS:
+            raise ValueError(f"unknown format {fmt!r} (mxfp8 or mxfp4)")
+        if K % 32:
+            raise ValueError(f"K = {K}: microscaled matrices take multiples of 32 columns")
+        data = (torch.empty(rows, K, dtype=torch.float8_e4m3fn, device=device) if fmt == "mxfp8"
+                else torch.empty(rows, K // 2, dtype=torch.uint8, device=device))
+        return cls(data, torch.empty(_scale_shape(rows, K), dtype=torch.uint8, device=device), fmt,
+                   (rows, K))
+
+    @property
+    def device(self):
+        return self.data.device
+
+
+def _check_mx(name, t, device=None):
+    if not isinstance(t, MxTensor):
+        raise ValueError(f"{name} must be an MxTensor")
+    rows, K = t.shape
+    if t.fmt == "mxfp8":
+        _check(name + ".data", t.data, torch.float8_e4m3fn, (rows, K), device)
+    else:
+        _check(name + ".data", t.data, torch.uint8, (rows, K // 2), device)
+    _check(name + ".scales", t.scales, torch.uint8, _scale_shape(rows, K), t.data.device)
+
+
+def mx_quantize(x, fmt="mxfp4"):
+    """x [..., K] (bf16 or fp32) as an MxTensor of [rows, K]: for each row and 32
+    columns the least power-of-two scale with which nothing saturates, elements
+    rounded to nearest even."""
+    dtype = _dtype("x", x)
+    if x.dim() < 1:
+        raise ValueError("expected [..., K]")
+    _check("x", x)
+    K = x.shape[-1]
+    rows = x.numel() // K if K else 0
+    t = MxTensor.empty(rows, K, fmt, x.device)
+    a = _abi_layer.gdn_mx_quantize_args(x.data_ptr(), rows, K, dtype, _FORMATS[fmt],
+                                        t.data.data_ptr(), t.scales.data_ptr())
+    _abi_layer.call("gdn_mx_quantize", a, _stream(x.device))
+    return t
+
+
+def mx_dequantize(t, dtype=torch.float32):
+    """The values of an MxTensor, [rows, K] in bf16 or fp32."""
+    _check_mx("t", t)
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    x = torch.empty(t.shape, dtype=dtype, device=t.device)
+    a = _abi_layer.gdn_mx_dequantize_args(t.data.data_ptr(), t.scales.data_ptr(), *t.shape,
+                                          _DT[dtype], _FORMATS[t.fmt], x.data_ptr())
+    _abi_layer.call("gdn_mx_dequantize", a, _stream(t.device))
+    return x
+
+
+def mx_from_parts(data, exponents, fmt):
+    """An MxTensor from its elements (as MxTensor.data) and row-major scale bytes
+    [rows, K / 32], as checkpoints hold them: laid out once, on load."""
+    rows, blocks = exponents.shape
+    t = MxTensor.empty(rows, 32 * blocks, fmt, data.device)
+    _check("exponents", exponents, torch.uint8, None, data.device)
+    _check("data", data, t.data.dtype, tuple(t.data.shape))
+    R, B = t.scales.shape[:2]
+    padded = torch.zeros(128 * R, 4 * B, dtype=torch.uint8, device=data.device)
+    padded[:rows, :blocks] = exponents
+    t.scales.copy_(padded.view(R, 4, 32, B, 4).permute(0, 3, 2, 1, 4))
+    t.data = data
+    return t
+
+
+def mx_matmul(a, b, out_dtype=torch.bfloat16):
+    """a b^T of MxTensors a [M, K] and b [N, K] of one format: [M, N], summed in fp32."""
+    _check_mx("a", a)
+    _check_mx("b", b, a.device)
+    if a.fmt != b.fmt or a.shape[1] != b.shape[1]:
+        raise ValueError(f"a is {a.fmt} {a.shape}, b is {b.fmt} {b.shape}: one format and one K")
+    if out_dtype not in _DT:
+        raise ValueError(f"unsupported dtype {out_dtype}")
+    (M, K), N = a.shape, b.shape[0]
+    c = torch.empty(M, N, dtype=out_dtype, device=a.device)
+    args = _abi_layer.gdn_mx_matmul_args(a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
+                                         b.scales.data_ptr(), M, N, K, _FORMATS[a.fmt],
+                                         _DT[out_dtype], c.data_ptr())
+    _abi_layer.call("gdn_mx_matmul", args, _stream(a.device))
+    return c
+
+
+def mx_linear(x, weight, out_dtype=None):
+    """x weight^T for x [..., K] (bf16 or fp32, quantised here to the weight's format,
+    or an MxTensor of it) and a weight MxTensor [N, K].  Returns [..., N] in x's type
+    (bf16 for an MxTensor), or in `out_dtype`."""
+    if isinstance(x, MxTensor):
+        return mx_matmul(x, weight, out_dtype or torch.bfloat16)
+    _check_mx("weight", weight, x.device)
+    if x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x has shape {tuple(x.shape)}, the weight {weight.shape}")
+    y = mx_matmul(mx_quantize(x, weight.fmt), weight, out_dtype or x.dtype)
+    return y.view(*x.shape[:-1], weight.shape[0])
+
+
+# ------------------------------------------------------------------ residual addition + RMS norm
+def add_rms_norm_fwd(x, weight, residual=None, eps=1e-6, out=None, save_rstd=False):
+    """s = x + residual; y = s (mean(s^2) + eps)^-1/2 weight, over the last axis of
+    x [..., D] (bf16 or fp32).  Returns (y, s, rstd): y in x's type, or with
+    out="mxfp8" an MxTensor of [rows, D]; s in x's type (x itself without a
+    residual); rstd [rows] fp32 with save_rstd, else None."""
+    dtype = _dtype("x", x)
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., D]")
+    if out not in (None, "mxfp8"):
+        raise ValueError(f"unknown output {out!r} (None or mxfp8)")
+    dev, D = x.device, x.shape[-1]
+    rows = x.numel() // D
+    _check("x", x)
+    _check("weight", weight, x.dtype, (D,), dev)
+    _check("residual", residual, x.dtype, tuple(x.shape), dev)
+    y = torch.empty_like(x) if out is None else MxTensor.empty(rows, D, out, dev)
+    s = x if residual is None else torch.empty_like(x)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if save_rstd else None
+    a = _abi_layer.gdn_rms_norm_fwd_args(
+        x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, D, dtype, eps, int(out is not None),
+        y.data_ptr() if out is None else y.data.data_ptr(),
+        None if out is None else y.scales.data_ptr(),
+        None if residual is None else s.data_ptr(), _ptr(rstd))
+    _abi_layer.call("gdn_rms_norm_fwd", a, _stream(dev))
+    return y, s, rstd
+
+
+def add_rms_norm_bwd(dy, s, weight, rstd, dresidual=None):
+    """Backward of add_rms_norm_fwd from its s and rstd: (ds, dweight), ds in dy's type
+    (the gradient of x and of the residual), dweight fp32.  `dresidual` is the gradient
+    that reaches s past the norm."""
+    dtype = _dtype("dy", dy)
+    if dy.dim() < 1 or dy.shape[-1] == 0:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected [..., D]")
+    dev, D = dy.device, dy.shape[-1]
+    rows = dy.numel() // D
+    _check("dy", dy)
+    _check("s", s, dy.dtype, tuple(dy.shape), dev)
+    _check("weight", weight, dy.dtype, (D,), dev)
+    _check("rstd", rstd, torch.float32, (rows,), dev)
+    _check("dresidual", dresidual, dy.dtype, tuple(dy.shape), dev)
+    ds = torch.empty_like(dy)
+    dw = torch.empty(D, dtype=torch.float32, device=dev)
+    a = _abi_layer.gdn_rms_norm_bwd_args(dy.data_ptr(), s.data_ptr(), weight.data_ptr(),
+                                         rstd.data_ptr(), _ptr(dresidual), rows, D, dtype,
+                                         ds.data_ptr(), dw.data_ptr())
+    n = _abi_layer.workspace_size("gdn_rms_norm_bwd", a)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _abi_layer.call_ws("gdn_rms_norm_bwd", a, ws.data_ptr(), n, _stream(dev))
+    return ds, dw
+
+
+class _AddRmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, s, rstd = add_rms_norm_fwd(x, weight, residual, eps, save_rstd=True)
+        ctx.save_for_backward(s, weight, rstd)
+        ctx.with_residual = residual is not None
+        return (y, s) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, ds=None):
+        s, weight, rstd = ctx.saved_tensors
+        d, dw = add_rms_norm_bwd(dy.contiguous(), s, weight, rstd,
+                                 None if ds is None else ds.contiguous())
+        return d, dw.to(weight.dtype), d if ctx.with_residual else None, None
+
+
+def add_rms_norm(x, weight, residual=None, eps=1e-6):
+    """add_rms_norm_fwd, differentiable in x, weight and residual: (y, s), or y alone
+    without a residual."""
+    return _AddRmsNorm.apply(x, weight, residual, eps)

@@ -78,6 +78,104 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *args, void *workspace,
                           size_t workspace_bytes, void *stream);
 gdn_status gdn_linrec_step(const gdn_linrec_step_args *args, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled (MX) tensors.  A matrix [rows, K], K a multiple of 32, is held as
+ * elements of 8 or 4 bits and one scale for each row and 32 columns:
+ * value = element * 2^(scale byte - 127); a scale byte of 255 stands for NaN.
+ *
+ *   GDN_MXFP8   e4m3 elements, a byte each, [rows, K]
+ *   GDN_MXFP4   e2m1 elements, two to a byte (the first in the low half), [rows, K / 2]
+ *
+ * Scales are held in the order the product's tensor-core instructions read them:
+ * tiles of 128 rows x 4 blocks (512 bytes), row-tile-major, ceil(rows / 128) x
+ * ceil(K / 128) of them.  Inside a tile the byte of (row, block) is at
+ * 16 (row % 32) + 4 (row / 32) + block.  Rows and blocks past the end of the
+ * matrix hold zeros (2^-127).
+ *
+ * Quantisation takes, for each block, the least exponent that keeps the block's
+ * largest magnitude within the element type (448 or 6), at least -127, and rounds
+ * the scaled elements to nearest, ties to even: nothing saturates.  (The rounded-
+ * down exponent that is the usual choice lets the largest element of a block
+ * saturate, an error of up to 1/8 for e4m3 and 1/4 for e2m1 in the element that
+ * matters most.)  A block that holds a NaN or an infinity gets a NaN scale. */
+enum { GDN_MXFP8 = 0, GDN_MXFP4 = 1 };
+
+/* Bytes of the scales of a [rows, K] matrix (0 for rows or K of none). */
+size_t gdn_mx_scale_bytes(int32_t rows, int32_t K);
+
+typedef struct gdn_mx_quantize_args {
+    const void *x;              /* [rows, K], dtype                                  */
+    int32_t rows, K;
+    int32_t dtype;              /* GDN_FP32 or GDN_BF16                              */
+    int32_t format;             /* GDN_MXFP8 or GDN_MXFP4                            */
+    void *data;                 /* elements                                          */
+    uint8_t *scales;            /* gdn_mx_scale_bytes(rows, K)                       */
+} gdn_mx_quantize_args;
+gdn_status gdn_mx_quantize(const gdn_mx_quantize_args *args, void *stream);
+
+/* The values of an MX matrix: x [rows, K], dtype (the same struct, read the other way). */
+typedef struct gdn_mx_dequantize_args {
+    const void *data;
+    const uint8_t *scales;
+    int32_t rows, K;
+    int32_t dtype, format;
+    void *x;
+} gdn_mx_dequantize_args;
+gdn_status gdn_mx_dequantize(const gdn_mx_dequantize_args *args, void *stream);
+
+/* C [M, N] = A B^T of MX matrices A [M, K] and B [N, K] of one format, summed in
+ * fp32.  A block with a NaN scale makes its row's (column's) results NaN. */
+typedef struct gdn_mx_matmul_args {
+    const void *a;
+    const uint8_t *a_scales;
+    const void *b;
+    const uint8_t *b_scales;
+    int32_t M, N, K;            /* K a multiple of 32; 0 gives zeros                 */
+    int32_t format;
+    int32_t out_dtype;          /* GDN_FP32 or GDN_BF16                              */
+    void *c;                    /* [M, N]                                            */
+} gdn_mx_matmul_args;
+gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition and RMS norm, per row of D columns:
+ *
+ *     s = x + residual;  rstd = (mean(s^2) + eps)^-1/2;  y = s rstd weight
+ *
+ * in fp32 from the unrounded sum.  y has the input's type, or is an MXFP8 matrix
+ * for gdn_mx_matmul. */
+typedef struct gdn_rms_norm_fwd_args {
+    const void *x;              /* [rows, D], dtype                                  */
+    const void *residual;       /* [rows, D], dtype, NULL = none                     */
+    const void *weight;         /* [D], dtype                                        */
+    int32_t rows, D;            /* 1 <= D <= 16384; a multiple of 32 for MXFP8       */
+    int32_t dtype;
+    float eps;
+    int32_t mx;                 /* 0: y in dtype; 1: y is MXFP8                      */
+    void *y;                    /* [rows, D], dtype or e4m3                          */
+    uint8_t *scales;            /* mx: gdn_mx_scale_bytes(rows, D)                   */
+    void *sum;                  /* [rows, D], dtype: s; required with residual, else unused */
+    float *rstd;                /* [rows], NULL = not written                        */
+} gdn_rms_norm_fwd_args;
+gdn_status gdn_rms_norm_fwd(const gdn_rms_norm_fwd_args *args, void *stream);
+
+/* Backward, xh = s rstd:  ds = rstd (w dy - xh mean(w dy xh)) + d_sum;  dw = sum over rows of dy xh.
+ * ds is the gradient of x and of the residual. */
+typedef struct gdn_rms_norm_bwd_args {
+    const void *dy;             /* [rows, D], dtype                                  */
+    const void *sum;            /* [rows, D], dtype: s (x itself without a residual) */
+    const void *weight;         /* [D], dtype                                        */
+    const float *rstd;          /* [rows]                                            */
+    const void *d_sum;          /* [rows, D], dtype: gradient that reaches s past the norm; NULL = none */
+    int32_t rows, D;
+    int32_t dtype;
+    void *ds;                   /* [rows, D], dtype                                  */
+    float *dweight;             /* [D]                                               */
+} gdn_rms_norm_bwd_args;
+size_t gdn_rms_norm_bwd_workspace_size(const gdn_rms_norm_bwd_args *args);
+gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *args, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

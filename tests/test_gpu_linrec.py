@@ -9,7 +9,7 @@ again for the pairs' composition; with bf16 gate logits the hardware logarithm
 and exponential add at most 3e-7 (5 u) to softplus, hence 8 u |gate_scale| to
 the log decay: c = 16.  The error of a state then follows E_t = a_t E_{t-1} +
 c u m_t with m_t = a_t m_{t-1} + |x_t|, computed beside the reference.  Outputs
-stored in bf16 add 2^-8 of their own magnitude (half a step, twice over)."""
+stored in bf16, of 8 significant bits, add 2^-8 of their own magnitude."""
 import numpy as np
 import pytest
 import torch
