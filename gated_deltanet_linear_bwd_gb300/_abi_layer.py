@@ -39,6 +39,11 @@ class gdn_mx_matmul_args(ctypes.Structure):
                 ("N", _i32), ("K", _i32), ("format", _i32), ("out_dtype", _i32), ("c", _vp)]
 
 
+class gdn_mx_linear_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("w", _vp), ("w_scales", _vp), ("M", _i32), ("N", _i32), ("K", _i32),
+                ("dtype", _i32), ("format", _i32), ("out_dtype", _i32), ("c", _vp)]
+
+
 class gdn_rms_norm_fwd_args(ctypes.Structure):
     _fields_ = [("x", _vp), ("residual", _vp), ("weight", _vp), ("rows", _i32), ("D", _i32),
                 ("dtype", _i32), ("eps", _f32), ("mx", _i32), ("y", _vp), ("scales", _vp),
@@ -55,48 +60,48 @@ GDN_MXFP8, GDN_MXFP4 = 0, 1
 _PLAIN = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_step": gdn_linrec_step_args,
           "gdn_mx_quantize": gdn_mx_quantize_args, "gdn_mx_dequantize": gdn_mx_dequantize_args,
           "gdn_mx_matmul": gdn_mx_matmul_args, "gdn_rms_norm_fwd": gdn_rms_norm_fwd_args}
-_WITH_WORKSPACE = {"gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args}
+_WITH_WORKSPACE = {"gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_mx_linear": gdn_mx_linear_args,
+                   "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args}
 STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
 EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \
     tuple(n + "_workspace_size" for n in _WITH_WORKSPACE) + ("gdn_mx_scale_bytes",)
 
-_declared = False
+_functions = {}
 
 
 def load():
     """libgdn.so with the signatures of gdn_layer.h declared."""
-    global _declared
     lib = _abi.load()
-    if not _declared:
+    if not _functions:
         p = ctypes.POINTER
         for name, args in _PLAIN.items():
-            getattr(lib, name).restype = _i32
-            getattr(lib, name).argtypes = [p(args), _vp]
+            f = getattr(lib, name)
+            f.restype, f.argtypes = _i32, [p(args), _vp]
         for name, args in _WITH_WORKSPACE.items():
-            getattr(lib, name).restype = _i32
-            getattr(lib, name).argtypes = [p(args), _vp, ctypes.c_size_t, _vp]
-            getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
-            getattr(lib, name + "_workspace_size").argtypes = [p(args)]
+            f = getattr(lib, name)
+            f.restype, f.argtypes = _i32, [p(args), _vp, ctypes.c_size_t, _vp]
+            f = getattr(lib, name + "_workspace_size")
+            f.restype, f.argtypes = ctypes.c_size_t, [p(args)]
         lib.gdn_mx_scale_bytes.restype = ctypes.c_size_t
         lib.gdn_mx_scale_bytes.argtypes = [_i32, _i32]
-        _declared = True
+        _functions.update((name, getattr(lib, name)) for name in EXPORTS)
     return lib
 
 
 def call(name: str, args, stream: int) -> None:
-    rc = getattr(load(), name)(ctypes.byref(args), stream)
+    rc = _functions[name](ctypes.byref(args), stream)
     if rc != GDN_OK:
         raise GdnError(name, rc)
 
 
 def call_ws(name: str, args, workspace: int, ws_bytes: int, stream: int) -> None:
-    rc = getattr(load(), name)(ctypes.byref(args), workspace, ws_bytes, stream)
+    rc = _functions[name](ctypes.byref(args), workspace, ws_bytes, stream)
     if rc != GDN_OK:
         raise GdnError(name, rc)
 
 
 def workspace_size(name: str, args) -> int:
-    n = int(getattr(load(), name + "_workspace_size")(ctypes.byref(args)))
+    n = int(_functions[name + "_workspace_size"](ctypes.byref(args)))
     if n == 0:
         raise GdnError(name + "_workspace_size", GDN_ERR_INVALID_ARG)
     return n

@@ -255,3 +255,31 @@ extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) {
     }
     return mx::run(a, dev, (cudaStream_t)stream);
 }
+
+// Bytes of X's elements in the workspace, its scales following.
+static size_t linear_data_bytes(const gdn_mx_linear_args *a) {
+    const size_t n = (size_t)a->M * a->K;
+    return ((a->format == GDN_MXFP4 ? n / 2 : n) + 255) / 256 * 256;
+}
+
+extern "C" size_t gdn_mx_linear_workspace_size(const gdn_mx_linear_args *a) {
+    if (!a || a->M < 0 || a->K < 0) {
+        fail(GDN_ERR_INVALID_ARG, "null args or bad sizes");
+        return 0;
+    }
+    return std::max<size_t>(256, linear_data_bytes(a) + gdn_mx_scale_bytes(a->M, a->K));
+}
+
+extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    const size_t need = gdn_mx_linear_workspace_size(a);
+    if (need == 0) return GDN_ERR_INVALID_ARG;
+    if (!ws || misaligned(ws) || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    uint8_t *data = (uint8_t *)ws, *scales = data + linear_data_bytes(a);
+    const gdn_mx_quantize_args q{a->x, a->M, a->K, a->dtype, a->format, data, scales};
+    const gdn_status st = gdn_mx_quantize(&q, stream);
+    if (st != GDN_OK) return st;
+    const gdn_mx_matmul_args m{data, scales, a->w, a->w_scales, a->M, a->N, a->K, a->format, a->out_dtype, a->c};
+    return gdn_mx_matmul(&m, stream);
+}

@@ -9,40 +9,52 @@ import torch
 from . import _abi_layer
 from .api import _DT, _check, _ptr
 
-
-def _stream(dev):
-    """The current stream of `dev`, which has to be the current device: the
-    library launches there."""
-    if torch.cuda.current_device() != dev.index:
-        raise ValueError(f"the tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream(dev).cuda_stream
+# The stream and device of a call, without the Stream and device objects that
+# torch.cuda.current_stream() makes (2 us of a decode step's 10)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _dtype(name, t):
+def _need(name, t, dtype, shape, index):
+    """_check for a tensor that has to be there: contiguous, on device `index`."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _check(name, t, dtype, shape, torch.device("cuda", index) if index >= 0 else None)
+        raise ValueError(f"{name} is not a tensor the library takes")
+
+
+def _first(name, t):
+    """(dtype, device index) of the tensor the others are checked against; its device
+    has to be the current one, where the library launches."""
     if t.dtype not in _DT:
         raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    return _DT[t.dtype]
+    index = t.get_device()
+    if index < 0 or not t.is_contiguous():
+        _check(name, t)
+    if index != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+    return t.dtype, index
 
 
 # ------------------------------------------------------------------ gated linear recurrence
-def _recurrence(args, src, g, initial_state, cu_seqlens, gate_scale):
+def _recurrence(name, src, g, initial_state, cu_seqlens, gate_scale):
+    """Checks what the forward and backward share: (dtype, device index, B, T, D, N)."""
     if src.dim() != 3:
         raise ValueError(f"expected [B, T, D] tensors, got shape {tuple(src.shape)}")
-    args.dtype = _dtype("the input", src)
-    B, T, D = src.shape
-    dev = src.device
-    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
-        raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [N + 1]")
-    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _check("g", g, src.dtype, (B, T, D), dev)
-    _check("initial_state", initial_state, torch.float32, (N, D), dev)
-    _check("cu_seqlens", cu_seqlens, torch.int32, None, dev)
-    _check("gate_scale", gate_scale, torch.float32, (D,), dev)
-    args.g, args.gate_scale = g.data_ptr(), _ptr(gate_scale)
-    args.initial_state, args.cu_seqlens = _ptr(initial_state), _ptr(cu_seqlens)
-    args.B, args.T, args.D, args.N = B, T, D, N
-    return B, T, D, N, dev
+    dtype, index = _first(name, src)
+    B, T, D = shape = src.shape
+    N = B
+    _need("g", g, dtype, shape, index)
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [N + 1]")
+        N = cu_seqlens.numel() - 1
+        _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), index)
+    if initial_state is not None:
+        _need("initial_state", initial_state, torch.float32, (N, D), index)
+    if gate_scale is not None:
+        _need("gate_scale", gate_scale, torch.float32, (D,), index)
+    return dtype, index, B, T, D, N
 
 
 def gated_linear_recurrence_fwd(x, g, initial_state=None, cu_seqlens=None, gate_scale=None,
@@ -51,13 +63,12 @@ def gated_linear_recurrence_fwd(x, g, initial_state=None, cu_seqlens=None, gate_
     fp32): l = g, or -gate_scale softplus(g) with `gate_scale` ([D] fp32).
     States are [N, D] fp32; with `cu_seqlens` ([N + 1] int32) B is 1 and the
     tokens are N packed sequences.  Returns (h, final_state or None)."""
-    a = _abi_layer.gdn_linrec_fwd_args()
-    _check("x", x)
-    B, T, D, N, dev = _recurrence(a, x, g, initial_state, cu_seqlens, gate_scale)
+    dtype, index, B, T, D, N = _recurrence("x", x, g, initial_state, cu_seqlens, gate_scale)
     h = torch.empty_like(x)
-    ht = torch.empty(N, D, dtype=torch.float32, device=dev) if output_final_state else None
-    a.x, a.h, a.final_state = x.data_ptr(), h.data_ptr(), _ptr(ht)
-    _abi_layer.call("gdn_linrec_fwd", a, _stream(dev))
+    ht = torch.empty((N, D), dtype=torch.float32, device=x.device) if output_final_state else None
+    _abi_layer.call("gdn_linrec_fwd", _abi_layer.gdn_linrec_fwd_args(
+        x.data_ptr(), g.data_ptr(), _ptr(gate_scale), _ptr(initial_state), _ptr(cu_seqlens), B, T, D,
+        N, _DT[dtype], h.data_ptr(), _ptr(ht)), _raw_stream(index))
     return h, ht
 
 
@@ -66,24 +77,24 @@ def gated_linear_recurrence_bwd(dh, g, h, dht=None, initial_state=None, cu_seqle
     """Backward of gated_linear_recurrence_fwd from its output h: returns
     (dx, dg, d(initial_state) or None), and d(gate_scale) as a fourth when
     `gate_scale` is given (dg is then the gradient of the logits)."""
-    a = _abi_layer.gdn_linrec_bwd_args()
-    _check("dh", dh)
-    B, T, D, N, dev = _recurrence(a, dh, g, initial_state, cu_seqlens, gate_scale)
-    _check("h", h, dh.dtype, (B, T, D), dev)
-    _check("dht", dht, torch.float32, (N, D), dev)
+    dtype, index, B, T, D, N = _recurrence("dh", dh, g, initial_state, cu_seqlens, gate_scale)
+    _need("h", h, dtype, dh.shape, index)
+    if dht is not None:
+        _need("dht", dht, torch.float32, (N, D), index)
+    dev = dh.device
     dx, dg = torch.empty_like(dh), torch.empty_like(dh)
-    dh0 = torch.empty(N, D, dtype=torch.float32, device=dev) if want_dh0 else None
-    a.d_h, a.h, a.d_final_state = dh.data_ptr(), h.data_ptr(), _ptr(dht)
-    a.dx, a.dg, a.d_initial_state = dx.data_ptr(), dg.data_ptr(), _ptr(dh0)
-    stream = _stream(dev)
-    if gate_scale is None:
-        _abi_layer.call_ws("gdn_linrec_bwd", a, 0, 0, stream)
+    dh0 = torch.empty((N, D), dtype=torch.float32, device=dev) if want_dh0 else None
+    ds = None if gate_scale is None else torch.empty(D, dtype=torch.float32, device=dev)
+    a = _abi_layer.gdn_linrec_bwd_args(
+        dh.data_ptr(), g.data_ptr(), h.data_ptr(), _ptr(gate_scale), _ptr(initial_state),
+        _ptr(cu_seqlens), _ptr(dht), B, T, D, N, _DT[dtype], dx.data_ptr(), dg.data_ptr(), _ptr(dh0),
+        _ptr(ds))
+    if ds is None:
+        _abi_layer.call_ws("gdn_linrec_bwd", a, 0, 0, _raw_stream(index))
         return dx, dg, dh0
-    ds = torch.empty(D, dtype=torch.float32, device=dev)
-    a.d_gate_scale = ds.data_ptr()
     n = _abi_layer.workspace_size("gdn_linrec_bwd", a)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _abi_layer.call_ws("gdn_linrec_bwd", a, ws.data_ptr(), n, stream)
+    _abi_layer.call_ws("gdn_linrec_bwd", a, ws.data_ptr(), n, _raw_stream(index))
     return dx, dg, dh0, ds
 
 
@@ -113,22 +124,22 @@ def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None, gate_scal
 def gated_linear_recurrence_step(x, g, state, gate_scale=None, out_state=None):
     """One token for each of N sequences: x, g [N, D], state [N, D] fp32.
     Returns h [N, D]; the new state goes to `out_state`, or over `state`."""
-    a = _abi_layer.gdn_linrec_step_args()
     if x.dim() != 2:
         raise ValueError(f"expected [N, D] tensors, got shape {tuple(x.shape)}")
-    a.dtype = _dtype("x", x)
-    N, D = x.shape
-    dev = x.device
-    _check("x", x)
-    _check("g", g, x.dtype, (N, D), dev)
-    _check("state", state, torch.float32, (N, D), dev)
-    _check("gate_scale", gate_scale, torch.float32, (D,), dev)
-    _check("out_state", out_state, torch.float32, (N, D), dev)
+    dtype, index = _first("x", x)
+    N, D = shape = x.shape
+    _need("g", g, dtype, shape, index)
+    _need("state", state, torch.float32, shape, index)
+    if gate_scale is not None:
+        _need("gate_scale", gate_scale, torch.float32, (D,), index)
+    if out_state is None:
+        out_state = state
+    else:
+        _need("out_state", out_state, torch.float32, shape, index)
     h = torch.empty_like(x)
-    a.x, a.g, a.gate_scale, a.state = x.data_ptr(), g.data_ptr(), _ptr(gate_scale), state.data_ptr()
-    a.N, a.D = N, D
-    a.h, a.out_state = h.data_ptr(), state.data_ptr() if out_state is None else out_state.data_ptr()
-    _abi_layer.call("gdn_linrec_step", a, _stream(dev))
+    _abi_layer.call("gdn_linrec_step", _abi_layer.gdn_linrec_step_args(
+        x.data_ptr(), g.data_ptr(), _ptr(gate_scale), state.data_ptr(), N, D, _DT[dtype],
+        h.data_ptr(), out_state.data_ptr()), _raw_stream(index))
     return h
 
 
@@ -157,8 +168,8 @@ class MxTensor:
             raise ValueError(f"unknown format {fmt!r} (mxfp8 or mxfp4)")
         if K % 32:
             raise ValueError(f"K = {K}: microscaled matrices take multiples of 32 columns")
-        data = (torch.empty(rows, K, dtype=torch.float8_e4m3fn, device=device) if fmt == "mxfp8"
-                else torch.empty(rows, K // 2, dtype=torch.uint8, device=device))
+        data = (torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device) if fmt == "mxfp8"
+                else torch.empty((rows, K // 2), dtype=torch.uint8, device=device))
         return cls(data, torch.empty(_scale_shape(rows, K), dtype=torch.uint8, device=device), fmt,
                    (rows, K))
 
@@ -167,43 +178,48 @@ class MxTensor:
         return self.data.device
 
 
-def _check_mx(name, t, device=None):
+def _mx_index(name, t, index=None):
+    """Checks an MxTensor; its device index (the current device's, or `index`)."""
     if not isinstance(t, MxTensor):
         raise ValueError(f"{name} must be an MxTensor")
     rows, K = t.shape
+    if index is None:
+        index = t.data.get_device()
+        if index >= 0 and index != _current_device():
+            raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
     if t.fmt == "mxfp8":
-        _check(name + ".data", t.data, torch.float8_e4m3fn, (rows, K), device)
+        _need(name + ".data", t.data, torch.float8_e4m3fn, (rows, K), index)
     else:
-        _check(name + ".data", t.data, torch.uint8, (rows, K // 2), device)
-    _check(name + ".scales", t.scales, torch.uint8, _scale_shape(rows, K), t.data.device)
+        _need(name + ".data", t.data, torch.uint8, (rows, K // 2), index)
+    _need(name + ".scales", t.scales, torch.uint8, _scale_shape(rows, K), index)
+    return index
 
 
 def mx_quantize(x, fmt="mxfp4"):
     """x [..., K] (bf16 or fp32) as an MxTensor of [rows, K]: for each row and 32
     columns the least power-of-two scale with which nothing saturates, elements
     rounded to nearest even."""
-    dtype = _dtype("x", x)
     if x.dim() < 1:
         raise ValueError("expected [..., K]")
-    _check("x", x)
+    dtype, index = _first("x", x)
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
     t = MxTensor.empty(rows, K, fmt, x.device)
-    a = _abi_layer.gdn_mx_quantize_args(x.data_ptr(), rows, K, dtype, _FORMATS[fmt],
-                                        t.data.data_ptr(), t.scales.data_ptr())
-    _abi_layer.call("gdn_mx_quantize", a, _stream(x.device))
+    _abi_layer.call("gdn_mx_quantize", _abi_layer.gdn_mx_quantize_args(
+        x.data_ptr(), rows, K, _DT[dtype], _FORMATS[fmt], t.data.data_ptr(), t.scales.data_ptr()),
+        _raw_stream(index))
     return t
 
 
 def mx_dequantize(t, dtype=torch.float32):
     """The values of an MxTensor, [rows, K] in bf16 or fp32."""
-    _check_mx("t", t)
+    index = _mx_index("t", t)
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}")
     x = torch.empty(t.shape, dtype=dtype, device=t.device)
-    a = _abi_layer.gdn_mx_dequantize_args(t.data.data_ptr(), t.scales.data_ptr(), *t.shape,
-                                          _DT[dtype], _FORMATS[t.fmt], x.data_ptr())
-    _abi_layer.call("gdn_mx_dequantize", a, _stream(t.device))
+    _abi_layer.call("gdn_mx_dequantize", _abi_layer.gdn_mx_dequantize_args(
+        t.data.data_ptr(), t.scales.data_ptr(), *t.shape, _DT[dtype], _FORMATS[t.fmt], x.data_ptr()),
+        _raw_stream(index))
     return x
 
 
@@ -224,18 +240,17 @@ def mx_from_parts(data, exponents, fmt):
 
 def mx_matmul(a, b, out_dtype=torch.bfloat16):
     """a b^T of MxTensors a [M, K] and b [N, K] of one format: [M, N], summed in fp32."""
-    _check_mx("a", a)
-    _check_mx("b", b, a.device)
+    index = _mx_index("a", a)
+    _mx_index("b", b, index)
     if a.fmt != b.fmt or a.shape[1] != b.shape[1]:
         raise ValueError(f"a is {a.fmt} {a.shape}, b is {b.fmt} {b.shape}: one format and one K")
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
     (M, K), N = a.shape, b.shape[0]
-    c = torch.empty(M, N, dtype=out_dtype, device=a.device)
-    args = _abi_layer.gdn_mx_matmul_args(a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
-                                         b.scales.data_ptr(), M, N, K, _FORMATS[a.fmt],
-                                         _DT[out_dtype], c.data_ptr())
-    _abi_layer.call("gdn_mx_matmul", args, _stream(a.device))
+    c = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _abi_layer.call("gdn_mx_matmul", _abi_layer.gdn_mx_matmul_args(
+        a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(), b.scales.data_ptr(), M, N, K,
+        _FORMATS[a.fmt], _DT[out_dtype], c.data_ptr()), _raw_stream(index))
     return c
 
 
@@ -245,11 +260,24 @@ def mx_linear(x, weight, out_dtype=None):
     (bf16 for an MxTensor), or in `out_dtype`."""
     if isinstance(x, MxTensor):
         return mx_matmul(x, weight, out_dtype or torch.bfloat16)
-    _check_mx("weight", weight, x.device)
-    if x.shape[-1] != weight.shape[1]:
+    dtype, index = _first("x", x)
+    _mx_index("weight", weight, index)
+    N, K = weight.shape
+    if x.dim() < 1 or x.shape[-1] != K:
         raise ValueError(f"x has shape {tuple(x.shape)}, the weight {weight.shape}")
-    y = mx_matmul(mx_quantize(x, weight.fmt), weight, out_dtype or x.dtype)
-    return y.view(*x.shape[:-1], weight.shape[0])
+    out_dtype = out_dtype or dtype
+    if out_dtype not in _DT:
+        raise ValueError(f"unsupported dtype {out_dtype}")
+    shape, dev = (*x.shape[:-1], N), x.device
+    c = torch.empty(shape, dtype=out_dtype, device=dev)
+    M = c.numel() // N if N else 0
+    a = _abi_layer.gdn_mx_linear_args(x.data_ptr(), weight.data.data_ptr(), weight.scales.data_ptr(),
+                                      M, N, K, _DT[dtype], _FORMATS[weight.fmt], _DT[out_dtype],
+                                      c.data_ptr())
+    n = _abi_layer.workspace_size("gdn_mx_linear", a)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _abi_layer.call_ws("gdn_mx_linear", a, ws.data_ptr(), n, _raw_stream(index))
+    return c
 
 
 # ------------------------------------------------------------------ residual addition + RMS norm
@@ -258,25 +286,30 @@ def add_rms_norm_fwd(x, weight, residual=None, eps=1e-6, out=None, save_rstd=Fal
     x [..., D] (bf16 or fp32).  Returns (y, s, rstd): y in x's type, or with
     out="mxfp8" an MxTensor of [rows, D]; s in x's type (x itself without a
     residual); rstd [rows] fp32 with save_rstd, else None."""
-    dtype = _dtype("x", x)
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., D]")
-    if out not in (None, "mxfp8"):
+    shape = x.shape
+    if x.dim() < 1 or shape[-1] == 0:
+        raise ValueError(f"x has shape {tuple(shape)}, expected [..., D]")
+    if out is not None and out != "mxfp8":
         raise ValueError(f"unknown output {out!r} (None or mxfp8)")
-    dev, D = x.device, x.shape[-1]
+    dtype, index = _first("x", x)
+    D = shape[-1]
     rows = x.numel() // D
-    _check("x", x)
-    _check("weight", weight, x.dtype, (D,), dev)
-    _check("residual", residual, x.dtype, tuple(x.shape), dev)
-    y = torch.empty_like(x) if out is None else MxTensor.empty(rows, D, out, dev)
-    s = x if residual is None else torch.empty_like(x)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if save_rstd else None
-    a = _abi_layer.gdn_rms_norm_fwd_args(
-        x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, D, dtype, eps, int(out is not None),
-        y.data_ptr() if out is None else y.data.data_ptr(),
-        None if out is None else y.scales.data_ptr(),
-        None if residual is None else s.data_ptr(), _ptr(rstd))
-    _abi_layer.call("gdn_rms_norm_fwd", a, _stream(dev))
+    _need("weight", weight, dtype, (D,), index)
+    s, sum_ptr = x, None
+    if residual is not None:
+        _need("residual", residual, dtype, shape, index)
+        s = torch.empty_like(x)
+        sum_ptr = s.data_ptr()
+    if out is None:
+        y = torch.empty_like(x)
+        y_ptr, scales = y.data_ptr(), None
+    else:
+        y = MxTensor.empty(rows, D, out, x.device)
+        y_ptr, scales = y.data.data_ptr(), y.scales.data_ptr()
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if save_rstd else None
+    _abi_layer.call("gdn_rms_norm_fwd", _abi_layer.gdn_rms_norm_fwd_args(
+        x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, D, _DT[dtype], eps, out is not None,
+        y_ptr, scales, sum_ptr, _ptr(rstd)), _raw_stream(index))
     return y, s, rstd
 
 
@@ -284,24 +317,26 @@ def add_rms_norm_bwd(dy, s, weight, rstd, dresidual=None):
     """Backward of add_rms_norm_fwd from its s and rstd: (ds, dweight), ds in dy's type
     (the gradient of x and of the residual), dweight fp32.  `dresidual` is the gradient
     that reaches s past the norm."""
-    dtype = _dtype("dy", dy)
-    if dy.dim() < 1 or dy.shape[-1] == 0:
-        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected [..., D]")
-    dev, D = dy.device, dy.shape[-1]
+    shape = dy.shape
+    if dy.dim() < 1 or shape[-1] == 0:
+        raise ValueError(f"dy has shape {tuple(shape)}, expected [..., D]")
+    dtype, index = _first("dy", dy)
+    D = shape[-1]
     rows = dy.numel() // D
-    _check("dy", dy)
-    _check("s", s, dy.dtype, tuple(dy.shape), dev)
-    _check("weight", weight, dy.dtype, (D,), dev)
-    _check("rstd", rstd, torch.float32, (rows,), dev)
-    _check("dresidual", dresidual, dy.dtype, tuple(dy.shape), dev)
+    _need("s", s, dtype, shape, index)
+    _need("weight", weight, dtype, (D,), index)
+    _need("rstd", rstd, torch.float32, (rows,), index)
+    if dresidual is not None:
+        _need("dresidual", dresidual, dtype, shape, index)
+    dev = dy.device
     ds = torch.empty_like(dy)
     dw = torch.empty(D, dtype=torch.float32, device=dev)
     a = _abi_layer.gdn_rms_norm_bwd_args(dy.data_ptr(), s.data_ptr(), weight.data_ptr(),
-                                         rstd.data_ptr(), _ptr(dresidual), rows, D, dtype,
+                                         rstd.data_ptr(), _ptr(dresidual), rows, D, _DT[dtype],
                                          ds.data_ptr(), dw.data_ptr())
     n = _abi_layer.workspace_size("gdn_rms_norm_bwd", a)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _abi_layer.call_ws("gdn_rms_norm_bwd", a, ws.data_ptr(), n, _stream(dev))
+    _abi_layer.call_ws("gdn_rms_norm_bwd", a, ws.data_ptr(), n, _raw_stream(index))
     return ds, dw
 
 

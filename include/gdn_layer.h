@@ -137,6 +137,22 @@ typedef struct gdn_mx_matmul_args {
 } gdn_mx_matmul_args;
 gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *args, void *stream);
 
+/* C [M, N] = X W^T with X [M, K] quantised to W's format on the way: gdn_mx_quantize
+ * into the workspace, then gdn_mx_matmul, in one call. */
+typedef struct gdn_mx_linear_args {
+    const void *x;              /* [M, K], dtype                                     */
+    const void *w;              /* [N, K] MX matrix                                  */
+    const uint8_t *w_scales;
+    int32_t M, N, K;
+    int32_t dtype;              /* of x: GDN_FP32 or GDN_BF16                        */
+    int32_t format;
+    int32_t out_dtype;
+    void *c;                    /* [M, N]                                            */
+} gdn_mx_linear_args;
+size_t gdn_mx_linear_workspace_size(const gdn_mx_linear_args *args);
+gdn_status gdn_mx_linear(const gdn_mx_linear_args *args, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
 /* ------------------------------------------------------------------------
  * Residual addition and RMS norm, per row of D columns:
  *

@@ -54,6 +54,7 @@ OK = dict(
     gdn_mx_quantize=dict(x=4096, data=4096, scales=4096, rows=3, K=64),
     gdn_mx_dequantize=dict(x=4096, data=4096, scales=4096, rows=3, K=64),
     gdn_mx_matmul=dict(a=4096, a_scales=4096, b=4096, b_scales=4096, c=4096, M=3, N=5, K=64),
+    gdn_mx_linear=dict(x=4096, w=4096, w_scales=4096, c=4096, M=3, N=5, K=64),
     gdn_rms_norm_fwd=dict(x=4096, weight=4096, y=4096, rows=3, D=64),
     gdn_rms_norm_bwd=dict(dy=4096, sum=4096, weight=4096, rstd=4096, ds=4096, dweight=4096, rows=3, D=64),
 )
@@ -92,6 +93,9 @@ def call(abi, name, **kw):
     ("gdn_mx_matmul", dict(b_scales=None), 1, "required"),
     ("gdn_mx_matmul", dict(c=4098), 1, "aligned"),
     ("gdn_mx_matmul", dict(M=-4), 1, "bad sizes"),
+    ("gdn_mx_linear", dict(M=-1), 1, "bad sizes"),
+    ("gdn_mx_linear", dict(K=40), 2, "multiple of 32"),
+    ("gdn_mx_linear", dict(x=None), 1, "required"),
     ("gdn_rms_norm_fwd", dict(D=20000), 2, "16384"),
     ("gdn_rms_norm_fwd", dict(mx=1, scales=4096, D=40), 2, "multiples of 32"),
     ("gdn_rms_norm_fwd", dict(mx=1), 1, "required"),
