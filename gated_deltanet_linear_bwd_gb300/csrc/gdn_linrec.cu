@@ -2,95 +2,137 @@
 // its backward pass and its one-token step.
 //
 // A token's map h -> a h + x composes as (A, B) then (A', B') = (A A', A' B + B'),
-// so a run of tokens is one pair per channel.  A CTA takes 32 or 64 channels (one
-// 128-byte row per warp load) of one sequence and walks it in tiles of kWarps x R
-// tokens.  Each warp reduces its R tokens to a pair, the pairs meet in shared
-// memory, and every warp, knowing the value before its first token, forms its R
-// results from the tile it still holds in registers: one pass over memory.
+// so a run of tokens is one pair per channel.  A CTA takes 64 channels of one sequence
+// and walks it in tiles of W x R tokens that TMA keeps coming.  Each warp reduces its R
+// tokens to a pair, the pairs meet in shared memory, and every warp, knowing the value
+// before its first token, forms its R results from the decays it still holds in
+// registers: one pass over memory.
+//
+// Where channels and sequences are too few for the GPU, a cluster of S CTAs shares
+// a sequence: its CTAs take neighbouring tiles, each sends its tile's pair into
+// every other's shared memory, and each folds the pairs of the tiles before its own.
+// No CTA ever waits on global memory, and the order of every sum is fixed.
+//
+// Bound by memory: 16 x (512 .. 8192) tokens x 4096 gated bf16 forward 269 us, 94% of
+// the measured copy rate; 4 x 4096 x 4096 backward 114 us, 87% (the gate's arithmetic
+// takes the issue slots); 65536 x 2048 in clusters of 8 163 us, 73% (the rounds' length:
+// each waits for the slowest of 8 CTAs).
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_layer_internal.h"
+#include "tc_mx_ptx.cuh"
 
 namespace gdn {
 namespace linrec {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;          // tokens a warp holds in registers
-constexpr int kTile = kWarps * kRows;
+constexpr int kChannels = 64;      // of a CTA: two to a lane
+constexpr int kMaxCluster = 8;
 
-// The channels a lane carries: VC elements of T as one load.
-template <typename T, int VC>
-struct Lane;
-template <>
-struct Lane<__nv_bfloat16, 2> {
-    using Raw = uint32_t;
-    static __device__ __forceinline__ void get(Raw r, float (&v)[2]) {
-        v[0] = __uint_as_float(r << 16);
-        v[1] = __uint_as_float(r & 0xffff0000u);
-    }
-    static __device__ __forceinline__ Raw put(const float (&v)[2]) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
-        return *reinterpret_cast<const uint32_t *>(&b);
-    }
-};
-template <>
-struct Lane<__nv_bfloat16, 1> {
-    using Raw = unsigned short;
-    static __device__ __forceinline__ void get(Raw r, float (&v)[1]) {
-        v[0] = __uint_as_float((uint32_t)r << 16);
-    }
-    static __device__ __forceinline__ Raw put(const float (&v)[1]) {
-        return __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-    }
-};
-template <>
-struct Lane<float, 1> {
-    using Raw = float;
-    static __device__ __forceinline__ void get(Raw r, float (&v)[1]) { v[0] = r; }
-    static __device__ __forceinline__ Raw put(const float (&v)[1]) { return v[0]; }
-};
-
-// Functions of an element, in full single precision for fp32 tensors.  For bf16
-// ones softplus and its derivative come from the hardware approximations, whose
-// errors (about 1e-7, in the log decay) lie far below the 2^-9 of the input's own
-// rounding; with the accurate functions the gated pass would be bound by
-// arithmetic instead of memory.  The decay itself is always the accurate expf: a
-// slow channel multiplies a thousand decays near 1 together, so that a relative
-// error of 2e-7 that always points the same way (the approximation's) would grow
-// to 2e-4 in the fp32 states.
-template <typename T>
-struct Fn {
-    static __device__ __forceinline__ float gate_exp(float x) { return expf(x); }
-    static __device__ __forceinline__ float softplus(float x, float e) {
-        return fmaxf(x, 0.f) + log1pf(e);
-    }
-    static __device__ __forceinline__ float rcp(float x) { return 1.f / x; }
-};
-template <>
-struct Fn<__nv_bfloat16> {
-    static __device__ __forceinline__ float gate_exp(float x) { return __expf(x); }
-    static __device__ __forceinline__ float softplus(float x, float e) {
-        return fmaxf(x, 0.f) + __logf(1.f + e);
-    }
-    static __device__ __forceinline__ float rcp(float x) { return __fdividef(1.f, x); }
-};
-
-// a = exp(g), or exp(-s softplus(g)); fmaxf drops a NaN, so a NaN gate is put back.
-template <typename T, bool GATED>
-__device__ __forceinline__ float decay(float g, float s) {
-    if (!GATED) return expf(g);
-    const float a = expf(-s * Fn<T>::softplus(g, Fn<T>::gate_exp(-fabsf(g))));
-    return g != g ? g : a;
+// The two channels a lane carries, as two elements of T side by side.
+__device__ __forceinline__ float2 get2(uint32_t r) {
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
 }
+__device__ __forceinline__ float2 get2(float2 r) { return r; }
+__device__ __forceinline__ uint32_t put2(float2 v, const __nv_bfloat16 *) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ float2 put2(float2 v, const float *) { return v; }
+template <typename T>
+struct Raw2;
+template <>
+struct Raw2<__nv_bfloat16> {
+    using type = uint32_t;
+};
+template <>
+struct Raw2<float> {
+    using type = float2;
+};
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float bounded(float x) { return fminf(x, 3e38f); }
+
+// A token's gate: the decay a = exp(l) with l = g, or -s softplus(g); and for the
+// backward pass softplus(g) in units of kUnit and its derivative, the logistic function.
+//
+// fp32 tensors take the accurate functions.  For bf16 ones the two exponentials and
+// the logarithm are the hardware's (about 1e-7 in the log decay, far below the 2^-9
+// of the input's own rounding): with the accurate ones the pass is bound by
+// arithmetic (106 instructions for a token of two channels, 46% of the memory rate;
+// 40 in this form).  But a slow channel multiplies a thousand decays near 1 together,
+// and the hardware exponential's errors there lean one way (2e-8 on average, 2e-5 in
+// the fp32 state of such a channel).  So 2^y is its Taylor polynomial to the fifth
+// power for |y| < 1/8, off by (y ln 2)^6 / 720 < 6e-10 and otherwise by roundings
+// that point either way.
+template <typename T, bool GATED>
+struct Gate {
+    static constexpr float kUnit = 1.f;      // of softplus
+    static __device__ __forceinline__ float decay(float g, float s, float &sp) {
+        sp = 0.f;
+        if (GATED) sp = fmaxf(g, 0.f) + log1pf(expf(-fabsf(g)));
+        return expf(GATED ? -s * sp : g);
+    }
+    static __device__ __forceinline__ float2 decay(float2 g, float2 s, float2 &sp) {
+        return make_float2(decay(g.x, s.x, sp.x), decay(g.y, s.y, sp.y));
+    }
+    static __device__ __forceinline__ float slope(float g) {
+        const float e = expf(-fabsf(g));
+        return (g >= 0.f ? 1.f : e) / (1.f + e);
+    }
+    static __device__ __forceinline__ float2 slope(float2 g, float2) {
+        return make_float2(slope(g.x), slope(g.y));
+    }
+};
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+template <bool GATED>
+struct Gate<__nv_bfloat16, GATED> {
+    static constexpr float kUnit = kLn2;
+    static __device__ __forceinline__ float2 decay(float2 g, float2 s, float2 &sp) {
+        float2 y = mul2(g, both(kLog2e));
+        if (GATED) {
+            const float2 u = add2(make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y))), both(1.f));
+            sp = add2(make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)), make_float2(lg2(u.x), lg2(u.y)));
+            y = mul2(sp, make_float2(-s.x, -s.y));
+        }
+        float2 p = fma2(y, both(1.3333558146e-3f), both(9.6181291076e-3f));
+        p = fma2(p, y, both(5.5504108665e-2f));
+        p = fma2(p, y, both(2.4022650696e-1f));
+        p = fma2(p, y, both(kLn2));
+        p = fma2(p, y, both(1.f));
+        return make_float2(fabsf(y.x) < 0.125f ? p.x : ex2(y.x), fabsf(y.y) < 0.125f ? p.y : ex2(y.y));
+    }
+    // the logistic function is e^g / (1 + e^g) = 2^(g log2 e - softplus(g)); an infinite g
+    // as the largest number, whose softplus it is too
+    static __device__ __forceinline__ float2 slope(float2 g, float2 sp) {
+        const float2 y = mul2(g, both(kLog2e));
+        return make_float2(ex2(bounded(y.x) - bounded(sp.x)), ex2(bounded(y.y) - bounded(sp.y)));
+    }
+};
 
 struct Shape {
     const int32_t *cu;
     long long T;               // tokens per row, or of the packed batch
     int N, D, groups;          // sequences, channels, channel groups
     int lanes_n;               // clusters that share a channel group's sequences
+    int cluster;               // CTAs of a cluster
     int *status;
+    long long spin_limit;
 };
 
 // Token range of sequence n; an impossible cu_seqlens is recorded and reads as empty.
@@ -108,6 +150,136 @@ __device__ __forceinline__ void range(const Shape &s, int n, long long &bos, lon
     len = bad ? 0 : hi - lo;
 }
 
+// Pairs (A and B of two channels) of a tile's warps, and of a round's tiles in the
+// cluster.  Two of each: a tile's are written while the one before it may still be read.
+template <int W>
+struct Pairs {
+    float4 warp[2][W][32];
+    float4 tile[2][kMaxCluster][32];
+    uint64_t got[2];           // one phase a round: the pairs of every CTA have come
+};
+
+// 16 bytes into another CTA's shared memory, counted by that CTA's barrier.
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, float4 v) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(addr),
+        "r"(bar), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+        : "memory");
+}
+
+// The pair of a warp's tokens joins the others' in two halves, so that other work fits
+// between them.  offer() leaves it where the tile's, or the cluster's, warps find it;
+// take() turns the value before the round's first tile (carry) into the value before
+// this warp's first token, and carry into the value after the round.
+//
+// The pairs of a cluster travel by st.async, each counted by the receiver's barrier,
+// and no CTA waits for more than them.  (The cluster's own barrier, whose release
+// also waits for the results stored to global memory before it, made a round of
+// 65536 x 2048 tokens by 8 CTAs 3.5 us long instead of 2.5.)  A CTA can be two rounds
+// ahead of none: its pair of the next round is what lets the others go on.
+template <int W>
+struct Join {
+    Pairs<W> &p;
+    int warp, lane, rank, size;
+    const Shape &s;
+    float2 A, B;               // of the tile's warps before this one (clusters only)
+    bool alive;                // no wait for pairs gave up
+
+    // Past its barrier every warp of the CTA is done with the tile before.
+    __device__ __forceinline__ void offer(int round, float2 a, float2 b) {
+        const int buf = round & 1;
+        p.warp[buf][warp][lane] = make_float4(a.x, a.y, b.x, b.y);
+        __syncthreads();
+        if (size == 1) return;
+        if (!alive) return;
+        if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&p.got[buf], (uint32_t)size * 512u);
+        float2 allA = both(1.f), allB = both(0.f);
+        A = allA, B = allB;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w == warp) A = allA, B = allB;
+            const float4 q = p.warp[buf][w][lane];
+            allA = mul2(allA, make_float2(q.x, q.y));
+            allB = fma2(make_float2(q.x, q.y), allB, make_float2(q.z, q.w));
+        }
+        for (int to = warp; to < size; to += W)      // the warps share the receivers out
+            send(tc::map_rank(tc::smem_u32(&p.tile[buf][rank][lane]), to),
+                 tc::map_rank(tc::smem_u32(&p.got[buf]), to), make_float4(allA.x, allA.y, allB.x, allB.y));
+    }
+    __device__ __forceinline__ float2 take(int round, float2 &carry) {
+        const int buf = round & 1;
+        float2 before = carry;
+        if (size == 1) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w == warp) before = carry;
+                const float4 q = p.warp[buf][w][lane];
+                carry = fma2(make_float2(q.x, q.y), carry, make_float2(q.z, q.w));
+            }
+            return before;
+        }
+        // a limit of its own: the pairs come whether or not a wait for tiles gave up.  If
+        // they do not, nothing more is counted or sent, and the others stop a round later.
+        if (alive) alive = tc::mbar_wait(&p.got[buf], (round >> 1) & 1, 1ll << 22, s.status);
+        for (int k = 0; k < size; ++k) {
+            if (k == rank) before = carry;
+            const float4 q = p.tile[buf][k][lane];
+            carry = fma2(make_float2(q.x, q.y), carry, make_float2(q.z, q.w));
+        }
+        return fma2(A, before, B);
+    }
+};
+
+// Where a lane's channels are, and which of the two exist.
+struct Place {
+    int warp, lane, rank, size, cluster, ch;
+    bool in0, in1;
+};
+__device__ __forceinline__ Place place(const Shape &s) {
+    Place p;
+    p.warp = threadIdx.x >> 5, p.lane = threadIdx.x & 31;
+    p.rank = (int)tc::cluster_rank(), p.size = (int)tc::cluster_size();
+    p.cluster = blockIdx.x / p.size;
+    p.ch = p.cluster % s.groups * kChannels + 2 * p.lane;
+    p.in0 = p.ch < s.D, p.in1 = p.ch + 1 < s.D;
+    return p;
+}
+__device__ __forceinline__ float2 load_state(const float *base, long long at, const Place &p) {
+    return make_float2(base && p.in0 ? base[at] : 0.f, base && p.in1 ? base[at + 1] : 0.f);
+}
+__device__ __forceinline__ void store_state(float *base, long long at, const Place &p, float2 v) {
+    if (p.in0) base[at] = v.x;
+    if (p.in1) base[at + 1] = v.y;
+}
+
+// Two elements at p, which may be on no 4- or 8-byte boundary (PAIRS false) and of
+// which the second may not exist.
+template <typename T, bool PAIRS>
+__device__ __forceinline__ float2 load2(const T *p, const Place &at) {
+    if (PAIRS) return get2(*reinterpret_cast<const typename Raw2<T>::type *>(p));
+    return make_float2(to_f(p[0]), at.in1 ? to_f(p[1]) : 0.f);
+}
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void store2(T *p, const Place &at, float2 v) {
+    if (PAIRS) {
+        *reinterpret_cast<typename Raw2<T>::type *>(p) = put2(v, (const T *)nullptr);
+    } else {
+        from_f(p, v.x);
+        if (at.in1) from_f(p + 1, v.y);
+    }
+}
+
+// A ring of stages, each a tile of every input: rows of kChannels elements.  TMA
+// fills stage i % S with tile i; the barrier in Join::offer() is what frees a stage, so one
+// thread keeps the ring S - 1 tiles ahead without further waiting.
+template <typename T, int W, int R, int INPUTS, int STAGES>
+struct Ring {
+    static constexpr int kTile = W * R;
+    T tile[STAGES][INPUTS][kTile][kChannels];
+    Pairs<W> pairs;
+    uint64_t full[STAGES];
+};
+
 struct FwdArgs {
     const void *x, *g;
     const float *scale, *h0;
@@ -115,209 +287,266 @@ struct FwdArgs {
     float *ht;
 };
 
-template <typename T, int VC, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) fwd_kernel(FwdArgs a, Shape s) {
-    using L = Lane<T, VC>;
-    using Raw = typename L::Raw;
-    __shared__ float2 pairs[2][kWarps][32 * VC];
+// Forward over TMA tiles (TMA true), or with plain loads for widths whose rows do not
+// start on 16 bytes.
+template <typename T, bool GATED, int W, int R, int STAGES, bool TMA>
+__global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUtensorMap map_x,
+                                                       const __grid_constant__ CUtensorMap map_g,
+                                                       const FwdArgs a, const Shape s) {
+    using Ring = linrec::Ring<T, W, R, 2, STAGES>;
+    constexpr int kTile = Ring::kTile;
+    constexpr uint32_t kBytes = 2u * kTile * kChannels * sizeof(T);
+    extern __shared__ __align__(128) uint8_t raw[];
+    Ring &ring = *reinterpret_cast<Ring *>(raw);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) tc::mbar_init(&ring.full[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&ring.pairs.got[i], 1);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
     pdl_enter();
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = blockIdx.x % s.groups, first_n = blockIdx.x / s.groups;
-    const int ch = group * 32 * VC + lane * VC;
-    const bool live = ch < s.D;
-    float sc[VC];
-#pragma unroll
-    for (int j = 0; j < VC; ++j) sc[j] = GATED && live ? a.scale[ch + j] : 0.f;
+    const Place at = place(s);
+    const int ch0 = at.ch - 2 * at.lane;
+    const float2 sc = GATED ? load_state(a.scale, at.ch, at) : both(0.f);
+    if (at.size > 1) tc::cluster_sync();     // the others' barriers are ready
 
-    int buf = 0;
-    for (int n = first_n; n < s.N; n += s.lanes_n) {
+    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true};
+    bool ok = true;                // no wait gave up
+    int tiles = 0, issued = 0;     // tiles walked and asked for, over all sequences
+    for (int n = at.cluster / s.groups; n < s.N; n += s.lanes_n) {
         long long bos, len;
         range(s, n, bos, len);
-        const Raw *x = reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(a.x) + bos * s.D + ch);
-        const Raw *g = reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(a.g) + bos * s.D + ch);
-        Raw *h = reinterpret_cast<Raw *>(reinterpret_cast<T *>(a.h) + bos * s.D + ch);
-        const long long pitch = s.D / VC;
-        float carry[VC];
+        const long long step = (long long)at.size * kTile;
+        float2 carry = load_state(a.h0, (long long)n * s.D + at.ch, at);
+        const int base = tiles;
+        const int rounds = (int)((len + step - 1) / step);
+        auto ask = [&](int round) {          // thread 0: tile `round` of this sequence
+            const int st = (base + round) % STAGES;
+            const int row = (int)(bos + round * step + at.rank * kTile);
+            tc::mbar_arrive_expect_tx(&ring.full[st], kBytes);
+            tc::tma_load_2d(&ring.tile[st][0], &map_x, &ring.full[st], ch0, row);
+            tc::tma_load_2d(&ring.tile[st][1], &map_g, &ring.full[st], ch0, row);
+            ++issued;
+        };
+        if (TMA && threadIdx.x == 0)
+            for (int i = 0; i < STAGES - 1 && i < rounds && ok; ++i) ask(i);
+        auto token = [&](int i) { return i * step + at.rank * kTile + at.warp * R; };
+        auto rows_of = [&](int i) {          // tokens this lane has of tile i
+            return ok && at.in0 ? (int)max(0ll, min((long long)R, len - token(i))) : 0;
+        };
+        auto cell = [&](int i, int input, int r) {
+            return get2(*reinterpret_cast<const typename Raw2<T>::type *>(
+                &ring.tile[(base + i) % STAGES][input][at.warp * R + r][2 * at.lane]));
+        };
+        // tile i: its decays and its pair
+        auto scan = [&](int i, float2 (&al)[R], float2 (&xv)[TMA ? 1 : R], float2 &A, float2 &B) {
+            if (TMA && ok)
+                ok = tc::mbar_wait(&ring.full[(base + i) % STAGES], ((base + i) / STAGES) & 1, s.spin_limit, s.status);
+            const int rows = rows_of(i);
+            auto go = [&](auto whole) {
+                if constexpr (!TMA) {
+                    const long long row0 = (bos + token(i)) * s.D + at.ch;
 #pragma unroll
-        for (int j = 0; j < VC; ++j)
-            carry[j] = a.h0 && live ? a.h0[(long long)n * s.D + ch + j] : 0.f;
-
-        for (long long t0 = 0; t0 < len; t0 += kTile, buf ^= 1) {
-            const long long tw = t0 + warp * kRows;
-            const int rows = live ? (int)max(0ll, min((long long)kRows, len - tw)) : 0;
-            Raw xr[kRows], gr[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                xr[r] = r < rows ? x[(tw + r) * pitch] : Raw(0);
-                gr[r] = r < rows ? g[(tw + r) * pitch] : Raw(0);
-            }
-            float al[kRows][VC], A[VC], Bv[VC];
-#pragma unroll
-            for (int j = 0; j < VC; ++j) A[j] = 1.f, Bv[j] = 0.f;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float xv[VC], gv[VC];
-                L::get(xr[r], xv);
-                L::get(gr[r], gv);
-#pragma unroll
-                for (int j = 0; j < VC; ++j) {
-                    al[r][j] = r < rows ? decay<T, GATED>(gv[j], sc[j]) : 1.f;
-                    A[j] *= al[r][j];
-                    Bv[j] = al[r][j] * Bv[j] + xv[j];
+                    for (int r = 0; r < R; ++r) {
+                        const bool in = whole.value || r < rows;
+                        xv[r] = in ? load2<T, false>(reinterpret_cast<const T *>(a.x) + row0 + (long long)r * s.D, at) : both(0.f);
+                        al[r] = in ? load2<T, false>(reinterpret_cast<const T *>(a.g) + row0 + (long long)r * s.D, at) : both(0.f);
+                    }
                 }
-            }
+                A = both(1.f), B = both(0.f);
 #pragma unroll
-            for (int j = 0; j < VC; ++j) pairs[buf][warp][lane * VC + j] = make_float2(A[j], Bv[j]);
-            __syncthreads();      // two buffers: one barrier per tile is enough
-            float hv[VC];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                for (int j = 0; j < VC; ++j) {
-                    if (w == warp) hv[j] = carry[j];
-                    const float2 p = pairs[buf][w][lane * VC + j];
-                    carry[j] = p.x * carry[j] + p.y;
+                for (int r = 0; r < R; ++r) {
+                    const float2 g = TMA ? cell(i, 1, r) : al[r];
+                    float2 x = TMA ? cell(i, 0, r) : xv[TMA ? 0 : r];
+                    float2 sp;
+                    al[r] = Gate<T, GATED>::decay(g, sc, sp);
+                    if (!whole.value && r >= rows) al[r] = both(1.f), x = both(0.f);
+                    A = mul2(A, al[r]);
+                    B = fma2(al[r], B, x);
                 }
+            };
+            if (rows == R) go(std::true_type());
+            else go(std::false_type());
+        };
+        // tile i's results from the value before this warp's first token
+        auto emit = [&](int i, const float2 (&al)[R], const float2 (&xv)[TMA ? 1 : R], float2 h) {
+            const int rows = rows_of(i);
+            auto go = [&](auto whole) {
+                T *out = reinterpret_cast<T *>(a.h) + (bos + token(i)) * s.D + at.ch;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float xv[VC];
-                L::get(xr[r], xv);
-#pragma unroll
-                for (int j = 0; j < VC; ++j) hv[j] = al[r][j] * hv[j] + xv[j];
-                if (r < rows) h[(tw + r) * pitch] = L::put(hv);
-            }
+                for (int r = 0; r < R; ++r) {
+                    h = fma2(al[r], h, TMA ? cell(i, 0, r) : xv[TMA ? 0 : r]);
+                    if (whole.value || r < rows) store2<T, TMA>(out, at, h);
+                    out += s.D;
+                }
+            };
+            if (rows == R) go(std::true_type());
+            else if (rows > 0) go(std::false_type());
+        };
+        auto refill = [&](int i) {           // after offer(i): the stage of tile i - 1 is free
+            if (TMA && threadIdx.x == 0 && ok && i + STAGES - 1 < rounds) ask(i + STAGES - 1);
+        };
+        for (int i = 0; i < rounds; ++i) {
+            float2 al[R], xv[TMA ? 1 : R], A, B;
+            scan(i, al, xv, A, B);
+            join.offer(base + i, A, B);
+            refill(i);
+            emit(i, al, xv, join.take(base + i, carry));
         }
-        if (a.ht && warp == 0 && live)
-#pragma unroll
-            for (int j = 0; j < VC; ++j) a.ht[(long long)n * s.D + ch + j] = carry[j];
+        tiles += rounds;
+        // the next sequence's first tiles go into stages that this one's last are read from
+        __syncthreads();
+        if (a.ht && at.rank == 0 && at.warp == 0) store_state(a.ht, (long long)n * s.D + at.ch, at, carry);
     }
+    if (at.size > 1) tc::cluster_sync();     // nor does a CTA go before the others are done
+    if (TMA && threadIdx.x == 0 && !ok)      // nothing may land after the CTA has gone
+        for (int i = max(0, issued - STAGES); i < issued; ++i)
+            tc::mbar_drain(&ring.full[i % STAGES], (i / STAGES) & 1);
 }
 
 struct BwdArgs {
     const void *dh, *g, *h;
     const float *scale, *h0, *dht;
     void *dx, *dg;
-    float *dh0, *partial;      // partial: [lanes_n][D], or null
+    float *dh0, *partial;      // partial: [lanes_n * cluster][D], or null
 };
 
 // The same walk from the last token to the first: with e_t = dh_t + c_t, a token's
-// map on the carried gradient is c -> a (dh + c), the pair (a, a dh).
-template <typename T, int VC, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) bwd_kernel(BwdArgs a, Shape s) {
-    using L = Lane<T, VC>;
-    using Raw = typename L::Raw;
-    __shared__ float2 pairs[2][kWarps][32 * VC];
+// map on the carried gradient is c -> a (dh + c), the pair (a, a dh).  Row u of the
+// walk is token len - 1 - u, so a tile's rows lie in shared memory from its last to
+// its first; the tile of h is one token earlier than the others.
+template <typename T, bool GATED, int W, int R, int STAGES, bool TMA>
+__global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUtensorMap map_dh,
+                                                       const __grid_constant__ CUtensorMap map_g,
+                                                       const __grid_constant__ CUtensorMap map_h,
+                                                       const BwdArgs a, const Shape s) {
+    using Ring = linrec::Ring<T, W, R, 3, STAGES>;
+    constexpr int kTile = Ring::kTile;
+    constexpr uint32_t kBytes = 3u * kTile * kChannels * sizeof(T);
+    extern __shared__ __align__(128) uint8_t raw[];
+    Ring &ring = *reinterpret_cast<Ring *>(raw);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) tc::mbar_init(&ring.full[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&ring.pairs.got[i], 1);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
     pdl_enter();
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = blockIdx.x % s.groups, first_n = blockIdx.x / s.groups;
-    const int ch = group * 32 * VC + lane * VC;
-    const bool live = ch < s.D;
-    float sc[VC], dscale[VC];
-#pragma unroll
-    for (int j = 0; j < VC; ++j) {
-        sc[j] = GATED && live ? a.scale[ch + j] : 0.f;
-        dscale[j] = 0.f;
-    }
+    const Place at = place(s);
+    const int ch0 = at.ch - 2 * at.lane;
+    const float2 sc = GATED ? load_state(a.scale, at.ch, at) : both(0.f);
+    const float2 minus = make_float2(-sc.x, -sc.y);
+    float2 dscale = both(0.f);
+    if (at.size > 1) tc::cluster_sync();     // the others' barriers are ready
 
-    int buf = 0;
-    for (int n = first_n; n < s.N; n += s.lanes_n) {
+    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true};
+    bool ok = true;
+    int tiles = 0, issued = 0;
+    for (int n = at.cluster / s.groups; n < s.N; n += s.lanes_n) {
         long long bos, len;
         range(s, n, bos, len);
-        const long long base = bos * s.D + ch, pitch = s.D / VC;
-        const Raw *dh = reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(a.dh) + base);
-        const Raw *g = reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(a.g) + base);
-        const Raw *h = reinterpret_cast<const Raw *>(reinterpret_cast<const T *>(a.h) + base);
-        Raw *dx = reinterpret_cast<Raw *>(reinterpret_cast<T *>(a.dx) + base);
-        Raw *dg = reinterpret_cast<Raw *>(reinterpret_cast<T *>(a.dg) + base);
-        float carry[VC], h0[VC];
-#pragma unroll
-        for (int j = 0; j < VC; ++j) {
-            carry[j] = a.dht && live ? a.dht[(long long)n * s.D + ch + j] : 0.f;
-            h0[j] = a.h0 && live ? a.h0[(long long)n * s.D + ch + j] : 0.f;
-        }
-
-        for (long long u0 = 0; u0 < len; u0 += kTile, buf ^= 1) {
-            // token of row r: tw - r
-            const long long tw = len - 1 - (u0 + warp * kRows);
-            const int rows = live ? (int)max(0ll, min((long long)kRows, tw + 1)) : 0;
-            Raw dr[kRows], gr[kRows], hr[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                dr[r] = r < rows ? dh[(tw - r) * pitch] : Raw(0);
-                gr[r] = r < rows ? g[(tw - r) * pitch] : Raw(0);
-                hr[r] = r < rows && r < tw ? h[(tw - r - 1) * pitch] : Raw(0);
+        const long long step = (long long)at.size * kTile, state = (long long)n * s.D + at.ch;
+        float2 carry = load_state(a.dht, state, at);
+        const float2 h0 = load_state(a.h0, state, at);
+        const int base = tiles;
+        const int rounds = (int)((len + step - 1) / step);
+        auto ask = [&](int round) {
+            const int st = (base + round) % STAGES;
+            const int row = (int)(bos + len - kTile - (round * step + at.rank * kTile));
+            tc::mbar_arrive_expect_tx(&ring.full[st], kBytes);
+            tc::tma_load_2d(&ring.tile[st][0], &map_dh, &ring.full[st], ch0, row);
+            tc::tma_load_2d(&ring.tile[st][1], &map_g, &ring.full[st], ch0, row);
+            tc::tma_load_2d(&ring.tile[st][2], &map_h, &ring.full[st], ch0, row - 1);
+            ++issued;
+        };
+        if (TMA && threadIdx.x == 0)
+            for (int i = 0; i < STAGES - 1 && i < rounds && ok; ++i) ask(i);
+        for (int i = 0; i < rounds; ++i, ++tiles) {
+            const int st = tiles % STAGES;
+            const long long u = i * step + at.rank * kTile + at.warp * R, top = len - 1 - u;
+            int rows = at.in0 ? (int)max(0ll, min((long long)R, len - u)) : 0;
+            if (TMA) {
+                if (ok) ok = tc::mbar_wait(&ring.full[st], (tiles / STAGES) & 1, s.spin_limit, s.status);
+                if (!ok) rows = 0;
             }
-            float al[kRows][VC], A[VC], Bv[VC];
+            // row r of the walk: r rows back from the tile's row kTile - 1 - warp * R
+            auto cell = [&](int input, int r) {
+                return get2(*reinterpret_cast<const typename Raw2<T>::type *>(
+                    &ring.tile[st][input][kTile - 1 - at.warp * R - r][2 * at.lane]));
+            };
+            const long long row0 = (bos + top) * s.D + at.ch;
+            const T *gd = reinterpret_cast<const T *>(a.dh) + row0, *gg = reinterpret_cast<const T *>(a.g) + row0;
+            const T *gh = reinterpret_cast<const T *>(a.h) + row0;
+            float2 al[R], sp[GATED ? R : 1], dv[TMA ? 1 : R], gv[TMA ? 1 : R], hv[TMA ? 1 : R];
+            float2 A = both(1.f), B = both(0.f);
+            auto first = [&](auto whole) {
+                if constexpr (!TMA) {
 #pragma unroll
-            for (int j = 0; j < VC; ++j) A[j] = 1.f, Bv[j] = 0.f;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float dv[VC], gv[VC];
-                L::get(dr[r], dv);
-                L::get(gr[r], gv);
-#pragma unroll
-                for (int j = 0; j < VC; ++j) {
-                    al[r][j] = r < rows ? decay<T, GATED>(gv[j], sc[j]) : 1.f;
-                    A[j] *= al[r][j];
-                    Bv[j] = al[r][j] * (Bv[j] + dv[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < VC; ++j) pairs[buf][warp][lane * VC + j] = make_float2(A[j], Bv[j]);
-            __syncthreads();
-            float c[VC];
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                for (int j = 0; j < VC; ++j) {
-                    if (w == warp) c[j] = carry[j];
-                    const float2 p = pairs[buf][w][lane * VC + j];
-                    carry[j] = p.x * carry[j] + p.y;
-                }
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float dv[VC], gv[VC], hv[VC], e[VC], dl[VC];
-                L::get(dr[r], dv);
-                L::get(gr[r], gv);
-                L::get(hr[r], hv);
-#pragma unroll
-                for (int j = 0; j < VC; ++j) {
-                    if (r == tw) hv[j] = h0[j];        // the token before the first is h0
-                    e[j] = dv[j] + c[j];
-                    c[j] = al[r][j] * e[j];
-                    dl[j] = c[j] * hv[j];
-                    if (GATED && r < rows) {
-                        // d softplus = logistic(g) = 1 / (1 + e^-|g|), or e^-|g| times that
-                        const float q = Fn<T>::gate_exp(-fabsf(gv[j]));
-                        dscale[j] -= dl[j] * Fn<T>::softplus(gv[j], q);
-                        dl[j] *= -sc[j] * (gv[j] >= 0.f ? 1.f : q) * Fn<T>::rcp(1.f + q);
+                    for (int r = 0; r < R; ++r) {
+                        const bool in = whole.value || r < rows;
+                        const long long off = (long long)r * s.D;
+                        dv[r] = in ? load2<T, false>(gd - off, at) : both(0.f);
+                        gv[r] = in ? load2<T, false>(gg - off, at) : both(0.f);
+                        hv[r] = in && r < top ? load2<T, false>(gh - off - s.D, at) : both(0.f);
                     }
                 }
-                if (r < rows) {
-                    dx[(tw - r) * pitch] = L::put(e);
-                    dg[(tw - r) * pitch] = L::put(dl);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float2 d = TMA ? cell(0, r) : dv[TMA ? 0 : r];
+                    al[r] = Gate<T, GATED>::decay(TMA ? cell(1, r) : gv[TMA ? 0 : r], sc, sp[GATED ? r : 0]);
+                    if (!whole.value && r >= rows) al[r] = both(1.f), d = both(0.f);
+                    A = mul2(A, al[r]);
+                    B = mul2(al[r], add2(B, d));
                 }
-            }
+            };
+            if (rows == R) first(std::true_type());
+            else first(std::false_type());
+            join.offer(tiles, A, B);
+            if (TMA && threadIdx.x == 0 && ok && i + STAGES - 1 < rounds) ask(i + STAGES - 1);
+            float2 c = join.take(tiles, carry);
+            auto second = [&](auto whole) {
+                T *dx = reinterpret_cast<T *>(a.dx) + row0, *dg = reinterpret_cast<T *>(a.dg) + row0;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float2 hp = TMA ? cell(2, r) : hv[TMA ? 0 : r];
+                    if (!whole.value && r == top) hp = h0;     // before the first token is h0
+                    const float2 e = add2(TMA ? cell(0, r) : dv[TMA ? 0 : r], c);
+                    c = mul2(al[r], e);
+                    float2 dl = mul2(c, hp);
+                    if (whole.value || r < rows) {
+                        if (GATED) {
+                            // softplus finite even for an infinite gate, whose decay of 0 is in dl
+                            const float2 q = sp[GATED ? r : 0];
+                            dscale = fma2(dl, make_float2(bounded(q.x), bounded(q.y)), dscale);
+                            dl = mul2(mul2(dl, minus), Gate<T, GATED>::slope(TMA ? cell(1, r) : gv[TMA ? 0 : r], q));
+                        }
+                        store2<T, TMA>(dx, at, e);
+                        store2<T, TMA>(dg, at, dl);
+                    }
+                    dx -= s.D, dg -= s.D;
+                }
+            };
+            if (rows == R && top >= R) second(std::true_type());
+            else if (rows > 0) second(std::false_type());
         }
-        if (a.dh0 && warp == 0 && live)
-#pragma unroll
-            for (int j = 0; j < VC; ++j) a.dh0[(long long)n * s.D + ch + j] = carry[j];
+        __syncthreads();
+        if (a.dh0 && at.rank == 0 && at.warp == 0) store_state(a.dh0, state, at, carry);
     }
-    if (GATED && a.partial) {
+    if (at.size > 1) tc::cluster_sync();
+    if (TMA && threadIdx.x == 0 && !ok)
+        for (int i = max(0, issued - STAGES); i < issued; ++i)
+            tc::mbar_drain(&ring.full[i % STAGES], (i / STAGES) & 1);
+    if (GATED && a.partial) {                // the CTA's sum, its warps in order
+        float2 *sum = reinterpret_cast<float2 *>(ring.pairs.warp);
+        sum[at.warp * 32 + at.lane] = mul2(dscale, both(-Gate<T, GATED>::kUnit));
         __syncthreads();
-        float *sum = reinterpret_cast<float *>(pairs);
-#pragma unroll
-        for (int j = 0; j < VC; ++j) sum[(warp * 32 + lane) * VC + j] = dscale[j];
-        __syncthreads();
-        if (warp == 0 && live)
-#pragma unroll
-            for (int j = 0; j < VC; ++j) {
-                float t = 0.f;
-                for (int w = 0; w < kWarps; ++w) t += sum[(w * 32 + lane) * VC + j];
-                a.partial[(long long)first_n * s.D + ch + j] = t;
-            }
+        if (at.warp == 0) {
+            float2 t = both(0.f);
+            for (int w = 0; w < W; ++w) t = add2(t, sum[w * 32 + at.lane]);
+            store_state(a.partial, ((long long)(at.cluster / s.groups) * at.size + at.rank) * s.D + at.ch, at, t);
+        }
     }
 }
 
@@ -328,22 +557,39 @@ __global__ void __launch_bounds__(256) step_kernel(const T *x, const T *g, const
                                                    long long total, int D) {
     pdl_enter();
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const float a = decay<T, GATED>(to_f(g[i]), GATED ? scale[i % D] : 0.f);
+        float sp;
+        const float a = Gate<float, GATED>::decay(to_f(g[i]), GATED ? scale[i % D] : 0.f, sp);
         const float v = a * state[i] + to_f(x[i]);
         out[i] = v;
         from_f(h + i, v);
     }
 }
 
-// Channels a lane carries: bf16 pairs where every row starts on 4 bytes.
-int lane_channels(int dtype, int D) { return dtype == GDN_BF16 && D % 2 == 0 ? 2 : 1; }
-
-// Clusters (here single CTAs) that share a channel group's sequences: one each,
-// but no more than fill the GPU several times over, so that the per-CTA partial
-// sums of d(gate_scale) stay small beside the data.
+// Clusters that share a channel group's sequences: one each, but no more than fill
+// the GPU several times over, so that the per-CTA partial sums of d(gate_scale)
+// stay small beside the data.
 int group_lanes(int N, int groups) {
     const int most = std::max(1, 4096 / groups);
     return std::min(N, std::max(most, 64));
+}
+
+// Warps, tokens to a warp and stages: about 100 KB of tiles to a CTA, two CTAs to an SM.
+// Every warp reads every warp's pair, so that few warps with many tokens each do best:
+// forward, 65536 x 2048 gated bf16, 8 warps of 16 tokens 194 us, 4 of 32 163 us, 16 of 8
+// 490 us; backward, 4 x 4096 x 4096, 8 of 8 126 us, 4 of 16 114 us, 6 of 10 130 us.
+template <typename T>
+struct Tiles {
+    static constexpr bool kHalf = sizeof(T) == 2;
+    static constexpr int kFwdWarps = 4, kFwdRows = kHalf ? 32 : 16, kFwdStages = 3;
+    static constexpr int kBwdWarps = 4, kBwdRows = kHalf ? 16 : 8, kBwdStages = 4;
+};
+
+// CTAs that share a sequence: doubled while the grid leaves slots of the GPU (two
+// CTAs per SM) empty and the sequences have a tile for each.
+int cluster_of(long long clusters, long long mean_len, int sms) {
+    int c = 1;
+    while (c < kMaxCluster && clusters * c <= sms && mean_len > (long long)c * 128) c *= 2;
+    return c;
 }
 
 gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
@@ -352,42 +598,85 @@ gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
         return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", dtype);
     if (packed && (B != 1 || N < 1))
         return fail(GDN_ERR_INVALID_ARG, "cu_seqlens needs B == 1 and N >= 1 (B=%d N=%d)", B, N);
-    if ((long long)B * T >= (1ll << 31) || (long long)(packed ? N : B) * D >= (1ll << 40))
+    if ((long long)B * T >= (1ll << 31) - (1 << 16) || (long long)(packed ? N : B) * D >= (1ll << 40))
         return fail(GDN_ERR_INVALID_ARG, "problem too large");
     return GDN_OK;
 }
 
-Shape shape_of(const int32_t *cu, int B, int T, int D, int N, int dtype, int *status) {
+Shape shape_of(const int32_t *cu, int B, int T, int D, int N, const LayerDevice &dev) {
     Shape s;
     s.cu = cu;
     s.T = T;
     s.N = cu ? N : B;
     s.D = D;
-    const int width = 32 * lane_channels(dtype, D);
-    s.groups = (D + width - 1) / width;
+    s.groups = (D + kChannels - 1) / kChannels;
     s.lanes_n = group_lanes(s.N, s.groups);
-    s.status = status;
+    s.cluster = cluster_of((long long)s.groups * s.lanes_n, cu ? T / s.N : T, dev.sms);
+    s.status = dev.status;
+    s.spin_limit = dev.spin_limit;
     return s;
 }
 
-template <typename Args, typename K>
-cudaError_t launch(const char *name, K kernel, const Args &a, const Shape &s, cudaStream_t st) {
+// Rows that start on 16 bytes, as TMA wants them.
+bool tma_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(const char *name, void (*kernel)(KArgs...), int warps, size_t smem, const Shape &s, cudaStream_t st,
+                   const Args &...args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     prof_before(name, st);
-    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)(s.groups * s.lanes_n)), dim3(kThreads),
-                                     0, st, a, s);
+    e = launch_pdl_cluster(kernel, dim3((unsigned)((long long)s.groups * s.lanes_n * s.cluster)), dim3(32 * warps),
+                           smem, s.cluster, st, args..., s);
     prof_after(st);
     return e;
 }
 
-#define GDN_LINREC_KERNEL(kernel)                                                               \
-    (dtype == GDN_FP32 ? (gated ? kernel<float, 1, true> : kernel<float, 1, false>)             \
-     : vc == 2 ? (gated ? kernel<__nv_bfloat16, 2, true> : kernel<__nv_bfloat16, 2, false>)     \
-               : (gated ? kernel<__nv_bfloat16, 1, true> : kernel<__nv_bfloat16, 1, false>))
+// [tokens, D] of T, boxes of kChannels channels x `rows` tokens (an empty tensor's map
+// is never used).
+template <typename T>
+cudaError_t map_of(CUtensorMap *m, const void *base, const Shape &s, int rows) {
+    const long long tokens = s.cu ? s.T : s.T * s.N;
+    return tokens == 0 ? cudaSuccess : tc::make_map_rows(m, base, tokens, s.D, sizeof(T), kChannels, rows);
+}
+
+template <typename T, bool GATED>
+cudaError_t run_fwd(const FwdArgs &f, const Shape &s, bool tma, cudaStream_t q) {
+    constexpr int W = Tiles<T>::kFwdWarps, R = Tiles<T>::kFwdRows, S = Tiles<T>::kFwdStages;
+    CUtensorMap mx = {}, mg = {};
+    if (!tma)
+        return launch("linrec_fwd_plain", fwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 2, 1>),
+                      s, q, mx, mg, f);
+    cudaError_t e = tc::encoder();
+    if (e == cudaSuccess) e = map_of<T>(&mx, f.x, s, W * R);
+    if (e == cudaSuccess) e = map_of<T>(&mg, f.g, s, W * R);
+    if (e != cudaSuccess) return e;
+    return launch("linrec_fwd", fwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 2, S>), s, q, mx, mg, f);
+}
+
+template <typename T, bool GATED>
+cudaError_t run_bwd(const BwdArgs &b, const Shape &s, bool tma, cudaStream_t q) {
+    constexpr int W = Tiles<T>::kBwdWarps, R = Tiles<T>::kBwdRows, S = Tiles<T>::kBwdStages;
+    CUtensorMap md = {}, mg = {}, mh = {};
+    if (!tma)
+        return launch("linrec_bwd_plain", bwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 3, 1>),
+                      s, q, md, mg, mh, b);
+    cudaError_t e = tc::encoder();
+    if (e == cudaSuccess) e = map_of<T>(&md, b.dh, s, W * R);
+    if (e == cudaSuccess) e = map_of<T>(&mg, b.g, s, W * R);
+    if (e == cudaSuccess) e = map_of<T>(&mh, b.h, s, W * R);
+    if (e != cudaSuccess) return e;
+    return launch("linrec_bwd", bwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 3, S>), s, q,
+                  md, mg, mh, b);
+}
 
 size_t bwd_workspace(const gdn_linrec_bwd_args *a) {
     if (!a->gate_scale || !a->d_gate_scale) return 256;
-    const Shape s = shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, a->dtype, nullptr);
-    return std::max<size_t>(256, (size_t)s.lanes_n * s.D * sizeof(float));
+    // asked for without a device: sized for the largest cluster
+    LayerDevice any;
+    any.sms = 1 << 20;
+    const Shape s = shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, any);
+    return std::max<size_t>(256, (size_t)s.lanes_n * s.cluster * s.D * sizeof(float));
 }
 
 }  // namespace
@@ -409,12 +698,15 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *a, void *stream) {
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, a->dtype, dev.status);
-    const int dtype = a->dtype, vc = linrec::lane_channels(dtype, a->D);
+    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, dev);
+    const bool tma = linrec::tma_rows(a->dtype, a->D), bf = a->dtype == GDN_BF16;
     const bool gated = a->gate_scale != nullptr;
     const linrec::FwdArgs f{a->x, a->g, a->gate_scale, a->initial_state, a->h, a->final_state};
-    const cudaError_t e = linrec::launch("linrec_fwd", GDN_LINREC_KERNEL(linrec::fwd_kernel), f, s,
-                                         (cudaStream_t)stream);
+    cudaStream_t q = (cudaStream_t)stream;
+    const cudaError_t e = bf ? (gated ? linrec::run_fwd<__nv_bfloat16, true>(f, s, tma, q)
+                                      : linrec::run_fwd<__nv_bfloat16, false>(f, s, tma, q))
+                             : (gated ? linrec::run_fwd<float, true>(f, s, tma, q)
+                                      : linrec::run_fwd<float, false>(f, s, tma, q));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear recurrence launch");
 }
 
@@ -444,14 +736,17 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_byte
                     linrec::bwd_workspace(a));
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, a->dtype, dev.status);
-    const int dtype = a->dtype, vc = linrec::lane_channels(dtype, a->D);
+    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, dev);
+    const bool tma = linrec::tma_rows(a->dtype, a->D), bf = a->dtype == GDN_BF16;
     const linrec::BwdArgs b{a->d_h, a->g, a->h, a->gate_scale, a->initial_state, a->d_final_state,
                             a->dx, a->dg, a->d_initial_state, sums ? (float *)ws : nullptr};
     cudaStream_t q = (cudaStream_t)stream;
-    cudaError_t e = linrec::launch("linrec_bwd", GDN_LINREC_KERNEL(linrec::bwd_kernel), b, s, q);
+    cudaError_t e = bf ? (gated ? linrec::run_bwd<__nv_bfloat16, true>(b, s, tma, q)
+                                : linrec::run_bwd<__nv_bfloat16, false>(b, s, tma, q))
+                       : (gated ? linrec::run_bwd<float, true>(b, s, tma, q)
+                                : linrec::run_bwd<float, false>(b, s, tma, q));
     if (e == cudaSuccess && sums) {
-        e = column_sum((const float *)ws, s.lanes_n, a->D, a->d_gate_scale, q);
+        e = column_sum((const float *)ws, s.lanes_n * s.cluster, a->D, a->d_gate_scale, q);
     }
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear recurrence backward launch");
 }

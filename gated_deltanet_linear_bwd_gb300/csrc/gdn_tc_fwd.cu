@@ -835,6 +835,21 @@ cudaError_t make_map_bytes(CUtensorMap *m, const void *base, long long rows, lon
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// [rows, cols] of 2- or 4-byte elements viewed as 2-D, boxes of box_cols x box_rows in
+// plain row order; past the end reading as zeros.
+cudaError_t make_map_rows(CUtensorMap *m, const void *base, long long rows, long long cols, int elem,
+                          int box_cols, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    const CUresult r = g_encode(
+        m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+        const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 bool supported(const Plan &p) {
     // TMA row coordinates are 32-bit ints: the largest, of the chunk-state tiles
     // (two 128-row halves per (chunk, head)), is 2 (chunk * H + head) * 128 + 128

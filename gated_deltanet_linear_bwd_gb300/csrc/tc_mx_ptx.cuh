@@ -91,9 +91,19 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// Every thread of every CTA of the cluster meets; writes before it are seen after it.
+// Every thread of every CTA of the cluster meets; writes before the arrival are seen
+// after the wait.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The address of `saddr` in the shared memory of the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {

@@ -288,3 +288,21 @@ def test_refusals():
     with pytest.raises(lib().GdnError, match="aligned"):
         odd = torch.empty(1 + 2 * 8 * 64, dtype=torch.bfloat16, device="cuda")[1:].view(2, 8, 64)
         f(odd, p.g)
+
+
+@pytest.mark.parametrize("T,D", [(300, 8192), (4000, 64)])       # alone, and in clusters
+def test_bounded_waits_give_up_and_the_next_call_is_right(T, D):
+    p = Problem(1, T, D, "bf16", True, seed=6)
+    run = lambda: (*lib().gated_linear_recurrence_fwd(p.x, p.g, p.h0, None, p.scale),
+                   *lib().gated_linear_recurrence_bwd(p.dh, p.g, p.x, p.dht, p.h0, None, p.scale))
+    want, stream = run(), torch.cuda.current_stream().cuda_stream
+    try:
+        lib().gdn_set_spin_limit(0)
+        lib().gated_linear_recurrence_fwd(p.x, p.g, p.h0, None, p.scale)
+        assert lib().gdn_sync_status(stream) == 5
+        lib().gated_linear_recurrence_bwd(p.dh, p.g, p.x, p.dht, p.h0, None, p.scale)
+        assert lib().gdn_sync_status(stream) == 5
+    finally:
+        lib().gdn_set_spin_limit(-1)
+    assert all(torch.equal(a, b) for a, b in zip(run(), want))
+    assert lib().gdn_sync_status(stream) == 0
