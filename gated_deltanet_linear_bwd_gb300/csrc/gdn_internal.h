@@ -133,9 +133,11 @@ cudaError_t make_map(CUtensorMap *m, const void *base, long long tokens, int H);
 // Chunk-major transposed tiles [chunk][H][128][64] bf16 (W^T, u^T, dU^T): one box per tile.
 cudaError_t make_map_tiles(CUtensorMap *m, const void *base, long long rows_total,
                            int box_rows = 128);
-// [rows, cols] of `elem`-byte elements, box_cols x box_rows boxes, no swizzle.
+// [rows, cols] of `elem`-byte elements, box_cols x box_rows boxes, no swizzle or the 128-byte one.
 cudaError_t make_map_rows(CUtensorMap *m, const void *base, long long rows, long long cols, int elem,
-                          int box_cols, int box_rows);
+                          int box_cols, int box_rows, bool swizzle = false);
+// 512-byte scale tiles [row tile][K tile], boxes of kt x rt.
+cudaError_t make_map_scales(CUtensorMap *m, const void *base, int row_tiles, int k_tiles, int kt, int rt);
 // [rows, bytes] of bytes, 128 x box_rows boxes (bytes a multiple of 16).
 cudaError_t make_map_bytes(CUtensorMap *m, const void *base, long long rows, long long bytes,
                            int box_rows);

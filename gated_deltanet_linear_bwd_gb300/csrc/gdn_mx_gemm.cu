@@ -185,10 +185,245 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     if (warp == 1) tc::tmem_dealloc(tmem, (uint32_t)a.tmem_cols);
 }
 
+// ------------------------------------------------------------------ large products
+// CTA pairs (cta_group::2) on tiles of 256 tokens x 256 features, persistent over the
+// tiles.  A pair reads each operand tile once for both of its CTAs, which halves what an
+// SM takes from L2 per MMA; the accumulators of two tiles share 448 TMEM columns, the
+// last 64 of the one being the first 64 of the other, so that the epilogue of a tile
+// runs under the next one's MMAs once it has taken those 64.
+constexpr int kPairStages = 5;
+constexpr int kPairAcc = 192;                        // column of the second accumulator
+constexpr int kPairScales = 448;                     // columns of the scales: two sets of 24
+constexpr int kPairOut = 16384;                      // a staged 128 x 128-byte block of C
+
+struct PairArgs {
+    int M, N, K, kblocks, ktiles;
+    int m_tiles, n_tiles;
+    int *status;
+    long long spin_limit;
+};
+
+struct PairControl {
+    uint64_t full[kPairStages], empty[kPairStages], acc_full, acc_free, done;
+    uint32_t tmem;
+    int issued, failed;                              // failed: the epilogue's wait gave up
+};
+
+template <bool FP4>
+constexpr int pair_stage_bytes() { return 32768 + (FP4 ? 3072 : 2048); }
+
+template <bool FP4, typename TO>
+__global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_constant__ CUtensorMap map_x,
+                                                             const __grid_constant__ CUtensorMap map_w,
+                                                             const __grid_constant__ CUtensorMap map_sx,
+                                                             const __grid_constant__ CUtensorMap map_sw,
+                                                             const __grid_constant__ CUtensorMap map_c,
+                                                             const PairArgs a) {
+    constexpr int kStep = FP4 ? 64 : 32, kBlock = 4 * kStep, kScaleTiles = kBlock / 128;
+    constexpr int kStage = pair_stage_bytes<FP4>();
+    constexpr uint32_t kBytes = 32768u + 3u * 512u * kScaleTiles;    // of one CTA
+    constexpr int kCols = 128 / (int)sizeof(TO);     // columns of a staged block
+    extern __shared__ uint8_t raw[];
+    __shared__ PairControl ctl;
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *stage_out = ring + kPairStages * kStage;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            tc::mbar_init(&ctl.full[s], 1);
+            tc::mbar_init(&ctl.empty[s], 1);
+        }
+        tc::mbar_init(&ctl.acc_full, 1);
+        tc::mbar_init(&ctl.acc_free, 8);             // the epilogue warps of both CTAs
+        tc::mbar_init(&ctl.done, 1);
+        ctl.issued = ctl.failed = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) tc::tmem_alloc_pair(&ctl.tmem, 512);
+    tc::tc_fence_before();
+    tc::cluster_sync();                              // both CTAs' barriers and TMEM are there
+    tc::tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    pdl_enter();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;                               // stages asked for
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                const int row = (tile % a.m_tiles) * 2 + rank, feat = tile / a.m_tiles * 2;   // in 128s
+                for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
+                    const int s = i % kPairStages;
+                    if (i >= kPairStages &&
+                        !tc::mbar_wait(&ctl.empty[s], (i / kPairStages - 1) & 1, a.spin_limit, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = ring + s * kStage;
+                    const uint32_t bar = tc::map_rank(tc::smem_u32(&ctl.full[s]), 0);
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&ctl.full[s], 2u * kBytes);
+                    tc::tma_load_2d_pair(st, &map_x, bar, kb * 128, row * 128);
+                    tc::tma_load_2d_pair(st + 16384, &map_w, bar, kb * 128, (feat + rank) * 128);
+                    tc::tma_load_3d_pair(st + 32768, &map_sx, bar, 0, kb * kScaleTiles, row);
+                    tc::tma_load_3d_pair(st + 32768 + 512 * kScaleTiles, &map_sw, bar, 0, kb * kScaleTiles, feat);
+                }
+            }
+            ctl.issued = i;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int i = 0, t = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
+                if (t > 0) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_free, (t - 1) & 1, a.spin_limit, a.status));
+                    if (!ok) break;
+                }
+                tc::tc_fence_after();
+                const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
+                for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
+                    const int s = i % kPairStages;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.full[s], (i / kPairStages) & 1, a.spin_limit, a.status));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint32_t st = tc::smem_u32(ring + s * kStage);
+                    const uint32_t tsx = tmem + kPairScales + (i & 1) * 24, tsw = tsx + 4 * kScaleTiles;
+                    const int st_tiles = min(kScaleTiles, a.ktiles - kb * kScaleTiles);
+                    for (int k = 0; k < st_tiles; ++k) {
+                        tc::copy_scales_pair(tsx + 4 * k, tc::desc_scales(st + 32768 + 512 * k));
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            tc::copy_scales_pair(tsw + 8 * k + 4 * b,
+                                                 tc::desc_scales(st + 32768 + 512 * (kScaleTiles * (1 + b) + k)));
+                    }
+                    const uint64_t dx = tc::desc_sw128(st, 0, 1024), dw = tc::desc_sw128(st + 16384, 0, 1024);
+                    const int steps = min(4, (a.K - kb * kBlock + kStep - 1) / kStep);
+                    for (int j = 0; j < steps; ++j) {
+                        const int id = FP4 ? 2 * (j & 1) : j;
+                        tc::mma_mx_pair<FP4>(acc, dx + 2 * j, dw + 2 * j, tc::idesc_mx(FP4, 256, 256, id),
+                                             tsx + (FP4 ? 4 * (j >> 1) : 0), tsw + (FP4 ? 8 * (j >> 1) : 0),
+                                             kb > 0 || j > 0);
+                    }
+                    tc::mma_commit_pair(&ctl.empty[s]);
+                }
+                if (ok) tc::mma_commit_pair(&ctl.acc_full);
+            }
+            tc::mma_commit_pair(&ctl.done);
+        }
+    } else {
+        // epilogue: 64 (bf16) or 32 (fp32) columns at a time through shared memory to a TMA store
+        const bool storer = warp == 2 && lane == 0;
+        const int quarter = warp & 3;
+        int t = 0, staged = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++t) {
+            if (!tc::mbar_wait(&ctl.acc_full, t & 1, a.spin_limit, a.status)) ctl.failed = 1;
+            tc::named_sync(1, 128);                  // the four warps go on, or stop, together
+            if (ctl.failed) break;
+            tc::tc_fence_after();
+            const int row = ((tile % a.m_tiles) * 2 + rank) * 128, feat = tile / a.m_tiles * 256;
+            const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                // the 64 columns that the next tile's accumulator shares go first
+                const int col = (t & 1 ? c : (c + 3) & 3) * 64;
+                float v[64];
+                tc::tmem_ld32x2(tc::tmem_addr(acc, quarter, col), tc::tmem_addr(acc, quarter, col + 32), v, v + 32);
+                if (c == 0) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(&ctl.acc_free), 0));
+                }
+#pragma unroll
+                for (int b = 0; b < 64 / kCols; ++b, ++staged) {
+                    uint8_t *buf = stage_out + (staged & 1) * kPairOut;
+                    if (storer) tc::bulk_wait_read_but_newest();   // the store before last has left this buffer
+                    tc::named_sync(1, 128);
+                    if constexpr (sizeof(TO) == 2) {
+                        tc::st_row64(buf, 32 * quarter + lane, v);
+                    } else {
+                        const int r = 32 * quarter + lane;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4 *>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
+                                make_float4(v[32 * b + 4 * k], v[32 * b + 4 * k + 1], v[32 * b + 4 * k + 2], v[32 * b + 4 * k + 3]);
+                    }
+                    tc::fence_proxy_async();
+                    tc::named_sync(1, 128);
+                    if (storer) {
+                        if (row < a.M && feat + col + b * kCols < a.N)
+                            tc::tma_store_2d(&map_c, buf, feat + col + b * kCols, row);
+                        tc::bulk_commit();           // a group for every block, as the waits count them
+                    }
+                }
+            }
+        }
+        if (storer) tc::bulk_wait_read();
+        __syncwarp();
+    }
+    // every MMA done and every copy landed before TMEM is given back and a CTA goes
+    tc::mbar_drain(&ctl.done, 0);
+    tc::tc_fence_before();
+    tc::cluster_sync();
+    if (threadIdx.x == 0 && rank == 0)
+        for (int i = max(0, ctl.issued - kPairStages); i < ctl.issued; ++i)
+            tc::mbar_drain(&ctl.full[i % kPairStages], (i / kPairStages) & 1);
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+template <bool FP4, typename TO>
+gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t q) {
+    PairArgs g{};
+    g.M = a->M, g.N = a->N, g.K = a->K;
+    g.kblocks = (a->K + (FP4 ? 255 : 127)) / (FP4 ? 256 : 128);
+    g.ktiles = (a->K + 127) / 128;
+    g.m_tiles = (a->M + 255) / 256;
+    g.n_tiles = (a->N + 255) / 256;
+    g.status = dev.status;
+    g.spin_limit = dev.spin_limit;
+    const long long bytes = FP4 ? a->K / 2 : a->K;
+    const int st = FP4 ? 2 : 1;
+    CUtensorMap mx, mw, msx, msw, mc;
+    cudaError_t e;
+    if ((e = tc::make_map_bytes(&mx, a->a, a->M, bytes, 128)) != cudaSuccess ||
+        (e = tc::make_map_bytes(&mw, a->b, a->N, bytes, 128)) != cudaSuccess ||
+        (e = tc::make_map_scales(&msx, a->a_scales, (a->M + 127) / 128, g.ktiles, st, 1)) != cudaSuccess ||
+        (e = tc::make_map_scales(&msw, a->b_scales, (a->N + 127) / 128, g.ktiles, st, 2)) != cudaSuccess ||
+        (e = tc::make_map_rows(&mc, a->c, a->M, a->N, sizeof(TO), 128 / (int)sizeof(TO), 128, true)) != cudaSuccess)
+        return cuda_fail(e, "tensor map of a product");
+    const size_t smem = kPairStages * pair_stage_bytes<FP4>() + 2 * kPairOut + 1024;
+    auto k = gemm_pair_kernel<FP4, TO>;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+        return cuda_fail(e, "shared memory of the product");
+    const int pairs = (int)std::min<long long>((long long)g.m_tiles * g.n_tiles, dev.sms / 2);
+    prof_before("mx_gemm_pair", q);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kThreads), smem, 2, q, mx, mw, msx, msw, mc, g);
+    prof_after(q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "mx product launch");
+}
+
+// Pairs where their 256 x 256 tiles fill most of the GPU and TMA can store C's rows
+// (which start on 16 bytes).
+bool pair_fits(const gdn_mx_matmul_args *a, int sms) {
+    const long long tiles = (long long)((a->M + 255) / 256) * ((a->N + 255) / 256);
+    return (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0 && tiles * 4 >= sms &&
+           tiles < (1ll << 30);
+}
+
 gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t q) {
     const bool fp4 = a->format == GDN_MXFP4;
     cudaError_t e = tc::encoder();
     if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled lookup");
+    if (pair_fits(a, dev.sms)) {
+        if (a->out_dtype == GDN_FP32) return fp4 ? run_pair<true, float>(a, dev, q) : run_pair<false, float>(a, dev, q);
+        return fp4 ? run_pair<true, __nv_bfloat16>(a, dev, q) : run_pair<false, __nv_bfloat16>(a, dev, q);
+    }
     GemmArgs g{};
     g.sx = a->a_scales;
     g.sw = a->b_scales;

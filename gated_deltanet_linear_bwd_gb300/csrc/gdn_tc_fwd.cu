@@ -835,10 +835,24 @@ cudaError_t make_map_bytes(CUtensorMap *m, const void *base, long long rows, lon
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Scale tiles [row tile][K tile] of 512 bytes: boxes of kt x rt tiles, past the end
+// reading as zeros.
+cudaError_t make_map_scales(CUtensorMap *m, const void *base, int row_tiles, int k_tiles, int kt, int rt) {
+    const cuuint64_t dims[3] = {128, (cuuint64_t)k_tiles, (cuuint64_t)row_tiles};
+    const cuuint64_t strides[2] = {512, (cuuint64_t)k_tiles * 512};
+    const cuuint32_t box[3] = {128, (cuuint32_t)kt, (cuuint32_t)rt};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims,
+                                strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // [rows, cols] of 2- or 4-byte elements viewed as 2-D, boxes of box_cols x box_rows in
-// plain row order; past the end reading as zeros.
+// plain row order, or in the 128-byte swizzle; past the end reading as zeros.
 cudaError_t make_map_rows(CUtensorMap *m, const void *base, long long rows, long long cols, int elem,
-                          int box_cols, int box_rows) {
+                          int box_cols, int box_rows, bool swizzle) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
@@ -846,7 +860,8 @@ cudaError_t make_map_rows(CUtensorMap *m, const void *base, long long rows, long
     const CUresult r = g_encode(
         m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
         const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

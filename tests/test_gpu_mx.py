@@ -79,7 +79,9 @@ def reference_product(a, b):
 
 SIZES = [(1, 1, 32), (1, 128, 32), (3, 5, 64), (7, 129, 96), (16, 300, 160), (17, 64, 4096), (31, 1000, 992),
          (64, 513, 544), (65, 256, 512), (128, 128, 256), (129, 130, 288), (200, 77, 1056), (1000, 520, 320),
-         (257, 640, 2080), (512, 1024, 1024), (4, 4096, 4096), (300, 515, 8192)]
+         (257, 640, 2080), (512, 1024, 1024), (4, 4096, 4096), (300, 515, 8192),
+         # enough tiles for CTA pairs: whole, ragged rows, columns and K, several tiles to a pair
+         (2048, 2048, 512), (2500, 2568, 544), (1900, 5000, 96), (4097, 3336, 32), (2300, 2056, 1056)]
 
 
 @pytest.mark.parametrize("fmt", FMT)
@@ -112,9 +114,9 @@ def test_product_of_units_places_every_element(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
-@pytest.mark.parametrize("M", [5, 150, 600])
-def test_nan_blocks_reach_their_row_only(fmt, M):
-    x, w = draw(M, 256, 1), draw(200, 256, 2)
+@pytest.mark.parametrize("M,N", [(5, 200), (150, 200), (600, 200), (2100, 2400)])
+def test_nan_blocks_reach_their_row_only(fmt, M, N):
+    x, w = draw(M, 256, 1), draw(N, 256, 2)
     clean = lib().mx_matmul(lib().mx_quantize(x, fmt), lib().mx_quantize(w, fmt))
     x[3, 40] = float("inf")
     w[7, 3] = float("nan")
@@ -147,8 +149,8 @@ def test_checkpoint_parts_and_leading_axes(fmt):
 
 @pytest.mark.parametrize("fmt", FMT)
 def test_repeats_bit_for_bit_and_on_another_stream(fmt):
-    for M in (4, 300):
-        x, w = draw(M, 4096, 1), lib().mx_quantize(draw(640, 4096, 2), fmt)
+    for M, N in ((4, 640), (300, 640), (3000, 2048)):
+        x, w = draw(M, 4096, 1), lib().mx_quantize(draw(N, 4096, 2), fmt)
         first = lib().mx_linear(x, w)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -159,7 +161,7 @@ def test_repeats_bit_for_bit_and_on_another_stream(fmt):
             assert torch.equal(first, again)
 
 
-@pytest.mark.parametrize("M", [4, 2000])
+@pytest.mark.parametrize("M", [4, 3000])
 def test_bounded_waits_give_up_and_the_next_call_is_right(M):
     x, w = draw(M, 1024, 1), lib().mx_quantize(draw(2048, 1024, 2), "mxfp8")
     a = lib().mx_quantize(x, "mxfp8")
