@@ -293,6 +293,13 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
                     tc::tc_fence_after();
                     const uint32_t st = tc::smem_u32(ring + s * kStage);
                     const uint32_t tsx = tmem + kPairScales + (i & 1) * 24, tsw = tsx + 4 * kScaleTiles;
+                    const uint64_t dx = tc::desc_sw128(st, 0, 1024), dw = tc::desc_sw128(st + 16384, 0, 1024);
+                    if ((kb + 1) * kBlock <= a.K) {
+                        tc::mma_mx_stage_pair<FP4>(acc, dx, dw, tc::desc_scales(st + 32768), tsx, tsw, kb > 0,
+                                                   &ctl.empty[s]);
+                        continue;
+                    }
+                    // the last block of a K that is not whole stages
                     const int st_tiles = min(kScaleTiles, a.ktiles - kb * kScaleTiles);
                     for (int k = 0; k < st_tiles; ++k) {
                         tc::copy_scales_pair(tsx + 4 * k, tc::desc_scales(st + 32768 + 512 * k));
@@ -301,8 +308,7 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
                             tc::copy_scales_pair(tsw + 8 * k + 4 * b,
                                                  tc::desc_scales(st + 32768 + 512 * (kScaleTiles * (1 + b) + k)));
                     }
-                    const uint64_t dx = tc::desc_sw128(st, 0, 1024), dw = tc::desc_sw128(st + 16384, 0, 1024);
-                    const int steps = min(4, (a.K - kb * kBlock + kStep - 1) / kStep);
+                    const int steps = (a.K - kb * kBlock + kStep - 1) / kStep;
                     for (int j = 0; j < steps; ++j) {
                         const int id = FP4 ? 2 * (j & 1) : j;
                         tc::mma_mx_pair<FP4>(acc, dx + 2 * j, dw + 2 * j, tc::idesc_mx(FP4, 256, 256, id),

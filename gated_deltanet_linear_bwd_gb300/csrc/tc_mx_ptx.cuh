@@ -130,6 +130,72 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
         "h"((uint16_t)3)
         : "memory");
 }
+// A whole stage in one go: its scale tiles to TMEM, its four MMAs (K = 128 in 8 bits,
+// 256 in 4), and the arrival on `bar` of both CTAs when they are done.  The issuing
+// warp is what bounds a pair's mainloop: one election for the stage and operands that
+// differ by constants halve its time against the single calls above.  Scale tiles lie 512
+// bytes apart from `scales`: A's, then B's rows 0-127, then B's rows 128-255.
+template <bool FP4>
+__device__ __forceinline__ void mma_mx_stage_pair(uint32_t d, uint64_t a, uint64_t b, uint64_t scales, uint32_t sa,
+                                                  uint32_t sb, uint32_t accumulate, uint64_t *bar) {
+    constexpr uint32_t kId0 = idesc_mx(FP4, 256, 256, 0), kId1 = idesc_mx(FP4, 256, 256, 1),
+                       kId2 = idesc_mx(FP4, 256, 256, 2), kId3 = idesc_mx(FP4, 256, 256, 3);
+    if (FP4)
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            ".reg .b64 a1, a2, a3, b1, b2, b3, s1, s2, s3, s4, s5;\n"
+            ".reg .b32 i0, i2, ta, t4, t8, tc;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "mov.b32 i0, %9;\n"
+            "mov.b32 i2, %10;\n"
+            "add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+            "add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+            "add.s64 s1, %3, 32;\n add.s64 s2, %3, 64;\n add.s64 s3, %3, 96;\n"
+            "add.s64 s4, %3, 128;\n add.s64 s5, %3, 160;\n"
+            "add.s32 ta, %4, 4;\n add.s32 t4, %5, 4;\n add.s32 t8, %5, 8;\n add.s32 tc, %5, 12;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], %3;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], s2;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t4], s4;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, i0, [%4], [%5], p;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, i2, [%4], [%5], 1;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [ta], s1;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t8], s3;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [tc], s5;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, i0, [ta], [t8], 1;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, i2, [ta], [t8], 1;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %8;\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "l"(scales), "r"(sa), "r"(sb), "r"(accumulate), "r"(smem_u32(bar)), "h"((uint16_t)3),
+            "n"(kId0), "n"(kId2)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            ".reg .b64 a1, a2, a3, b1, b2, b3, s1, s2;\n"
+            ".reg .b32 i0, i1, i2, i3, t4;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "mov.b32 i0, %9;\n mov.b32 i1, %10;\n mov.b32 i2, %11;\n mov.b32 i3, %12;\n"
+            "add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+            "add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+            "add.s64 s1, %3, 32;\n add.s64 s2, %3, 64;\n"
+            "add.s32 t4, %5, 4;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], %3;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], s1;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t4], s2;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, i0, [%4], [%5], p;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, i1, [%4], [%5], 1;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, i2, [%4], [%5], 1;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, i3, [%4], [%5], 1;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %8;\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "l"(scales), "r"(sa), "r"(sb), "r"(accumulate), "r"(smem_u32(bar)), "h"((uint16_t)3),
+            "n"(kId0), "n"(kId1), "n"(kId2), "n"(kId3)
+            : "memory");
+}
 // Tiled loads into this CTA that complete on a barrier of the pair (`bar`: a
 // shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
