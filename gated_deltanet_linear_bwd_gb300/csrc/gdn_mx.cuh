@@ -45,7 +45,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return r;
 }
 // Eight e2m1 elements, the first in the low half of the low byte.
-__device__ __forceinline__ uint32_t e2m1x8(const float *v) {
+__device__ __forceinline__ uint32_t e2m1x8(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
+                                           float v7) {
     uint32_t r;
     asm("{\n"
         ".reg .b8 b0, b1, b2, b3;\n"
@@ -56,7 +57,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *v) {
         "mov.b32 %0, {b0, b1, b2, b3};\n"
         "}\n"
         : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+        : "f"(v0), "f"(v1), "f"(v2), "f"(v3), "f"(v4), "f"(v5), "f"(v6), "f"(v7));
     return r;
 }
 
