@@ -1,12 +1,14 @@
 // gdn_mx_gemm.cu -- C = A B^T of microscaled matrices on the block-scaled tcgen05
 // MMAs.
 //
-// One CTA makes 128 rows of B (features) x `nt` rows of A (tokens) of C: the weight
-// is the MMA's 128-row operand, so that few tokens cost a narrow MMA and not idle
-// rows.  A producer warp feeds a ring of stages with TMA (both operand tiles and
-// both scale tiles, 128 bytes of K at a time), one warp copies scales to TMEM and
-// issues the MMAs, and the fp32 tile leaves TMEM through shared memory so that
-// rows of C are written 128 features at a time.
+// Small and middling products: one CTA makes 128 rows of B (features) x `nt` rows of A
+// (tokens) of C: the weight is the MMA's 128-row operand, so that few tokens cost a narrow
+// MMA and not idle rows.  A producer warp feeds a ring of stages with TMA (both operand
+// tiles and both scale tiles, 128 bytes of K at a time), one warp copies scales to TMEM
+// and issues the MMAs, and the fp32 tile leaves TMEM through shared memory so that rows of
+// C are written 128 features at a time.  Where tiles are too few for the GPU the CTAs of a
+// cluster share K: each leaves its fp32 tile in its shared memory, and after the cluster's
+// barrier each adds up its share of the rows, in rank order.
 #include <algorithm>
 
 #include "gdn_layer_internal.h"
@@ -18,7 +20,8 @@ namespace {
 
 constexpr int kFeat = 128;         // features of a tile
 constexpr int kThreads = 192;      // producer, MMA and four epilogue warps
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 10;
+constexpr int kMaxSplits = 8;
 
 struct GemmArgs {
     const uint8_t *sx, *sw;        // scales of tokens and features
@@ -28,6 +31,7 @@ struct GemmArgs {
     int kblocks, ktiles;           // 128-byte blocks of K, scale tiles along K
     int stages, stage_bytes, tmem_cols;
     int c_fp32;
+    int early_w;                   // the weight was complete before the kernel ahead of this one began
     int *status;
     long long spin_limit;
 };
@@ -74,6 +78,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     const int kb0 = (int)((long long)a.kblocks * rank / splits);
     const int kb1 = (int)((long long)a.kblocks * (rank + 1) / splits);
 
+    if (threadIdx.x == 32) {
+        tc::prefetch_map(&map_x);
+        tc::prefetch_map(&map_w);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             tc::mbar_init(&ctl.full[s], 1);
@@ -91,32 +99,42 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    pdl_enter();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const uint32_t x_off = kFeat * 128, sw_off = x_off + a.nt * 128, sx_off = sw_off + kScaleTiles * 512;
     if (warp == 0) {
-        if (lane == 0) {
-            bool ok = true;
-            int kb = kb0;
-            for (; kb < kb1; ++kb) {
-                const int i = kb - kb0, s = i % a.stages;
-                if (i >= a.stages)
-                    ok = tc::mbar_wait(&ctl.empty[s], (i / a.stages - 1) & 1, a.spin_limit, a.status);
-                if (!ok) break;
-                uint8_t *st = ring + s * a.stage_bytes;
-                const uint32_t sb = 512u * (uint32_t)min(kScaleTiles, a.ktiles - kb * kScaleTiles);
-                tc::mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(kFeat + a.nt) * 128u + 2u * sb);
-                tc::tma_load_2d(st, &map_w, &ctl.full[s], kb * 128, f0);
-                tc::tma_load_2d(st + x_off, &map_x, &ctl.full[s], kb * 128, t0);
-                tc::bulk_load(st + sw_off, a.sw + ((long long)(f0 / 128) * a.ktiles + kb * kScaleTiles) * 512,
-                              sb, &ctl.full[s]);
-                tc::bulk_load(st + sx_off, a.sx + ((long long)(t0 / 128) * a.ktiles + kb * kScaleTiles) * 512,
-                              sb, &ctl.full[s]);
+        const int n = kb1 - kb0;
+        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full);
+        const uint8_t *sw = a.sw + (long long)(f0 / 128) * a.ktiles * 512, *sx = a.sx + (long long)(t0 / 128) * a.ktiles * 512;
+        auto tile_bytes = [&](int kb) { return 512u * (uint32_t)min(kScaleTiles, a.ktiles - kb * kScaleTiles); };
+        auto load_w = [&](int kb, uint32_t st, uint32_t bar) {       // arms the stage for all it gets
+            const uint32_t sb = tile_bytes(kb);
+            tc::expect_bytes(bar, (uint32_t)(kFeat + a.nt) * 128u + 2u * sb, true);
+            tc::load_operand(st, &map_w, kb * 128, f0, st + sw_off, sw + kb * (512 * kScaleTiles), sb, bar);
+        };
+        auto load_x = [&](int kb, uint32_t st, uint32_t bar) {
+            tc::load_operand(st + x_off, &map_x, kb * 128, t0, st + sx_off, sx + kb * (512 * kScaleTiles), tile_bytes(kb), bar);
+        };
+        // a ring's worth of weights may come before the kernel ahead has written the tokens
+        const int ahead = a.early_w ? min(n, a.stages) : 0;
+        for (int i = 0; i < ahead; ++i) load_w(kb0 + i, ring0 + i * a.stage_bytes, full0 + 8 * i);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int i = 0, s = 0;
+        uint32_t parity = 1;                         // of the stage's last release; the first round has none
+        for (; i < n; ++i) {
+            if (i >= a.stages) {
+                const bool free = tc::mbar_wait(&ctl.empty[s], parity, a.spin_limit, a.status);
+                if (!__all_sync(0xffffffffu, free)) {
+                    ctl.failed = 1;
+                    break;
+                }
             }
-            if (!ok) ctl.failed = 1;
-            ctl.issued = kb - kb0;
+            const uint32_t st = ring0 + s * a.stage_bytes, bar = full0 + 8 * s;
+            if (i >= ahead) load_w(kb0 + i, st, bar);
+            load_x(kb0 + i, st, bar);
+            if (++s == a.stages) s = 0, parity ^= 1;
         }
-        __syncwarp();
+        if (lane == 0) ctl.issued = i;
     } else if (warp == 1) {
         const uint32_t tsw = tmem + a.nt, tsx = tsw + 4 * kScaleTiles;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -128,13 +146,19 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
             }
             tc::tc_fence_after();
             const uint32_t st = tc::smem_u32(ring + s * a.stage_bytes);
+            const uint64_t dw = tc::desc_sw128(st, 0, 1024), dx = tc::desc_sw128(st + x_off, 0, 1024);
+            if ((kb + 1) * kBlock <= a.K) {
+                tc::mma_mx_stage<FP4>(tmem, dw, dx, tc::desc_scales(st + sw_off), tsw, tsx,
+                                      tc::idesc_mx(FP4, kFeat, a.nt, 0), i > 0, &ctl.empty[s]);
+                continue;
+            }
+            // the last block of a K that is not whole stages
             const int tiles = min(kScaleTiles, a.ktiles - kb * kScaleTiles);
             for (int k = 0; k < tiles; ++k) {
                 tc::copy_scales(tsw + 4 * k, tc::desc_scales(st + sw_off + 512 * k));
                 tc::copy_scales(tsx + 4 * k, tc::desc_scales(st + sx_off + 512 * k));
             }
-            const uint64_t dw = tc::desc_sw128(st, 0, 1024), dx = tc::desc_sw128(st + x_off, 0, 1024);
-            const int steps = min(4, (a.K - kb * kBlock + kStep - 1) / kStep);
+            const int steps = (a.K - kb * kBlock + kStep - 1) / kStep;
             for (int j = 0; j < steps; ++j) {
                 const int id = FP4 ? 2 * (j & 1) : j, col = FP4 ? 4 * (j >> 1) : 0;
                 tc::mma_mx<FP4>(tmem, dw + 2 * j, dx + 2 * j, tc::idesc_mx(FP4, kFeat, a.nt, id),
@@ -144,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         }
         tc::mma_commit(&ctl.done);
     }
+    if (warp != 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // C may be written
     __syncwarp();
     // every MMA done: the ring is free and the tile is whole
     if (!tc::mbar_wait(&ctl.done, 0, a.spin_limit, a.status)) {
@@ -158,11 +183,19 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
             tc::mbar_drain(&ctl.full[j % a.stages], (j / a.stages) & 1);
     float *out = reinterpret_cast<float *>(ring);    // [nt][128]
     if (ok && warp >= 2) {
-        for (int c = 0; c < a.nt; c += 16) {
+        float *to = out + 32 * (warp & 3) + lane;
+        if (a.nt == 16) {
             float v[16];
-            tc::tmem_ld8x2(tc::tmem_addr(tmem, warp, c), tc::tmem_addr(tmem, warp, c + 8), v, v + 8);
+            tc::tmem_ld8x2(tc::tmem_addr(tmem, warp, 0), tc::tmem_addr(tmem, warp, 8), v, v + 8);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) out[(c + j) * kFeat + 32 * (warp & 3) + lane] = v[j];
+            for (int j = 0; j < 16; ++j) to[j * kFeat] = v[j];
+        } else {
+            for (int c = 0; c < a.nt; c += 32) {
+                float v[32];
+                tc::tmem_ld32(tc::tmem_addr(tmem, warp, c), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) to[(c + j) * kFeat] = v[j];
+            }
         }
     }
     tc::tc_fence_before();
@@ -171,12 +204,21 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     tc::tc_fence_after();
     if (ok) {
         const uint32_t base = tc::smem_u32(out);
-        for (int j = rank * (kThreads / 32) + warp; j < a.nt && t0 + j < a.tokens; j += splits * (kThreads / 32)) {
-            const uint32_t at = base + (uint32_t)(j * kFeat + 4 * lane) * 4u;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < splits; ++r) {
-                const float4 p = tc::ld_cluster4(tc::map_rank(at, r));
-                v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        const int step = splits * (kThreads / 32), rows = min(a.nt, a.tokens - t0);
+        for (int j = rank * (kThreads / 32) + warp; j < rows; j += step) {
+            const int at = j * kFeat + 4 * lane;
+            float4 v;
+            if (splits == 1) {
+                v = *reinterpret_cast<const float4 *>(out + at);
+            } else {
+                float4 p[kMaxSplits];
+#pragma unroll
+                for (int r = 0; r < kMaxSplits; ++r)
+                    if (r < splits) p[r] = tc::ld_cluster4(tc::map_rank(base + 4u * (uint32_t)at, r));
+                v = p[0];
+#pragma unroll
+                for (int r = 1; r < kMaxSplits; ++r)
+                    if (r < splits) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
             }
             store_c4(a, t0 + j, f0 + 4 * lane, v);
         }
@@ -199,6 +241,7 @@ constexpr int kPairOut = 16384;                      // a staged 128 x 128-byte 
 struct PairArgs {
     int M, N, K, kblocks, ktiles;
     int m_tiles, n_tiles;
+    int early_w;                                     // as in GemmArgs
     int *status;
     long long spin_limit;
 };
@@ -232,6 +275,13 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
     const int rank = (int)tc::cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
 
+    if (threadIdx.x == 32) {
+        tc::prefetch_map(&map_x);
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_sx);
+        tc::prefetch_map(&map_sw);
+        tc::prefetch_map(&map_c);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             tc::mbar_init(&ctl.full[s], 1);
@@ -248,36 +298,45 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
     tc::cluster_sync();                              // both CTAs' barriers and TMEM are there
     tc::tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    pdl_enter();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;                               // stages asked for
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                const int row = (tile % a.m_tiles) * 2 + rank, feat = tile / a.m_tiles * 2;   // in 128s
-                for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
-                    const int s = i % kPairStages;
-                    if (i >= kPairStages &&
-                        !tc::mbar_wait(&ctl.empty[s], (i / kPairStages - 1) & 1, a.spin_limit, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = ring + s * kStage;
-                    const uint32_t bar = tc::map_rank(tc::smem_u32(&ctl.full[s]), 0);
-                    if (rank == 0) tc::mbar_arrive_expect_tx(&ctl.full[s], 2u * kBytes);
-                    tc::tma_load_2d_pair(st, &map_x, bar, kb * 128, row * 128);
-                    tc::tma_load_2d_pair(st + 16384, &map_w, bar, kb * 128, (feat + rank) * 128);
-                    tc::tma_load_3d_pair(st + 32768, &map_sx, bar, 0, kb * kScaleTiles, row);
-                    tc::tma_load_3d_pair(st + 32768 + 512 * kScaleTiles, &map_sw, bar, 0, kb * kScaleTiles, feat);
+        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), bar0 = tc::map_rank(full0, 0);
+        auto load_w = [&](int kb, int feat, int s) {                 // and arms the pair's barrier for both CTAs
+            const uint32_t st = ring0 + s * kStage;
+            tc::expect_bytes(full0 + 8 * s, 2u * kBytes, rank == 0);
+            tc::load_operand_pair(st + 16384, &map_w, kb * 128, (feat + rank) * 128, st + 32768 + 512 * kScaleTiles,
+                                  &map_sw, kb * kScaleTiles, feat, bar0 + 8 * s);
+        };
+        auto load_x = [&](int kb, int row, int s) {
+            const uint32_t st = ring0 + s * kStage;
+            tc::load_operand_pair(st, &map_x, kb * 128, row * 128, st + 32768, &map_sx, kb * kScaleTiles, row,
+                                  bar0 + 8 * s);
+        };
+        // the first tile's weights may come before the kernel ahead has written the tokens
+        const int ahead = a.early_w && pair < tiles ? min(kPairStages, a.kblocks) : 0;
+        for (int i = 0; i < ahead; ++i) load_w(i, pair / a.m_tiles * 2, i);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int i = 0, s = 0;                            // stages asked for
+        uint32_t parity = 1;                         // of the stage's last release; the first round has none
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            const int feat = tile / a.m_tiles * 2, row = (tile - feat / 2 * a.m_tiles) * 2 + rank;    // in 128s
+            for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
+                if (i >= kPairStages) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.empty[s], parity, a.spin_limit, a.status));
+                    if (!ok) break;
                 }
+                if (i >= ahead) load_w(kb, feat, s);
+                load_x(kb, row, s);
+                if (++s == kPairStages) s = 0, parity ^= 1;
             }
-            ctl.issued = i;
         }
-        __syncwarp();
+        if (lane == 0) ctl.issued = i;
     } else if (warp == 1) {
         if (rank == 0) {
-            int i = 0, t = 0;
+            int i = 0, t = 0, s = 0;
+            uint32_t parity = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
                 if (t > 0) {
@@ -287,16 +346,16 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
                 tc::tc_fence_after();
                 const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
                 for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
-                    const int s = i % kPairStages;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.full[s], (i / kPairStages) & 1, a.spin_limit, a.status));
+                    const int at = s;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.full[at], parity, a.spin_limit, a.status));
                     if (!ok) break;
-                    tc::tc_fence_after();
-                    const uint32_t st = tc::smem_u32(ring + s * kStage);
+                    if (++s == kPairStages) s = 0, parity ^= 1;
+                    const uint32_t st = tc::smem_u32(ring) + at * kStage;
                     const uint32_t tsx = tmem + kPairScales + (i & 1) * 24, tsw = tsx + 4 * kScaleTiles;
                     const uint64_t dx = tc::desc_sw128(st, 0, 1024), dw = tc::desc_sw128(st + 16384, 0, 1024);
                     if ((kb + 1) * kBlock <= a.K) {
                         tc::mma_mx_stage_pair<FP4>(acc, dx, dw, tc::desc_scales(st + 32768), tsx, tsw, kb > 0,
-                                                   &ctl.empty[s]);
+                                                   &ctl.empty[at]);
                         continue;
                     }
                     // the last block of a K that is not whole stages
@@ -315,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
                                              tsx + (FP4 ? 4 * (j >> 1) : 0), tsw + (FP4 ? 8 * (j >> 1) : 0),
                                              kb > 0 || j > 0);
                     }
-                    tc::mma_commit_pair(&ctl.empty[s]);
+                    tc::mma_commit_pair(&ctl.empty[at]);
                 }
                 if (ok) tc::mma_commit_pair(&ctl.acc_full);
             }
@@ -324,6 +383,7 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
     } else {
         // epilogue: 64 (bf16) or 32 (fp32) columns at a time through shared memory to a TMA store
         const bool storer = warp == 2 && lane == 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // C may be written
         const int quarter = warp & 3;
         int t = 0, staged = 0;
         for (int tile = pair; tile < tiles; tile += pairs, ++t) {
@@ -384,13 +444,14 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
 }
 
 template <bool FP4, typename TO>
-gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t q) {
+gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, cudaStream_t q) {
     PairArgs g{};
     g.M = a->M, g.N = a->N, g.K = a->K;
     g.kblocks = (a->K + (FP4 ? 255 : 127)) / (FP4 ? 256 : 128);
     g.ktiles = (a->K + 127) / 128;
     g.m_tiles = (a->M + 255) / 256;
     g.n_tiles = (a->N + 255) / 256;
+    g.early_w = early_w;
     g.status = dev.status;
     g.spin_limit = dev.spin_limit;
     const long long bytes = FP4 ? a->K / 2 : a->K;
@@ -414,34 +475,57 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStr
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "mx product launch");
 }
 
-// Pairs where their 256 x 256 tiles fill most of the GPU and TMA can store C's rows
-// (which start on 16 bytes).
+// Tokens of a tile: 16, or as many as there are up to 128.
+int token_tile(int tokens) {
+    int nt = 16;
+    while (nt < 128 && nt < tokens) nt *= 2;
+    return nt;
+}
+
+// Pairs take over from single CTAs where those fill the GPU without sharing K, unless few
+// tokens leave most of a pair's tile idle, and TMA can store C's rows (which start on 16
+// bytes).  Us of single CTAs | pairs in 4 bits at K = 4096: 256 x 4096 10.3 | 11.2, 384 x
+// 4096 13.2 | 10.8, 128 x 12288 13.2 | 11.3, 7 x 12288 7.1 | 11.5, 512 x 1024 7.4 | 10.6,
+// 1536 x 1024 14 | 10.8.
 bool pair_fits(const gdn_mx_matmul_args *a, int sms) {
+    const int nt = token_tile(a->M);
+    const long long singles = (long long)((a->N + kFeat - 1) / kFeat) * ((a->M + nt - 1) / nt);
     const long long tiles = (long long)((a->M + 255) / 256) * ((a->N + 255) / 256);
-    return (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0 && tiles * 4 >= sms &&
+    return (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0 && nt > 32 && 2 * singles > sms &&
            tiles < (1ll << 30);
 }
 
-gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t q) {
+gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, cudaStream_t q) {
     const bool fp4 = a->format == GDN_MXFP4;
     cudaError_t e = tc::encoder();
     if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled lookup");
     if (pair_fits(a, dev.sms)) {
-        if (a->out_dtype == GDN_FP32) return fp4 ? run_pair<true, float>(a, dev, q) : run_pair<false, float>(a, dev, q);
-        return fp4 ? run_pair<true, __nv_bfloat16>(a, dev, q) : run_pair<false, __nv_bfloat16>(a, dev, q);
+        if (a->out_dtype == GDN_FP32) return fp4 ? run_pair<true, float>(a, dev, early_w, q) : run_pair<false, float>(a, dev, early_w, q);
+        return fp4 ? run_pair<true, __nv_bfloat16>(a, dev, early_w, q)
+                   : run_pair<false, __nv_bfloat16>(a, dev, early_w, q);
     }
     GemmArgs g{};
     g.sx = a->a_scales;
     g.sw = a->b_scales;
     g.c = a->c;
     g.tokens = a->M, g.feats = a->N, g.K = a->K;
-    g.nt = 16;
-    while (g.nt < 128 && g.nt < a->M) g.nt *= 2;
+    g.nt = token_tile(a->M);
     g.token_tiles = (a->M + g.nt - 1) / g.nt;
     g.kblocks = (a->K + (fp4 ? 255 : 127)) / (fp4 ? 256 : 128);
     g.ktiles = (a->K + 127) / 128;
     g.stage_bytes = (kFeat + g.nt) * 128 + (fp4 ? 2048 : 1024);
-    g.stages = std::min(kMaxStages, 96 * 1024 / g.stage_bytes);
+    // The CTAs of a cluster share K, by powers of two (clusters of 3 took longer than no
+    // cluster), while slots of the GPU are empty: two CTAs to an SM and up to 8 to a cluster
+    // for few tokens; one and up to 4 for many, whose tiles take long to add up (4096 x
+    // 4096, 128 tokens, 4 bits: 7.4 us with 4, 9.7 with 2, 13.5 with 8 at two to an SM).
+    const long long tiles = (long long)((a->N + kFeat - 1) / kFeat) * g.token_tiles;
+    const bool few = g.nt <= 32;
+    int splits = 1;
+    while (splits < (few ? kMaxSplits : 4) && 2 * splits <= g.kblocks && 2 * splits * tiles <= (few ? 2 : 1) * dev.sms)
+        splits *= 2;
+    const int per = (g.kblocks + splits - 1) / splits;
+    g.stages = std::max(1, std::min({kMaxStages, per, (tiles * splits <= dev.sms ? 200 : 100) * 1024 / g.stage_bytes}));
+    g.early_w = early_w;
     g.tmem_cols = 32;
     while (g.tmem_cols < g.nt + 16) g.tmem_cols *= 2;
     g.c_fp32 = a->out_dtype == GDN_FP32;
@@ -456,8 +540,7 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t
     auto k = fp4 ? gemm_kernel<true> : gemm_kernel<false>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
         return cuda_fail(e, "shared memory of the product");
-    const int splits = 1;
-    const long long ctas = (long long)((a->N + kFeat - 1) / kFeat) * g.token_tiles * splits;
+    const long long ctas = tiles * splits;
     if (ctas >= (1ll << 31)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
     prof_before("mx_gemm", q);
     e = launch_pdl_cluster(k, dim3((unsigned)ctas), dim3(kThreads), smem, splits, q, mapx, mapw, g);
@@ -471,7 +554,9 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, cudaStream_t
 
 using namespace gdn;
 
-extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) {
+// early_w: the kernel ahead in the stream began only when all before it, the writers of b
+// among them, had ended.
+static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, void *stream) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->M < 0 || a->N < 0 || a->K < 0)
         return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
@@ -494,8 +579,10 @@ extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) {
                                               (cudaStream_t)stream);
         return e == cudaSuccess ? GDN_OK : cuda_fail(e, "clearing c");
     }
-    return mx::run(a, dev, (cudaStream_t)stream);
+    return mx::run(a, dev, early_w, (cudaStream_t)stream);
 }
+
+extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) { return matmul(a, false, stream); }
 
 // Bytes of X's elements in the workspace, its scales following.
 static size_t linear_data_bytes(const gdn_mx_linear_args *a) {
@@ -522,5 +609,5 @@ extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_
     const gdn_status st = gdn_mx_quantize(&q, stream);
     if (st != GDN_OK) return st;
     const gdn_mx_matmul_args m{data, scales, a->w, a->w_scales, a->M, a->N, a->K, a->format, a->out_dtype, a->c};
-    return gdn_mx_matmul(&m, stream);
+    return matmul(&m, a->M > 0 && a->K > 0, stream);
 }

@@ -77,7 +77,10 @@ template <typename T, bool FP4, bool ROWS>
 __global__ void __launch_bounds__(256) quantize_kernel(const T *x, uint8_t *data, uint8_t *scales,
                                                        int rows, int K, int ktiles, int log_parts) {
     using Raw = typename Load8<T>::Raw;
-    pdl_enter();
+    // the kernel behind may start once all before this one has ended: a product that
+    // follows loads its weight under the quantisation
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, spans = (ktiles + 1) / 2, parts = 1 << log_parts;
     const int per = ((spans + parts - 1) / parts + kSpans - 1) / kSpans * kSpans;
     const long long padded = (rows + 127ll) / 128 * 128;

@@ -72,6 +72,62 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
         : "memory");
 }
 
+// A whole stage in one go: its scale tiles to TMEM, its four MMAs (K = 128 in 8 bits,
+// 256 in 4), and the arrival on `bar` when they are done.  One election for the stage and
+// operands that differ by constants: single calls take the issuing warp twice as long.
+// Scale tiles lie 512 bytes apart from `scales`: A's, then B's.
+template <bool FP4>
+__device__ __forceinline__ void mma_mx_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t scales, uint32_t sa,
+                                             uint32_t sb, uint32_t idesc, uint32_t accumulate, uint64_t *bar) {
+    if (FP4)                       // scale ids 0 and 2: bits 4-5 and 29-30
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            ".reg .b64 a1, a2, a3, b1, b2, b3, s1, s2, s3;\n"
+            ".reg .b32 i2, ta, tb;\n"
+            "setp.ne.b32 p, %7, 0;\n"
+            "or.b32 i2, %6, 0x40000020;\n"
+            "add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+            "add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+            "add.s64 s1, %3, 32;\n add.s64 s2, %3, 64;\n add.s64 s3, %3, 96;\n"
+            "add.s32 ta, %4, 4;\n add.s32 tb, %5, 4;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %3;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], s2;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %6, [%4], [%5], p;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, i2, [%4], [%5], 1;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [ta], s1;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [tb], s3;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %6, [ta], [tb], 1;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, i2, [ta], [tb], 1;\n"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "l"(scales), "r"(sa), "r"(sb), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar))
+            : "memory");
+    else                           // scale ids 0 to 3
+        asm volatile(
+            "{\n"
+            ".reg .pred p, e;\n"
+            ".reg .b64 a1, a2, a3, b1, b2, b3, s1;\n"
+            ".reg .b32 i1, i2, i3;\n"
+            "setp.ne.b32 p, %7, 0;\n"
+            "or.b32 i1, %6, 0x20000010;\n or.b32 i2, %6, 0x40000020;\n or.b32 i3, %6, 0x60000030;\n"
+            "add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+            "add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+            "add.s64 s1, %3, 32;\n"
+            "elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %3;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], s1;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %6, [%4], [%5], p;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, i1, [%4], [%5], 1;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, i2, [%4], [%5], 1;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, i3, [%4], [%5], 1;\n"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n"
+            "}\n" ::"r"(d),
+            "l"(a), "l"(b), "l"(scales), "r"(sa), "r"(sb), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar))
+            : "memory");
+}
+
 // ------------------------------------------------------------------ CTA pairs
 // The same for cta_group::2: two CTAs of a cluster work on one 256-row tile.  Each
 // holds its 128 rows of A, half the rows of B, and 128 lanes of D; the even CTA issues
@@ -196,21 +252,49 @@ __device__ __forceinline__ void mma_mx_stage_pair(uint32_t d, uint64_t a, uint64
             "n"(kId0), "n"(kId1), "n"(kId2), "n"(kId3)
             : "memory");
 }
-// Tiled loads into this CTA that complete on a barrier of the pair (`bar`: a
-// shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+// One operand's tile and scale tiles into this CTA, completing on a barrier of the pair
+// (`bar`: a shared::cluster address).  Warp-collective, like the MMAs and for the same
+// reason: issued by one lane of divergent code, the loads of a stage took longer than its
+// MMAs.
+__device__ __forceinline__ void load_operand_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                                  uint32_t scales, const CUtensorMap *smap, int k, int r,
+                                                  uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        "{\n"
+        ".reg .pred e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%8];\n"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%4], [%5, {%9, %6, %7}], [%8];\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(scales), "l"(reinterpret_cast<uint64_t>(smap)),
+        "r"(k), "r"(r), "r"(bar), "r"(0)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
-                                                 int c2) {
+// The same for one CTA: the scale tiles as a contiguous copy, the barrier its own.
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t scales,
+                                             const uint8_t *src, uint32_t bytes, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        "{\n"
+        ".reg .pred e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%7];\n"
+        "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%4], [%5], %6, [%7];\n"
+        "}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(scales), "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+// One lane arms `bar` for `bytes`, if `here`.  Warp-collective.
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes, bool here) {
+    asm volatile(
+        "{\n"
+        ".reg .pred e, q;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.and.u32 q, %2, 0, e;\n"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+        "}\n" ::"r"(bar),
+        "r"(bytes), "r"((uint32_t)here)
         : "memory");
 }
 // Arrives on another CTA's barrier (a shared::cluster address).
@@ -218,13 +302,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
+// Starts the fetch of a tensor map (a kernel parameter) that a load will soon use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
