@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     const uint32_t x_off = kFeat * 128, sw_off = x_off + a.nt * 128, sx_off = sw_off + kScaleTiles * 512;
     if (warp == 0) {
         const int n = kb1 - kb0;
-        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full);
+        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), empty0 = tc::smem_u32(ctl.empty);
         const uint8_t *sw = a.sw + (long long)(f0 / 128) * a.ktiles * 512, *sx = a.sx + (long long)(t0 / 128) * a.ktiles * 512;
         auto tile_bytes = [&](int kb) { return 512u * (uint32_t)min(kScaleTiles, a.ktiles - kb * kScaleTiles); };
         auto load_w = [&](int kb, uint32_t st, uint32_t bar) {       // arms the stage for all it gets
@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         uint32_t parity = 1;                         // of the stage's last release; the first round has none
         for (; i < n; ++i) {
             if (i >= a.stages) {
-                const bool free = tc::mbar_wait(&ctl.empty[s], parity, a.spin_limit, a.status);
-                if (!__all_sync(0xffffffffu, free)) {
+                if (!tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status)) {
                     ctl.failed = 1;
                     break;
                 }
@@ -136,15 +135,14 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         }
         if (lane == 0) ctl.issued = i;
     } else if (warp == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");           // waits with a limit begin when work does
         const uint32_t tsw = tmem + a.nt, tsx = tsw + 4 * kScaleTiles;
         for (int kb = kb0; kb < kb1; ++kb) {
             const int i = kb - kb0, s = i % a.stages;
-            const bool full = tc::mbar_wait(&ctl.full[s], (i / a.stages) & 1, a.spin_limit, a.status);
-            if (!__all_sync(0xffffffffu, full)) {
+            if (!tc::mbar_spin(tc::smem_u32(&ctl.full[s]), (i / a.stages) & 1, a.spin_limit, a.status)) {
                 ctl.failed = 1;
                 break;
             }
-            tc::tc_fence_after();
             const uint32_t st = tc::smem_u32(ring + s * a.stage_bytes);
             const uint64_t dw = tc::desc_sw128(st, 0, 1024), dx = tc::desc_sw128(st + x_off, 0, 1024);
             if ((kb + 1) * kBlock <= a.K) {
@@ -168,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         }
         tc::mma_commit(&ctl.done);
     }
-    if (warp != 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // C may be written
+    if (warp > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // C may be written
     __syncwarp();
     // every MMA done: the ring is free and the tile is whole
     if (!tc::mbar_wait(&ctl.done, 0, a.spin_limit, a.status)) {
@@ -233,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
 // SM takes from L2 per MMA; the accumulators of two tiles share 448 TMEM columns, the
 // last 64 of the one being the first 64 of the other, so that the epilogue of a tile
 // runs under the next one's MMAs once it has taken those 64.
+constexpr int kPairThreads = 224;                    // weights, MMA, four epilogue warps, tokens
 constexpr int kPairStages = 5;
 constexpr int kPairAcc = 192;                        // column of the second accumulator
 constexpr int kPairScales = 448;                     // columns of the scales: two sets of 24
@@ -256,7 +255,7 @@ template <bool FP4>
 constexpr int pair_stage_bytes() { return 32768 + (FP4 ? 3072 : 2048); }
 
 template <bool FP4, typename TO>
-__global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_constant__ CUtensorMap map_x,
+__global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_constant__ CUtensorMap map_x,
                                                              const __grid_constant__ CUtensorMap map_w,
                                                              const __grid_constant__ CUtensorMap map_sx,
                                                              const __grid_constant__ CUtensorMap map_sw,
@@ -300,22 +299,25 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
     const uint32_t tmem = ctl.tmem;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 0) {
-        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), bar0 = tc::map_rank(full0, 0);
-        auto load_w = [&](int kb, int feat, int s) {                 // and arms the pair's barrier for both CTAs
+    const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), empty0 = tc::smem_u32(ctl.empty);
+    if (warp == 0 || warp == 6) {
+        // two warps, as one alone is late with a stage's four loads
+        const bool weights = warp == 0;
+        const uint32_t bar0 = tc::map_rank(full0, 0);
+        auto load = [&](int kb, int row, int feat, int s) {
             const uint32_t st = ring0 + s * kStage;
-            tc::expect_bytes(full0 + 8 * s, 2u * kBytes, rank == 0);
-            tc::load_operand_pair(st + 16384, &map_w, kb * 128, (feat + rank) * 128, st + 32768 + 512 * kScaleTiles,
-                                  &map_sw, kb * kScaleTiles, feat, bar0 + 8 * s);
-        };
-        auto load_x = [&](int kb, int row, int s) {
-            const uint32_t st = ring0 + s * kStage;
-            tc::load_operand_pair(st, &map_x, kb * 128, row * 128, st + 32768, &map_sx, kb * kScaleTiles, row,
-                                  bar0 + 8 * s);
+            if (weights) {                           // and arms the pair's barrier for all that both CTAs get
+                tc::expect_bytes(full0 + 8 * s, 2u * kBytes, rank == 0);
+                tc::load_operand_pair(st + 16384, &map_w, kb * 128, (feat + rank) * 128,
+                                      st + 32768 + 512 * kScaleTiles, &map_sw, kb * kScaleTiles, feat, bar0 + 8 * s);
+            } else {
+                tc::load_operand_pair(st, &map_x, kb * 128, row * 128, st + 32768, &map_sx, kb * kScaleTiles, row,
+                                      bar0 + 8 * s);
+            }
         };
         // the first tile's weights may come before the kernel ahead has written the tokens
-        const int ahead = a.early_w && pair < tiles ? min(kPairStages, a.kblocks) : 0;
-        for (int i = 0; i < ahead; ++i) load_w(i, pair / a.m_tiles * 2, i);
+        const int ahead = weights && a.early_w && pair < tiles ? min(kPairStages, a.kblocks) : 0;
+        for (int i = 0; i < ahead; ++i) load(i, 0, pair / a.m_tiles * 2, i);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int i = 0, s = 0;                            // stages asked for
         uint32_t parity = 1;                         // of the stage's last release; the first round has none
@@ -324,33 +326,33 @@ __global__ void __launch_bounds__(kThreads) gemm_pair_kernel(const __grid_consta
             const int feat = tile / a.m_tiles * 2, row = (tile - feat / 2 * a.m_tiles) * 2 + rank;    // in 128s
             for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
                 if (i >= kPairStages) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.empty[s], parity, a.spin_limit, a.status));
+                    ok = tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status);
                     if (!ok) break;
                 }
-                if (i >= ahead) load_w(kb, feat, s);
-                load_x(kb, row, s);
+                if (i >= ahead) load(kb, row, feat, s);
                 if (++s == kPairStages) s = 0, parity ^= 1;
             }
         }
-        if (lane == 0) ctl.issued = i;
+        if (weights && lane == 0) ctl.issued = i;
     } else if (warp == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");           // waits with a limit begin when work does
         if (rank == 0) {
             int i = 0, t = 0, s = 0;
             uint32_t parity = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
                 if (t > 0) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_free, (t - 1) & 1, a.spin_limit, a.status));
+                    ok = tc::mbar_spin(tc::smem_u32(&ctl.acc_free), (t - 1) & 1, a.spin_limit, a.status);
                     if (!ok) break;
                 }
                 tc::tc_fence_after();
                 const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
                 for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
                     const int at = s;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.full[at], parity, a.spin_limit, a.status));
+                    ok = tc::mbar_spin(full0 + 8 * at, parity, a.spin_limit, a.status);
                     if (!ok) break;
                     if (++s == kPairStages) s = 0, parity ^= 1;
-                    const uint32_t st = tc::smem_u32(ring) + at * kStage;
+                    const uint32_t st = ring0 + at * kStage;
                     const uint32_t tsx = tmem + kPairScales + (i & 1) * 24, tsw = tsx + 4 * kScaleTiles;
                     const uint64_t dx = tc::desc_sw128(st, 0, 1024), dw = tc::desc_sw128(st + 16384, 0, 1024);
                     if ((kb + 1) * kBlock <= a.K) {
@@ -470,7 +472,7 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
         return cuda_fail(e, "shared memory of the product");
     const int pairs = (int)std::min<long long>((long long)g.m_tiles * g.n_tiles, dev.sms / 2);
     prof_before("mx_gemm_pair", q);
-    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kThreads), smem, 2, q, mx, mw, msx, msw, mc, g);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), smem, 2, q, mx, mw, msx, msw, mc, g);
     prof_after(q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "mx product launch");
 }

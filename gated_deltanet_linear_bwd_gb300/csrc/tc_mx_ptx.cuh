@@ -128,6 +128,27 @@ __device__ __forceinline__ void mma_mx_stage(uint32_t d, uint64_t a, uint64_t b,
             : "memory");
 }
 
+// mbar_wait for a whole warp by plain polling: the polls of mbar_wait may put the warp to
+// sleep, and waking costs a mainloop that is short of time more than polling does.  The
+// same answer in every lane.
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, long long limit, int *status) {
+    for (long long i = 0; i < limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+    }
+    set_status(status, GDN_ERR_TIMEOUT);
+    return false;
+}
+
 // ------------------------------------------------------------------ CTA pairs
 // The same for cta_group::2: two CTAs of a cluster work on one 256-row tile.  Each
 // holds its 128 rows of A, half the rows of B, and 128 lanes of D; the even CTA issues
