@@ -57,10 +57,10 @@ class gdn_rms_norm_bwd_args(ctypes.Structure):
 
 GDN_MXFP8, GDN_MXFP4 = 0, 1
 
-_PLAIN = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_step": gdn_linrec_step_args,
+_PLAIN = {"gdn_linrec_step": gdn_linrec_step_args,
           "gdn_mx_quantize": gdn_mx_quantize_args, "gdn_mx_dequantize": gdn_mx_dequantize_args,
           "gdn_mx_matmul": gdn_mx_matmul_args, "gdn_rms_norm_fwd": gdn_rms_norm_fwd_args}
-_WITH_WORKSPACE = {"gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_mx_linear": gdn_mx_linear_args,
+_WITH_WORKSPACE = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_mx_linear": gdn_mx_linear_args,
                    "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args}
 STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
 EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \

@@ -41,6 +41,10 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Lets `kernel` take `bytes` of dynamic shared memory on the current device; asks the
+// runtime once for each kernel, device and larger size.
+cudaError_t allow_smem(const void *kernel, size_t bytes);
+
 // out[d] = sum over `rows` of partial[row][d], in a fixed order.
 cudaError_t column_sum(const float *partial, int rows, int D, float *out, cudaStream_t s);
 

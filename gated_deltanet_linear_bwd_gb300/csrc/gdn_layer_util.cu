@@ -1,5 +1,9 @@
-// gdn_layer_util.cu -- the sum over rows that the layer operators' weight
-// gradients end with.
+// gdn_layer_util.cu -- what the layer operators share: the sum over rows that their
+// weight gradients end with, and the shared-memory limits of their kernels.
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "gdn_layer_internal.h"
 
 namespace gdn {
@@ -26,6 +30,20 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void *kernel, size_t bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<const void *, int>, size_t> granted;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    size_t &has = granted[{kernel, dev}];
+    if (has >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) has = bytes;
+    return e;
+}
 
 cudaError_t column_sum(const float *partial, int rows, int D, float *out, cudaStream_t s) {
     prof_before("column_sum", s);

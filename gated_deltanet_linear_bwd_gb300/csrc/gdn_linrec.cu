@@ -11,7 +11,9 @@
 // Where channels and sequences are too few for the GPU, a cluster of S CTAs shares
 // a sequence: its CTAs take neighbouring tiles, each sends its tile's pair into
 // every other's shared memory, and each folds the pairs of the tiles before its own.
-// No CTA ever waits on global memory, and the order of every sum is fixed.
+// No CTA ever waits on global memory, and the order of every sum is fixed.  A cluster
+// has 8 CTAs at most; long sequences of few channels are instead cut into parts that are
+// walked twice, first for their pairs alone, then, the pairs joined, for the results.
 //
 // Bound by memory: 16 x (512 .. 8192) tokens x 4096 gated bf16 forward 269 us, 94% of
 // the measured copy rate; 4 x 4096 x 4096 backward 114 us, 87% (the gate's arithmetic
@@ -131,6 +133,10 @@ struct Shape {
     int N, D, groups;          // sequences, channels, channel groups
     int lanes_n;               // clusters that share a channel group's sequences
     int cluster;               // CTAs of a cluster
+    int parts;                 // parts a sequence is cut into (then cluster is 1)
+    float2 *pair;              // parts > 1: [N][parts][D] a part's pair, written by the first walk
+    float *start;              // parts > 1: [N][parts][D] the value before a part, for the second
+    int reduce;                // the first walk
     int *status;
     long long spin_limit;
 };
@@ -148,6 +154,17 @@ __device__ __forceinline__ void range(const Shape &s, int n, long long &bos, lon
     if (bad && threadIdx.x == 0) set_status(s.status, GDN_ERR_BAD_SEQLENS);
     bos = bad ? 0 : lo;
     len = bad ? 0 : hi - lo;
+}
+
+// Part `part` of a sequence, from its first token on (from its last, BACK); true if
+// tokens of the sequence lie before it.
+template <bool BACK>
+__device__ __forceinline__ bool cut(const Shape &s, int part, long long &bos, long long &len) {
+    const long long per = ((len + s.parts - 1) / s.parts + 127) / 128 * 128, off = min(part * per, len);
+    const long long mine = min(per, len - off), before = BACK ? len - off - mine : off;
+    bos += before;
+    len = mine;
+    return before > 0;
 }
 
 // Pairs (A and B of two channels) of a tile's warps, and of a round's tiles in the
@@ -184,6 +201,7 @@ struct Join {
     const Shape &s;
     float2 A, B;               // of the tile's warps before this one (clusters only)
     bool alive;                // no wait for pairs gave up
+    float2 product;            // of every decay so far (single CTAs only)
 
     // Past its barrier every warp of the CTA is done with the tile before.
     __device__ __forceinline__ void offer(int round, float2 a, float2 b) {
@@ -215,6 +233,7 @@ struct Join {
                 if (w == warp) before = carry;
                 const float4 q = p.warp[buf][w][lane];
                 carry = fma2(make_float2(q.x, q.y), carry, make_float2(q.z, q.w));
+                product = mul2(product, make_float2(q.x, q.y));
             }
             return before;
         }
@@ -250,6 +269,11 @@ __device__ __forceinline__ float2 load_state(const float *base, long long at, co
 __device__ __forceinline__ void store_state(float *base, long long at, const Place &p, float2 v) {
     if (p.in0) base[at] = v.x;
     if (p.in1) base[at + 1] = v.y;
+}
+
+__device__ __forceinline__ void store_pair(float2 *base, long long at, const Place &p, float2 A, float2 B) {
+    if (p.in0) base[at] = make_float2(A.x, B.x);
+    if (p.in1) base[at + 1] = make_float2(A.y, B.y);
 }
 
 // Two elements at p, which may be on no 4- or 8-byte boundary (PAIRS false) and of
@@ -311,14 +335,19 @@ __global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUt
     const float2 sc = GATED ? load_state(a.scale, at.ch, at) : both(0.f);
     if (at.size > 1) tc::cluster_sync();     // the others' barriers are ready
 
-    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true};
+    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true, both(1.f)};
     bool ok = true;                // no wait gave up
     int tiles = 0, issued = 0;     // tiles walked and asked for, over all sequences
-    for (int n = at.cluster / s.groups; n < s.N; n += s.lanes_n) {
+    for (int unit = at.cluster / s.groups; unit < s.N * s.parts; unit += s.lanes_n) {
+        const int n = unit / s.parts;
         long long bos, len;
         range(s, n, bos, len);
-        const long long step = (long long)at.size * kTile;
-        float2 carry = load_state(a.h0, (long long)n * s.D + at.ch, at);
+        if (s.parts > 1) cut<false>(s, unit - n * s.parts, bos, len);
+        const long long step = (long long)at.size * kTile, state = (long long)n * s.D + at.ch;
+        const long long part = (long long)unit * s.D + at.ch;
+        float2 carry = both(0.f);
+        if (!s.reduce) carry = s.parts > 1 ? load_state(s.start, part, at) : load_state(a.h0, state, at);
+        join.product = both(1.f);
         const int base = tiles;
         const int rounds = (int)((len + step - 1) / step);
         auto ask = [&](int round) {          // thread 0: tile `round` of this sequence
@@ -392,12 +421,16 @@ __global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUt
             scan(i, al, xv, A, B);
             join.offer(base + i, A, B);
             refill(i);
-            emit(i, al, xv, join.take(base + i, carry));
+            const float2 before = join.take(base + i, carry);
+            if (!s.reduce) emit(i, al, xv, before);
         }
         tiles += rounds;
         // the next sequence's first tiles go into stages that this one's last are read from
         __syncthreads();
-        if (a.ht && at.rank == 0 && at.warp == 0) store_state(a.ht, (long long)n * s.D + at.ch, at, carry);
+        if (at.rank == 0 && at.warp == 0) {
+            if (s.reduce) store_pair(s.pair, part, at, join.product, carry);
+            else if (a.ht && s.parts == 1) store_state(a.ht, state, at, carry);
+        }
     }
     if (at.size > 1) tc::cluster_sync();     // nor does a CTA go before the others are done
     if (TMA && threadIdx.x == 0 && !ok)      // nothing may land after the CTA has gone
@@ -441,24 +474,30 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
     float2 dscale = both(0.f);
     if (at.size > 1) tc::cluster_sync();     // the others' barriers are ready
 
-    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true};
+    Join<W> join{ring.pairs, at.warp, at.lane, at.rank, at.size, s, both(1.f), both(0.f), true, both(1.f)};
     bool ok = true;
     int tiles = 0, issued = 0;
-    for (int n = at.cluster / s.groups; n < s.N; n += s.lanes_n) {
+    const uint32_t bytes = s.reduce ? kBytes / 3 * 2 : kBytes;       // a pair needs no h
+    for (int unit = at.cluster / s.groups; unit < s.N * s.parts; unit += s.lanes_n) {
+        const int n = unit / s.parts;
         long long bos, len;
         range(s, n, bos, len);
+        const bool lead = s.parts > 1 && cut<true>(s, unit - n * s.parts, bos, len);
         const long long step = (long long)at.size * kTile, state = (long long)n * s.D + at.ch;
-        float2 carry = load_state(a.dht, state, at);
+        const long long part = (long long)unit * s.D + at.ch;
+        float2 carry = both(0.f);
+        if (!s.reduce) carry = s.parts > 1 ? load_state(s.start, part, at) : load_state(a.dht, state, at);
+        join.product = both(1.f);
         const float2 h0 = load_state(a.h0, state, at);
         const int base = tiles;
         const int rounds = (int)((len + step - 1) / step);
         auto ask = [&](int round) {
             const int st = (base + round) % STAGES;
             const int row = (int)(bos + len - kTile - (round * step + at.rank * kTile));
-            tc::mbar_arrive_expect_tx(&ring.full[st], kBytes);
+            tc::mbar_arrive_expect_tx(&ring.full[st], bytes);
             tc::tma_load_2d(&ring.tile[st][0], &map_dh, &ring.full[st], ch0, row);
             tc::tma_load_2d(&ring.tile[st][1], &map_g, &ring.full[st], ch0, row);
-            tc::tma_load_2d(&ring.tile[st][2], &map_h, &ring.full[st], ch0, row - 1);
+            if (!s.reduce) tc::tma_load_2d(&ring.tile[st][2], &map_h, &ring.full[st], ch0, row - 1);
             ++issued;
         };
         if (TMA && threadIdx.x == 0)
@@ -489,7 +528,7 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
                         const long long off = (long long)r * s.D;
                         dv[r] = in ? load2<T, false>(gd - off, at) : both(0.f);
                         gv[r] = in ? load2<T, false>(gg - off, at) : both(0.f);
-                        hv[r] = in && r < top ? load2<T, false>(gh - off - s.D, at) : both(0.f);
+                        hv[r] = in && !s.reduce && (lead || r < top) ? load2<T, false>(gh - off - s.D, at) : both(0.f);
                     }
                 }
 #pragma unroll
@@ -511,7 +550,7 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float2 hp = TMA ? cell(2, r) : hv[TMA ? 0 : r];
-                    if (!whole.value && r == top) hp = h0;     // before the first token is h0
+                    if (!whole.value && !lead && r == top) hp = h0;     // before the first token is h0
                     const float2 e = add2(TMA ? cell(0, r) : dv[TMA ? 0 : r], c);
                     c = mul2(al[r], e);
                     float2 dl = mul2(c, hp);
@@ -528,17 +567,21 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
                     dx -= s.D, dg -= s.D;
                 }
             };
-            if (rows == R && top >= R) second(std::true_type());
+            if (s.reduce) continue;
+            if (rows == R && (lead || top >= R)) second(std::true_type());
             else if (rows > 0) second(std::false_type());
         }
         __syncthreads();
-        if (a.dh0 && at.rank == 0 && at.warp == 0) store_state(a.dh0, state, at, carry);
+        if (at.rank == 0 && at.warp == 0) {
+            if (s.reduce) store_pair(s.pair, part, at, join.product, carry);
+            else if (a.dh0 && s.parts == 1) store_state(a.dh0, state, at, carry);
+        }
     }
     if (at.size > 1) tc::cluster_sync();
     if (TMA && threadIdx.x == 0 && !ok)
         for (int i = max(0, issued - STAGES); i < issued; ++i)
             tc::mbar_drain(&ring.full[i % STAGES], (i / STAGES) & 1);
-    if (GATED && a.partial) {                // the CTA's sum, its warps in order
+    if (GATED && a.partial && !s.reduce) {   // the CTA's sum, its warps in order
         float2 *sum = reinterpret_cast<float2 *>(ring.pairs.warp);
         sum[at.warp * 32 + at.lane] = mul2(dscale, both(-Gate<T, GATED>::kUnit));
         __syncthreads();
@@ -548,6 +591,23 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
             store_state(a.partial, ((long long)(at.cluster / s.groups) * at.size + at.rank) * s.D + at.ch, at, t);
         }
     }
+}
+
+// The parts' pairs joined: the value before each part, and after the last one.
+__global__ void __launch_bounds__(128) parts_kernel(const float2 *pair, float *start, const float *init,
+                                                    float *final, int N, int parts, int D) {
+    pdl_enter();
+    const long long i = blockIdx.x * 128ll + threadIdx.x;
+    if (i >= (long long)N * D) return;
+    const long long n = i / D, ch = i - n * D, at = n * parts * D + ch;
+    float v = init ? init[i] : 0.f;
+#pragma unroll 16
+    for (int k = 0; k < parts; ++k) {
+        const float2 q = pair[at + (long long)k * D];
+        start[at + (long long)k * D] = v;
+        v = q.x * v + q.y;
+    }
+    if (final) final[i] = v;
 }
 
 // One token: a channel per thread.
@@ -584,12 +644,28 @@ struct Tiles {
     static constexpr int kBwdWarps = 4, kBwdRows = kHalf ? 16 : 8, kBwdStages = 4;
 };
 
+constexpr int kSms = 152;          // of the GPU that the choices below are made for
+constexpr int kMaxParts = 128;
+
 // CTAs that share a sequence: doubled while the grid leaves slots of the GPU (two
 // CTAs per SM) empty and the sequences have a tile for each.
-int cluster_of(long long clusters, long long mean_len, int sms) {
+int cluster_of(long long clusters, long long mean_len) {
     int c = 1;
-    while (c < kMaxCluster && clusters * c <= sms && mean_len > (long long)c * 128) c *= 2;
+    while (c < kMaxCluster && clusters * c <= kSms && mean_len > (long long)c * 128) c *= 2;
     return c;
+}
+
+// Parts of a sequence, or 1: as many as fill the GPU, where the two walks' tiles, 1.8 us
+// each, and the two more launches, 8 us, are less than the cluster's rounds, 2.5 us each.
+// Gated bf16 forward / backward, us: 65536 x 64 114 / 190 in clusters, 39 / 45 in parts;
+// 65536 x 1024 156 / 257 and 121 / 162; 8192 x 64 18 / 30 and 25 / 34.
+int parts_of(long long clusters, int cluster, long long mean_len) {
+    if (cluster < kMaxCluster) return 1;
+    const long long parts = std::min<long long>({kMaxParts, 2 * kSms / clusters, mean_len / 256});
+    if (parts < 2) return 1;
+    const double rounds = (double)((mean_len + 128 * cluster - 1) / (128 * cluster));
+    const double tiles = 2.0 * (double)((mean_len / parts + 127) / 128);
+    return tiles * 1.8 + 8 < rounds * 2.5 ? (int)parts : 1;
 }
 
 gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
@@ -598,23 +674,34 @@ gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
         return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", dtype);
     if (packed && (B != 1 || N < 1))
         return fail(GDN_ERR_INVALID_ARG, "cu_seqlens needs B == 1 and N >= 1 (B=%d N=%d)", B, N);
-    if ((long long)B * T >= (1ll << 31) - (1 << 16) || (long long)(packed ? N : B) * D >= (1ll << 40))
+    if ((long long)B * T >= (1ll << 31) - (1 << 16) || D > (1 << 24) || (long long)(packed ? N : B) * D >= (1ll << 40))
         return fail(GDN_ERR_INVALID_ARG, "problem too large");
     return GDN_OK;
 }
 
-Shape shape_of(const int32_t *cu, int B, int T, int D, int N, const LayerDevice &dev) {
-    Shape s;
+Shape shape_of(const int32_t *cu, int B, int T, int D, int N) {
+    Shape s = {};
     s.cu = cu;
     s.T = T;
     s.N = cu ? N : B;
     s.D = D;
     s.groups = (D + kChannels - 1) / kChannels;
+    const long long mean = cu ? T / s.N : T;
     s.lanes_n = group_lanes(s.N, s.groups);
-    s.cluster = cluster_of((long long)s.groups * s.lanes_n, cu ? T / s.N : T, dev.sms);
-    s.status = dev.status;
-    s.spin_limit = dev.spin_limit;
+    s.cluster = cluster_of((long long)s.groups * s.lanes_n, mean);
+    s.parts = parts_of((long long)s.groups * s.lanes_n, s.cluster, mean);
+    if (s.parts > 1) {
+        s.cluster = 1;
+        s.lanes_n = group_lanes(s.N * s.parts, s.groups);
+    }
     return s;
+}
+
+// Workspace of the parts' pairs and starting values.
+size_t parts_bytes(const Shape &s) { return s.parts > 1 ? (size_t)s.N * s.parts * s.D * 12 : 0; }
+void place_parts(Shape &s, void *ws) {
+    s.pair = (float2 *)ws;
+    s.start = (float *)(s.pair + (size_t)s.N * s.parts * s.D);
 }
 
 // Rows that start on 16 bytes, as TMA wants them.
@@ -623,7 +710,7 @@ bool tma_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
 template <typename... KArgs, typename... Args>
 cudaError_t launch(const char *name, void (*kernel)(KArgs...), int warps, size_t smem, const Shape &s, cudaStream_t st,
                    const Args &...args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem((const void *)kernel, smem);
     if (e != cudaSuccess) return e;
     prof_before(name, st);
     e = launch_pdl_cluster(kernel, dim3((unsigned)((long long)s.groups * s.lanes_n * s.cluster)), dim3(32 * warps),
@@ -640,18 +727,38 @@ cudaError_t map_of(CUtensorMap *m, const void *base, const Shape &s, int rows) {
     return tokens == 0 ? cudaSuccess : tc::make_map_rows(m, base, tokens, s.D, sizeof(T), kChannels, rows);
 }
 
+// A walk, or with parts the walk for their pairs, their joining and the walk for the results.
+template <typename Walk>
+cudaError_t in_parts(Shape s, const float *init, float *final, cudaStream_t q, Walk walk) {
+    if (s.parts == 1) return walk(s);
+    s.reduce = 1;
+    cudaError_t e = walk(s);
+    if (e != cudaSuccess) return e;
+    prof_before("linrec_parts", q);
+    e = launch_pdl(parts_kernel, dim3((unsigned)(((long long)s.N * s.D + 127) / 128)), dim3(128), 0, q,
+                   (const float2 *)s.pair, s.start, init, final, s.N, s.parts, s.D);
+    prof_after(q);
+    if (e != cudaSuccess) return e;
+    s.reduce = 0;
+    return walk(s);
+}
+
 template <typename T, bool GATED>
 cudaError_t run_fwd(const FwdArgs &f, const Shape &s, bool tma, cudaStream_t q) {
     constexpr int W = Tiles<T>::kFwdWarps, R = Tiles<T>::kFwdRows, S = Tiles<T>::kFwdStages;
     CUtensorMap mx = {}, mg = {};
     if (!tma)
-        return launch("linrec_fwd_plain", fwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 2, 1>),
-                      s, q, mx, mg, f);
+        return in_parts(s, f.h0, f.ht, q, [&](const Shape &w) {
+            return launch("linrec_fwd_plain", fwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 2, 1>),
+                          w, q, mx, mg, f);
+        });
     cudaError_t e = tc::encoder();
     if (e == cudaSuccess) e = map_of<T>(&mx, f.x, s, W * R);
     if (e == cudaSuccess) e = map_of<T>(&mg, f.g, s, W * R);
     if (e != cudaSuccess) return e;
-    return launch("linrec_fwd", fwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 2, S>), s, q, mx, mg, f);
+    return in_parts(s, f.h0, f.ht, q, [&](const Shape &w) {
+        return launch("linrec_fwd", fwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 2, S>), w, q, mx, mg, f);
+    });
 }
 
 template <typename T, bool GATED>
@@ -659,24 +766,32 @@ cudaError_t run_bwd(const BwdArgs &b, const Shape &s, bool tma, cudaStream_t q) 
     constexpr int W = Tiles<T>::kBwdWarps, R = Tiles<T>::kBwdRows, S = Tiles<T>::kBwdStages;
     CUtensorMap md = {}, mg = {}, mh = {};
     if (!tma)
-        return launch("linrec_bwd_plain", bwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 3, 1>),
-                      s, q, md, mg, mh, b);
+        return in_parts(s, b.dht, b.dh0, q, [&](const Shape &w) {
+            return launch("linrec_bwd_plain", bwd_kernel<T, GATED, 8, 8, 1, false>, 8, sizeof(Ring<T, 8, 8, 3, 1>),
+                          w, q, md, mg, mh, b);
+        });
     cudaError_t e = tc::encoder();
     if (e == cudaSuccess) e = map_of<T>(&md, b.dh, s, W * R);
     if (e == cudaSuccess) e = map_of<T>(&mg, b.g, s, W * R);
     if (e == cudaSuccess) e = map_of<T>(&mh, b.h, s, W * R);
     if (e != cudaSuccess) return e;
-    return launch("linrec_bwd", bwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 3, S>), s, q,
-                  md, mg, mh, b);
+    return in_parts(s, b.dht, b.dh0, q, [&](const Shape &w) {
+        return launch("linrec_bwd", bwd_kernel<T, GATED, W, R, S, true>, W, sizeof(Ring<T, W, R, 3, S>), w, q,
+                      md, mg, mh, b);
+    });
 }
 
+// The answer to a workspace query: 256 stands for none.
+size_t asked_for(size_t need) { return need == 0 ? 256 : std::max<size_t>(512, need); }
+
+// Workspace: parts, then a row of d(gate_scale) for each CTA of a channel group.
+size_t fwd_workspace(const gdn_linrec_fwd_args *a) {
+    return parts_bytes(shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N));
+}
 size_t bwd_workspace(const gdn_linrec_bwd_args *a) {
-    if (!a->gate_scale || !a->d_gate_scale) return 256;
-    // asked for without a device: sized for the largest cluster
-    LayerDevice any;
-    any.sms = 1 << 20;
-    const Shape s = shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, any);
-    return std::max<size_t>(256, (size_t)s.lanes_n * s.cluster * s.D * sizeof(float));
+    const Shape s = shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    const bool sums = a->gate_scale && a->d_gate_scale;
+    return parts_bytes(s) + (sums ? (size_t)s.lanes_n * s.cluster * s.D * sizeof(float) : 0);
 }
 
 }  // namespace
@@ -687,7 +802,16 @@ using namespace gdn;
 
 extern "C" {
 
-gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *a, void *stream) {
+size_t gdn_linrec_fwd_workspace_size(const gdn_linrec_fwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (linrec::check(a->B, a->T, a->D, a->N, a->dtype, a->cu_seqlens != nullptr) != GDN_OK) return 0;
+    return linrec::asked_for(linrec::fwd_workspace(a));
+}
+
+gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *a, void *ws, size_t ws_bytes, void *stream) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     gdn_status st = linrec::check(a->B, a->T, a->D, a->N, a->dtype, a->cu_seqlens != nullptr);
     if (st != GDN_OK) return st;
@@ -696,9 +820,15 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *a, void *stream) {
     if (misaligned(a->x) || misaligned(a->g) || misaligned(a->h) || misaligned(a->gate_scale) ||
         misaligned(a->initial_state) || misaligned(a->cu_seqlens) || misaligned(a->final_state))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    const size_t need = linrec::fwd_workspace(a);
+    if (need > 0 && (!ws || misaligned(ws) || ws_bytes < need))
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, dev);
+    linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    s.status = dev.status;
+    s.spin_limit = dev.spin_limit;
+    linrec::place_parts(s, ws);
     const bool tma = linrec::tma_rows(a->dtype, a->D), bf = a->dtype == GDN_BF16;
     const bool gated = a->gate_scale != nullptr;
     const linrec::FwdArgs f{a->x, a->g, a->gate_scale, a->initial_state, a->h, a->final_state};
@@ -716,7 +846,7 @@ size_t gdn_linrec_bwd_workspace_size(const gdn_linrec_bwd_args *a) {
         return 0;
     }
     if (linrec::check(a->B, a->T, a->D, a->N, a->dtype, a->cu_seqlens != nullptr) != GDN_OK) return 0;
-    return linrec::bwd_workspace(a);
+    return linrec::asked_for(linrec::bwd_workspace(a));
 }
 
 gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -731,23 +861,25 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_byte
         misaligned(a->d_gate_scale))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
     const bool gated = a->gate_scale != nullptr, sums = gated && a->d_gate_scale;
-    if (sums && (!ws || misaligned(ws) || ws_bytes < linrec::bwd_workspace(a)))
-        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0,
-                    linrec::bwd_workspace(a));
+    const size_t need = linrec::bwd_workspace(a);
+    if (need > 0 && (!ws || misaligned(ws) || ws_bytes < need))
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    const linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N, dev);
+    linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    s.status = dev.status;
+    s.spin_limit = dev.spin_limit;
+    linrec::place_parts(s, ws);
+    float *partial = sums ? (float *)((char *)ws + linrec::parts_bytes(s)) : nullptr;
     const bool tma = linrec::tma_rows(a->dtype, a->D), bf = a->dtype == GDN_BF16;
     const linrec::BwdArgs b{a->d_h, a->g, a->h, a->gate_scale, a->initial_state, a->d_final_state,
-                            a->dx, a->dg, a->d_initial_state, sums ? (float *)ws : nullptr};
+                            a->dx, a->dg, a->d_initial_state, partial};
     cudaStream_t q = (cudaStream_t)stream;
     cudaError_t e = bf ? (gated ? linrec::run_bwd<__nv_bfloat16, true>(b, s, tma, q)
                                 : linrec::run_bwd<__nv_bfloat16, false>(b, s, tma, q))
                        : (gated ? linrec::run_bwd<float, true>(b, s, tma, q)
                                 : linrec::run_bwd<float, false>(b, s, tma, q));
-    if (e == cudaSuccess && sums) {
-        e = column_sum((const float *)ws, s.lanes_n * s.cluster, a->D, a->d_gate_scale, q);
-    }
+    if (e == cudaSuccess && sums) e = column_sum(partial, s.lanes_n * s.cluster, a->D, a->d_gate_scale, q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear recurrence backward launch");
 }
 

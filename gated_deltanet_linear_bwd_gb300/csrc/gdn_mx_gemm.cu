@@ -468,7 +468,7 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
         return cuda_fail(e, "tensor map of a product");
     const size_t smem = kPairStages * pair_stage_bytes<FP4>() + 2 * kPairOut + 1024;
     auto k = gemm_pair_kernel<FP4, TO>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    if ((e = allow_smem((const void *)k, smem)) != cudaSuccess)
         return cuda_fail(e, "shared memory of the product");
     const int pairs = (int)std::min<long long>((long long)g.m_tiles * g.n_tiles, dev.sms / 2);
     prof_before("mx_gemm_pair", q);
@@ -540,7 +540,7 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w
         return cuda_fail(e, "tensor map of an operand");
     const size_t smem = std::max(g.stages * g.stage_bytes, g.nt * kFeat * 4) + 1024;
     auto k = fp4 ? gemm_kernel<true> : gemm_kernel<false>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    if ((e = allow_smem((const void *)k, smem)) != cudaSuccess)
         return cuda_fail(e, "shared memory of the product");
     const long long ctas = tiles * splits;
     if (ctas >= (1ll << 31)) return fail(GDN_ERR_INVALID_ARG, "problem too large");

@@ -36,6 +36,16 @@ def _first(name, t):
     return t.dtype, index
 
 
+def _with_workspace(name, args, dev, index):
+    """A call with the workspace it asks for (at most 256 bytes: none)."""
+    n = _abi_layer.workspace_size(name, args)
+    if n <= 256:
+        _abi_layer.call_ws(name, args, 0, 0, _raw_stream(index))
+        return
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _abi_layer.call_ws(name, args, ws.data_ptr(), n, _raw_stream(index))
+
+
 # ------------------------------------------------------------------ gated linear recurrence
 def _recurrence(name, src, g, initial_state, cu_seqlens, gate_scale):
     """Checks what the forward and backward share: (dtype, device index, B, T, D, N)."""
@@ -66,9 +76,9 @@ def gated_linear_recurrence_fwd(x, g, initial_state=None, cu_seqlens=None, gate_
     dtype, index, B, T, D, N = _recurrence("x", x, g, initial_state, cu_seqlens, gate_scale)
     h = torch.empty_like(x)
     ht = torch.empty((N, D), dtype=torch.float32, device=x.device) if output_final_state else None
-    _abi_layer.call("gdn_linrec_fwd", _abi_layer.gdn_linrec_fwd_args(
+    _with_workspace("gdn_linrec_fwd", _abi_layer.gdn_linrec_fwd_args(
         x.data_ptr(), g.data_ptr(), _ptr(gate_scale), _ptr(initial_state), _ptr(cu_seqlens), B, T, D,
-        N, _DT[dtype], h.data_ptr(), _ptr(ht)), _raw_stream(index))
+        N, _DT[dtype], h.data_ptr(), _ptr(ht)), x.device, index)
     return h, ht
 
 
@@ -89,13 +99,8 @@ def gated_linear_recurrence_bwd(dh, g, h, dht=None, initial_state=None, cu_seqle
         dh.data_ptr(), g.data_ptr(), h.data_ptr(), _ptr(gate_scale), _ptr(initial_state),
         _ptr(cu_seqlens), _ptr(dht), B, T, D, N, _DT[dtype], dx.data_ptr(), dg.data_ptr(), _ptr(dh0),
         _ptr(ds))
-    if ds is None:
-        _abi_layer.call_ws("gdn_linrec_bwd", a, 0, 0, _raw_stream(index))
-        return dx, dg, dh0
-    n = _abi_layer.workspace_size("gdn_linrec_bwd", a)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _abi_layer.call_ws("gdn_linrec_bwd", a, ws.data_ptr(), n, _raw_stream(index))
-    return dx, dg, dh0, ds
+    _with_workspace("gdn_linrec_bwd", a, dev, index)
+    return (dx, dg, dh0) if ds is None else (dx, dg, dh0, ds)
 
 
 class _GatedLinearRecurrence(torch.autograd.Function):

@@ -71,8 +71,11 @@ typedef struct gdn_linrec_step_args {
     float *out_state;           /* [N, D]: may be `state` itself                     */
 } gdn_linrec_step_args;
 
-gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *args, void *stream);
-/* Bytes of workspace for these arguments: 256 at least, 0 when they are invalid. */
+/* Bytes of workspace for these arguments: 256 (then none is read, and it may be NULL) or
+ * more, 0 when the arguments are invalid. */
+size_t gdn_linrec_fwd_workspace_size(const gdn_linrec_fwd_args *args);
+gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *args, void *workspace,
+                          size_t workspace_bytes, void *stream);
 size_t gdn_linrec_bwd_workspace_size(const gdn_linrec_bwd_args *args);
 gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *args, void *workspace,
                           size_t workspace_bytes, void *stream);

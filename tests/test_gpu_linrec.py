@@ -128,6 +128,8 @@ CASES = [
     (1, 129, 130, None), (1, 1000, 33, None), (2, 2500, 256, None), (1, 9001, 40, None),
     (0, 0, 96, [5, 0, 300, 1, 0]), (0, 0, 45, [0, 0, 700]), (0, 0, 512, [1] * 40),
     (0, 0, 64, [0]), (0, 0, 2, [3000, 4, 129]),
+    # long enough to be cut into parts: TMA rows, plain ones, packed with short and empty ones beside
+    (1, 40000, 64, None), (2, 30001, 24, None), (1, 33000, 9, None), (0, 0, 32, [50000, 0, 100, 20, 40000]),
 ]
 
 
