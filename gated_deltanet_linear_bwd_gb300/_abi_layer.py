@@ -1,6 +1,7 @@
 """ctypes binding of the layer operators in libgdn.so (include/gdn_layer.h).
 Argument marshalling only; the names mirror the C entry points."""
 import ctypes
+import struct
 
 from . import _abi
 from ._abi import GDN_ERR_INVALID_ARG, GDN_OK, GdnError, _f32, _i32, _vp
@@ -66,42 +67,50 @@ STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
 EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \
     tuple(n + "_workspace_size" for n in _WITH_WORKSPACE) + ("gdn_mx_scale_bytes",)
 
-_functions = {}
+
+
+class Entry:
+    """A C entry point.  Its argument struct is packed straight to bytes in the struct's
+    own layout (half the time of filling a ctypes.Structure, which a decode step notices):
+    `pack` takes the fields in order, addresses as integers (0 for NULL)."""
+    _CODES = {_vp: "P", _i32: "i", _f32: "f"}
+
+    def __init__(self, name, fields):
+        self.name = name
+        self.pack = struct.Struct("@" + "".join(self._CODES[t] for _, t in fields)).pack
+        self._call = self._size = None
+
+    def bind(self, lib, with_workspace):
+        f = getattr(lib, self.name)
+        f.restype = _i32
+        f.argtypes = [ctypes.c_char_p] + ([_vp, ctypes.c_size_t] if with_workspace else []) + [_vp]
+        self._call = f
+        if with_workspace:
+            self._size = getattr(lib, self.name + "_workspace_size")
+            self._size.restype, self._size.argtypes = ctypes.c_size_t, [ctypes.c_char_p]
+
+    def __call__(self, *args):
+        """(packed arguments, [workspace address, bytes,] stream)"""
+        rc = self._call(*args)
+        if rc != GDN_OK:
+            raise GdnError(self.name, rc)
+
+    def workspace_size(self, packed):
+        n = self._size(packed)
+        if n == 0:
+            raise GdnError(self.name + "_workspace_size", GDN_ERR_INVALID_ARG)
+        return n
+
+
+ENTRIES = {name: Entry(name, args._fields_) for name, args in {**_PLAIN, **_WITH_WORKSPACE}.items()}
 
 
 def load():
     """libgdn.so with the signatures of gdn_layer.h declared."""
     lib = _abi.load()
-    if not _functions:
-        p = ctypes.POINTER
-        for name, args in _PLAIN.items():
-            f = getattr(lib, name)
-            f.restype, f.argtypes = _i32, [p(args), _vp]
-        for name, args in _WITH_WORKSPACE.items():
-            f = getattr(lib, name)
-            f.restype, f.argtypes = _i32, [p(args), _vp, ctypes.c_size_t, _vp]
-            f = getattr(lib, name + "_workspace_size")
-            f.restype, f.argtypes = ctypes.c_size_t, [p(args)]
+    if lib.gdn_mx_scale_bytes.argtypes is None:
+        for name, entry in ENTRIES.items():
+            entry.bind(lib, name in _WITH_WORKSPACE)
         lib.gdn_mx_scale_bytes.restype = ctypes.c_size_t
         lib.gdn_mx_scale_bytes.argtypes = [_i32, _i32]
-        _functions.update((name, getattr(lib, name)) for name in EXPORTS)
     return lib
-
-
-def call(name: str, args, stream: int) -> None:
-    rc = _functions[name](ctypes.byref(args), stream)
-    if rc != GDN_OK:
-        raise GdnError(name, rc)
-
-
-def call_ws(name: str, args, workspace: int, ws_bytes: int, stream: int) -> None:
-    rc = _functions[name](ctypes.byref(args), workspace, ws_bytes, stream)
-    if rc != GDN_OK:
-        raise GdnError(name, rc)
-
-
-def workspace_size(name: str, args) -> int:
-    n = int(_functions[name + "_workspace_size"](ctypes.byref(args)))
-    if n == 0:
-        raise GdnError(name + "_workspace_size", GDN_ERR_INVALID_ARG)
-    return n

@@ -60,15 +60,26 @@ OK = dict(
 )
 
 
-def call(abi, name, **kw):
-    cls = getattr(abi, name + "_args")
-    a = cls()
+def raw(abi, name, **kw):
+    a = getattr(abi, name + "_args")()
     for k, v in {**OK[name], **kw}.items():
         setattr(a, k, v)
+    return bytes(a)
+
+
+def call(abi, name, **kw):
+    args = raw(abi, name, **kw)
     f = getattr(abi.load(), name)
-    if name + "_workspace_size" in abi.EXPORTS:
-        return f(ctypes.byref(a), 4096, 1 << 40, None)
-    return f(ctypes.byref(a), None)
+    return f(args, 4096, 1 << 40, None) if name + "_workspace_size" in abi.EXPORTS else f(args, None)
+
+
+@pytest.mark.parametrize("name", sorted(OK))
+def test_packed_arguments_are_the_structs_bytes(abi, name):
+    cls = getattr(abi, name + "_args")
+    values = [0.5 if t is ctypes.c_float else 1 + i for i, (_, t) in enumerate(cls._fields_)]
+    packed = abi.ENTRIES[name].pack(*values)
+    a = cls.from_buffer_copy(packed.ljust(ctypes.sizeof(cls), b"\0"))
+    assert [getattr(a, f) for f, _ in cls._fields_] == values
 
 
 @pytest.mark.parametrize("name, bad, rc, msg", [
@@ -115,16 +126,17 @@ def test_null_arguments_and_small_workspaces(abi):
         f = getattr(lib, name)
         rc = f(None, None, 0, None) if name + "_workspace_size" in abi.EXPORTS else f(None, None)
         assert rc == 1
-    a = abi.gdn_rms_norm_bwd_args()
-    for k, v in OK["gdn_rms_norm_bwd"].items():
-        setattr(a, k, v)
-    need = abi.workspace_size("gdn_rms_norm_bwd", a)
+    a = raw(abi, "gdn_rms_norm_bwd")
+    need = abi.ENTRIES["gdn_rms_norm_bwd"].workspace_size(a)
     assert need >= 256
-    assert lib.gdn_rms_norm_bwd(ctypes.byref(a), 4096, need - 1, None) == 3
-    b = abi.gdn_linrec_bwd_args()
-    for k, v in dict(OK["gdn_linrec_bwd"], gate_scale=4096, d_gate_scale=4096).items():
-        setattr(b, k, v)
-    assert lib.gdn_linrec_bwd(ctypes.byref(b), None, 0, None) == 3
+    assert lib.gdn_rms_norm_bwd(a, 4096, need - 1, None) == 3
+    for name, kw in (("gdn_linrec_bwd", dict(gate_scale=4096, d_gate_scale=4096)),
+                     ("gdn_linrec_fwd", dict(B=1, T=60000)), ("gdn_mx_linear", {})):
+        a = raw(abi, name, **kw)
+        need = abi.ENTRIES[name].workspace_size(a)
+        assert need > 256 or name == "gdn_mx_linear"
+        f = getattr(lib, name)
+        assert f(a, None, 0, None) == 3 and f(a, 4096, need - 1, None) == 3 and f(a, 4100, need, None) == 3
 
 
 def test_empty_problems_are_host_side_no_ops(abi):

@@ -182,10 +182,11 @@ def test_refusals():
     x = draw(8, 64, 1)
     a8, a4 = q(x, "mxfp8"), q(x, "mxfp4")
     other = q(draw(8, 96, 1), "mxfp8")
-    broken = lib().MxTensor(a8.data, a8.scales.flatten()[:100], "mxfp8", (8, 64))
     for bad in (lambda: q(x.cpu()), lambda: q(x, "int4"), lambda: q(x[:, :40].contiguous()),
                 lambda: q(x[:, ::2]), lambda: q(x.half()), lambda: mm(a8, a4), lambda: mm(a8, other),
-                lambda: mm(x, a8), lambda: mm(a8, broken), lambda: mm(a8, a8, torch.float16),
+                lambda: mm(x, a8), lambda: lib().MxTensor(a8.data, a8.scales.flatten()[:100], "mxfp8", (8, 64)),
+                lambda: lib().MxTensor(a8.data, a8.scales, "mxfp4", (8, 64)),
+                lambda: lib().mx_from_parts(a8.data, torch.zeros(8, 3, dtype=torch.uint8, device="cuda"), "mxfp8"), lambda: mm(a8, a8, torch.float16),
                 lambda: lib().mx_linear(x, other), lambda: lib().mx_dequantize(a8, torch.float16)):
         with pytest.raises(ValueError):
             bad()
