@@ -610,19 +610,74 @@ __global__ void __launch_bounds__(128) parts_kernel(const float2 *pair, float *s
     if (final) final[i] = v;
 }
 
-// One token: a channel per thread.
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) step_kernel(const T *x, const T *g, const float *scale,
-                                                   const float *state, T *h, float *out,
-                                                   long long total, int D) {
-    pdl_enter();
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        float sp;
-        const float a = Gate<float, GATED>::decay(to_f(g[i]), GATED ? scale[i % D] : 0.f, sp);
-        const float v = a * state[i] + to_f(x[i]);
-        out[i] = v;
-        from_f(h + i, v);
+// One token: VEC neighbouring channels to a thread, which takes the same ones of every
+// gridDim.y-th group of blockDim.y sequences.
+template <typename T, int VEC>
+struct Few;
+template <>
+struct Few<__nv_bfloat16, 4> {
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *v) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(p);
+        const float2 a = get2(r.x), b = get2(r.y);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(put2(make_float2(v[0], v[1]), p), put2(make_float2(v[2], v[3]), p));
+    }
+};
+template <>
+struct Few<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float *v) {
+        const float4 r = *reinterpret_cast<const float4 *>(p);
+        v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float *v) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <typename T>
+struct Few<T, 1> {
+    static __device__ __forceinline__ void load(const T *p, float *v) { v[0] = to_f(*p); }
+    static __device__ __forceinline__ void store(T *p, const float *v) { from_f(p, v[0]); }
+};
+
+template <typename T, bool GATED, int VEC>
+__global__ void __launch_bounds__(256) step_kernel(const T *x, const T *g, const float *scale,
+                                                   const float *state, T *h, float *out, int N, int D) {
+    pdl_enter();
+    const int ch = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    if (ch >= D) return;
+    float s[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[j] = 0.f;
+    if (GATED) Few<float, VEC>::load(scale + ch, s);
+    for (int n = blockIdx.y * blockDim.y + threadIdx.y; n < N; n += gridDim.y * blockDim.y) {
+        const long long at = (long long)n * D + ch;
+        float xv[VEC], gv[VEC], v[VEC];
+        Few<T, VEC>::load(x + at, xv);
+        Few<T, VEC>::load(g + at, gv);
+        Few<float, VEC>::load(state + at, v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            float sp;
+            v[j] = Gate<float, GATED>::decay(gv[j], s[j], sp) * v[j] + xv[j];
+        }
+        Few<float, VEC>::store(out + at, v);
+        Few<T, VEC>::store(h + at, v);
+    }
+}
+
+template <typename T, bool GATED>
+cudaError_t run_step(const gdn_linrec_step_args *a, int sms, cudaStream_t q) {
+    // rows that start on 16 bytes are read by fours
+    const int vec = a->D % 4 == 0 ? 4 : 1, chunks = a->D / vec;
+    int wide = 1;
+    while (wide < 256 && wide < chunks) wide *= 2;
+    const dim3 block(wide, 256 / wide);
+    const int across = (chunks + wide - 1) / wide;
+    const int down = (int)std::min<long long>((a->N + block.y - 1) / block.y, std::max(1, 16 * sms / across));
+    return launch_pdl(vec == 4 ? step_kernel<T, GATED, 4> : step_kernel<T, GATED, 1>, dim3(across, down), block, 0, q,
+                      (const T *)a->x, (const T *)a->g, a->gate_scale, a->state, (T *)a->h, a->out_state, a->N, a->D);
 }
 
 // Clusters that share a channel group's sequences: one each, but no more than fill
@@ -886,6 +941,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_byte
 gdn_status gdn_linrec_step(const gdn_linrec_step_args *a, void *stream) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->N < 0 || a->D < 1) return fail(GDN_ERR_INVALID_ARG, "bad sizes N=%d D=%d", a->N, a->D);
+    if (a->D > (1 << 24) || a->N > (1 << 30)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
     if (a->dtype != GDN_FP32 && a->dtype != GDN_BF16)
         return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", a->dtype);
     if (a->N == 0) return GDN_OK;
@@ -897,22 +953,14 @@ gdn_status gdn_linrec_step(const gdn_linrec_step_args *a, void *stream) {
     LayerDevice dev;
     const gdn_status st = layer_device(&dev);
     if (st != GDN_OK) return st;
-    const long long total = (long long)a->N * a->D;
-    const unsigned grid = (unsigned)std::min<long long>((total + 255) / 256, 8ll * dev.sms);
     cudaStream_t q = (cudaStream_t)stream;
     prof_before("linrec_step", q);
-    cudaError_t e;
-    if (a->dtype == GDN_BF16) {
-        auto k = a->gate_scale ? linrec::step_kernel<__nv_bfloat16, true>
-                               : linrec::step_kernel<__nv_bfloat16, false>;
-        e = launch_pdl(k, dim3(grid), dim3(256), 0, q, (const __nv_bfloat16 *)a->x,
-                       (const __nv_bfloat16 *)a->g, a->gate_scale, a->state, (__nv_bfloat16 *)a->h,
-                       a->out_state, total, a->D);
-    } else {
-        auto k = a->gate_scale ? linrec::step_kernel<float, true> : linrec::step_kernel<float, false>;
-        e = launch_pdl(k, dim3(grid), dim3(256), 0, q, (const float *)a->x, (const float *)a->g,
-                       a->gate_scale, a->state, (float *)a->h, a->out_state, total, a->D);
-    }
+    const bool gated = a->gate_scale != nullptr;
+    const cudaError_t e = a->dtype == GDN_BF16
+                              ? (gated ? linrec::run_step<__nv_bfloat16, true>(a, dev.sms, q)
+                                       : linrec::run_step<__nv_bfloat16, false>(a, dev.sms, q))
+                              : (gated ? linrec::run_step<float, true>(a, dev.sms, q)
+                                       : linrec::run_step<float, false>(a, dev.sms, q));
     prof_after(q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "linear recurrence step launch");
 }
