@@ -92,12 +92,20 @@ __device__ __forceinline__ void store_chunk(void *base, long long at, const floa
 __device__ __forceinline__ float row_sum(float x, int tpr, float *red) {
     for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (tpr <= 32) return x;
-    const int warp = threadIdx.x >> 5, per = tpr >> 5;
-    if ((threadIdx.x & 31) == 0) red[warp] = x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = tpr >> 5;      // a power of two
+    if (lane == 0) red[warp] = x;
     __syncthreads();
-    x = 0.f;
-    for (int w = warp / per * per, e = w + per; w < e; ++w) x += red[w];
+    x = red[(warp & ~(per - 1)) + (lane & (per - 1))];
+    for (int o = per >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// The larger magnitude, or NaN if there is one.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
 struct FwdArgs {
@@ -105,7 +113,7 @@ struct FwdArgs {
     void *y, *sum;
     uint8_t *scales;
     float *rstd;
-    float eps;
+    float eps, inv_d;
     int rows, D, tpr, ktiles;
 };
 
@@ -123,51 +131,56 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(FwdArgs a) {
     w.load(a.w, 0, tid, a.tpr, a.D, true);
     // with MX scales the last tile's rows past the end are walked too: their scales are zeros
     const long long last = MX ? (a.rows + 127ll) / 128 * 128 : a.rows, step = (long long)gridDim.x * per_cta;
-    long long row = (long long)blockIdx.x * per_cta + group;
-    x.load(a.x, row * a.D, tid, a.tpr, a.D, row < a.rows);
-    if (a.res) r.load(a.res, row * a.D, tid, a.tpr, a.D, row < a.rows);
+    long long row = (long long)blockIdx.x * per_cta + group, base = row * a.D;
+    x.load(a.x, base, tid, a.tpr, a.D, row < a.rows);
+    if (a.res) r.load(a.res, base, tid, a.tpr, a.D, row < a.rows);
     int turn = 0;
-    for (; row - group < last; row += step, turn ^= 1) {
+    for (; row - group < last; row += step, base += step * a.D, turn ^= 1) {
         const bool live = row < a.rows;
-        const long long base = row * a.D;
-        float s[kPer], ss = 0.f;
+        // pairs of neighbouring columns (VEC 1: a column and one that is not there)
+        constexpr int P = VEC > 1 ? VEC / 2 : 1;
+        float2 s[NV][P], ss2 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int col = (v * a.tpr + tid) * VEC;
-            C::get(x.raw[v], s + v * VEC);
+            float *sv = reinterpret_cast<float *>(s[v]);
+            if (VEC == 1) s[v][0].y = 0.f;
+            C::get(x.raw[v], sv);
             if (a.res) {
-                float q[VEC];
-                C::get(r.raw[v], q);
+                float2 q[P];
+                if (VEC == 1) q[0].y = 0.f;
+                C::get(r.raw[v], reinterpret_cast<float *>(q));
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) s[v * VEC + i] += q[i];
-                if (live && col < a.D) store_chunk<T, VEC>(a.sum, base + col, s + v * VEC);
+                for (int i = 0; i < P; ++i) s[v][i] = __fadd2_rn(s[v][i], q[i]);
+                if (live && col < a.D) store_chunk<T, VEC>(a.sum, base + col, sv);
             }
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) ss += s[v * VEC + i] * s[v * VEC + i];
+            for (int i = 0; i < P; ++i) ss2 = __ffma2_rn(s[v][i], s[v][i], ss2);
         }
-        const long long next = row + step;
-        x.load(a.x, next * a.D, tid, a.tpr, a.D, next < a.rows);
-        if (a.res) r.load(a.res, next * a.D, tid, a.tpr, a.D, next < a.rows);
-        const float rstd = rsqrtf(row_sum(ss, a.tpr, red[turn]) / (float)a.D + a.eps);
+        x.load(a.x, base + step * a.D, tid, a.tpr, a.D, row + step < a.rows);
+        if (a.res) r.load(a.res, base + step * a.D, tid, a.tpr, a.D, row + step < a.rows);
+        const float rstd = rsqrtf(row_sum(ss2.x + ss2.y, a.tpr, red[turn]) * a.inv_d + a.eps);
         if (live && a.rstd && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int col = (v * a.tpr + tid) * VEC;
-            float y[VEC], g[VEC];
-            C::get(w.raw[v], g);
+            float2 y[P];
+            if (VEC == 1) y[0].y = 0.f;
+            C::get(w.raw[v], reinterpret_cast<float *>(y));
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = s[v * VEC + i] * rstd * g[i];
+            for (int i = 0; i < P; ++i) y[i] = __fmul2_rn(__fmul2_rn(s[v][i], both(rstd)), y[i]);
             if constexpr (!MX) {
-                if (live && col < a.D) store_chunk<T, VEC>(a.y, base + col, y);
+                if (live && col < a.D) store_chunk<T, VEC>(a.y, base + col, reinterpret_cast<float *>(y));
             } else {
                 // a block of 32 columns is 32 / VEC neighbouring lanes
-                uint32_t amax = 0;
+                float big = 0.f;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) amax = max(amax, mx::abs_bits(y[i]));
+                for (int i = 0; i < P; ++i) big = max_abs(max_abs(big, y[i].x), y[i].y);
+                uint32_t amax = mx::abs_bits(big);
 #pragma unroll
                 for (int o = 1; o < 32 / VEC; o <<= 1)
                     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const int byte = live && col < a.D ? mx::scale_byte<false>(amax) : 0;
+                const int byte = mx::scale_byte<false>(amax);        // 0 where nothing is
                 if (words) {
                     uint32_t word = (uint32_t)byte << (8 * (col / 32 & 3));
 #pragma unroll
@@ -179,15 +192,18 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(FwdArgs a) {
                     a.scales[mx::scale_offset(row, col / 32, a.ktiles)] = (uint8_t)byte;
                 }
                 if (live && col < a.D) {
-                    const float f = mx::scale_factor(byte);
+                    const float2 f = both(mx::scale_factor(byte));
+                    const bool bad = byte == 255;                    // the elements of a NaN block are zeros
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) y[i] = byte == 255 ? 0.f : y[i] * f;
+                    for (int i = 0; i < P; ++i) y[i] = __fmul2_rn(y[i], f);
                     uint32_t *o = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(a.y) + base + col);
-                    const uint32_t q0 = mx::e4m3x4(y[0], y[1], y[2], y[3]);
-                    if constexpr (VEC == 8)
-                        *reinterpret_cast<uint2 *>(o) = make_uint2(q0, mx::e4m3x4(y[4], y[5], y[6], y[7]));
-                    else
-                        *o = q0;
+                    const uint32_t q0 = mx::e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y);
+                    if constexpr (VEC == 8) {
+                        const uint32_t q1 = mx::e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y);
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(bad ? 0u : q0, bad ? 0u : q1);
+                    } else {
+                        *o = bad ? 0u : q0;
+                    }
                 }
             }
         }
@@ -199,6 +215,7 @@ struct BwdArgs {
     const float *rstd;
     void *ds;
     float *partial;                // [gridDim.x][D]
+    float inv_d;
     int rows, D, tpr;
 };
 
@@ -251,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
             }
         }
         fetch(row + step);
-        const float c = row_sum(dot, a.tpr, red[turn]) / (float)a.D;
+        const float c = row_sum(dot, a.tpr, red[turn]) * a.inv_d;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int col = (v * a.tpr + tid) * VEC;
@@ -350,7 +367,7 @@ gdn_status gdn_rms_norm_fwd(const gdn_rms_norm_fwd_args *a, void *stream) {
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     norm::FwdArgs f{a->x, a->residual, a->weight, a->y, a->sum, a->scales, a->rstd, a->eps,
-                    a->rows, a->D, norm::row_threads(a->D), (a->D + 127) / 128};
+                    1.f / (float)a->D, a->rows, a->D, norm::row_threads(a->D), (a->D + 127) / 128};
     const int threads = norm::cta_threads(f.tpr), per = threads / f.tpr;
     const long long rows = a->mx ? (a->rows + 127ll) / 128 * 128 : a->rows;
     const long long ctas = std::min<long long>((rows + per - 1) / per, (long long)dev.sms * (8 * 256 / threads));
@@ -394,7 +411,7 @@ gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *a, void *ws, size_t ws_
     const int ctas = norm::bwd_ctas(a->rows, a->D, std::min(dev.sms, norm::kMaxSms));
     const int tpr = norm::row_threads(a->D), threads = norm::cta_threads(tpr), per = threads / tpr;
     const norm::BwdArgs b{a->dy, a->sum, a->weight, a->d_sum, a->rstd, a->ds, (float *)ws,
-                          a->rows, a->D, tpr};
+                          1.f / (float)a->D, a->rows, a->D, tpr};
     const bool vec = norm::vector_rows(a->dtype, a->D);
     auto k = a->dtype == GDN_BF16
                  ? (vec ? norm::bwd_of<__nv_bfloat16, 8>(threads) : norm::bwd_of<__nv_bfloat16, 1>(threads))
