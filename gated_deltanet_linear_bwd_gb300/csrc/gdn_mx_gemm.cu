@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
 // last 64 of the one being the first 64 of the other, so that the epilogue of a tile
 // runs under the next one's MMAs once it has taken those 64.
 constexpr int kPairThreads = 224;                    // weights, MMA, four epilogue warps, tokens
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 6;
 constexpr int kPairAcc = 192;                        // column of the second accumulator
 constexpr int kPairScales = 448;                     // columns of the scales: two sets of 24
-constexpr int kPairOut = 16384;                      // a staged 128 x 128-byte block of C
+constexpr int kPairOut = 4096;                       // a warp's staged 32 x 128-byte block of C
 
 struct PairArgs {
     int M, N, K, kblocks, ktiles;
@@ -248,7 +248,7 @@ struct PairArgs {
 struct PairControl {
     uint64_t full[kPairStages], empty[kPairStages], acc_full, acc_free, done;
     uint32_t tmem;
-    int issued, failed;                              // failed: the epilogue's wait gave up
+    int issued;
 };
 
 template <bool FP4>
@@ -265,15 +265,18 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
     constexpr int kStage = pair_stage_bytes<FP4>();
     constexpr uint32_t kBytes = 32768u + 3u * 512u * kScaleTiles;    // of one CTA
     constexpr int kCols = 128 / (int)sizeof(TO);     // columns of a staged block
-    extern __shared__ uint8_t raw[];
-    __shared__ PairControl ctl;
-    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t ring[];
     uint8_t *stage_out = ring + kPairStages * kStage;
+    PairControl &ctl = *reinterpret_cast<PairControl *>(stage_out + 4 * kPairOut);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.m_tiles * a.n_tiles;
 
+    if (tc::smem_u32(ring) & 1023u) {                // the swizzle's unit; every CTA alike
+        if (threadIdx.x == 0) set_status(a.status, GDN_ERR_CUDA);
+        return;
+    }
     if (threadIdx.x == 32) {
         tc::prefetch_map(&map_x);
         tc::prefetch_map(&map_w);
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
         tc::mbar_init(&ctl.acc_full, 1);
         tc::mbar_init(&ctl.acc_free, 8);             // the epilogue warps of both CTAs
         tc::mbar_init(&ctl.done, 1);
-        ctl.issued = ctl.failed = 0;
+        ctl.issued = 0;
         tc::fence_barrier_init();
     }
     if (warp == 1) tc::tmem_alloc_pair(&ctl.tmem, 512);
@@ -383,17 +386,17 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
             tc::mma_commit_pair(&ctl.done);
         }
     } else {
-        // epilogue: 64 (bf16) or 32 (fp32) columns at a time through shared memory to a TMA store
-        const bool storer = warp == 2 && lane == 0;
+        // epilogue: each warp takes its 32 rows, 64 (bf16) or 32 (fp32) columns at a time,
+        // through a swizzled block of its own to a TMA store
         asm volatile("griddepcontrol.wait;" ::: "memory");   // C may be written
         const int quarter = warp & 3;
-        int t = 0, staged = 0;
+        uint8_t *buf = stage_out + quarter * kPairOut;
+        const uint32_t acc_free0 = tc::map_rank(tc::smem_u32(&ctl.acc_free), 0);
+        int t = 0;
         for (int tile = pair; tile < tiles; tile += pairs, ++t) {
-            if (!tc::mbar_wait(&ctl.acc_full, t & 1, a.spin_limit, a.status)) ctl.failed = 1;
-            tc::named_sync(1, 128);                  // the four warps go on, or stop, together
-            if (ctl.failed) break;
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_full, t & 1, a.spin_limit, a.status))) break;
             tc::tc_fence_after();
-            const int row = ((tile % a.m_tiles) * 2 + rank) * 128, feat = tile / a.m_tiles * 256;
+            const int row = ((tile % a.m_tiles) * 2 + rank) * 128 + 32 * quarter, feat = tile / a.m_tiles * 256;
             const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -404,33 +407,30 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
                 if (c == 0) {
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tc::smem_u32(&ctl.acc_free), 0));
+                    if (lane == 0) tc::mbar_arrive_cluster(acc_free0);
                 }
 #pragma unroll
-                for (int b = 0; b < 64 / kCols; ++b, ++staged) {
-                    uint8_t *buf = stage_out + (staged & 1) * kPairOut;
-                    if (storer) tc::bulk_wait_read_but_newest();   // the store before last has left this buffer
-                    tc::named_sync(1, 128);
+                for (int b = 0; b < 64 / kCols; ++b) {
+                    if (lane == 0) tc::bulk_wait_read();     // the store before has left the block
+                    __syncwarp();
                     if constexpr (sizeof(TO) == 2) {
-                        tc::st_row64(buf, 32 * quarter + lane, v);
+                        tc::st_row64(buf, lane, v);
                     } else {
-                        const int r = 32 * quarter + lane;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<float4 *>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
+                            *reinterpret_cast<float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4)) =
                                 make_float4(v[32 * b + 4 * k], v[32 * b + 4 * k + 1], v[32 * b + 4 * k + 2], v[32 * b + 4 * k + 3]);
                     }
                     tc::fence_proxy_async();
-                    tc::named_sync(1, 128);
-                    if (storer) {
-                        if (row < a.M && feat + col + b * kCols < a.N)
-                            tc::tma_store_2d(&map_c, buf, feat + col + b * kCols, row);
-                        tc::bulk_commit();           // a group for every block, as the waits count them
+                    __syncwarp();
+                    if (lane == 0 && row < a.M && feat + col + b * kCols < a.N) {
+                        tc::tma_store_2d(&map_c, buf, feat + col + b * kCols, row);
+                        tc::bulk_commit();
                     }
                 }
             }
         }
-        if (storer) tc::bulk_wait_read();
+        if (lane == 0) tc::bulk_wait_read();
         __syncwarp();
     }
     // every MMA done and every copy landed before TMEM is given back and a CTA goes
@@ -464,9 +464,9 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
         (e = tc::make_map_bytes(&mw, a->b, a->N, bytes, 128)) != cudaSuccess ||
         (e = tc::make_map_scales(&msx, a->a_scales, (a->M + 127) / 128, g.ktiles, st, 1)) != cudaSuccess ||
         (e = tc::make_map_scales(&msw, a->b_scales, (a->N + 127) / 128, g.ktiles, st, 2)) != cudaSuccess ||
-        (e = tc::make_map_rows(&mc, a->c, a->M, a->N, sizeof(TO), 128 / (int)sizeof(TO), 128, true)) != cudaSuccess)
+        (e = tc::make_map_rows(&mc, a->c, a->M, a->N, sizeof(TO), 128 / (int)sizeof(TO), 32, true)) != cudaSuccess)
         return cuda_fail(e, "tensor map of a product");
-    const size_t smem = kPairStages * pair_stage_bytes<FP4>() + 2 * kPairOut + 1024;
+    const size_t smem = kPairStages * pair_stage_bytes<FP4>() + 4 * kPairOut + sizeof(PairControl);
     auto k = gemm_pair_kernel<FP4, TO>;
     if ((e = allow_smem((const void *)k, smem)) != cudaSuccess)
         return cuda_fail(e, "shared memory of the product");
