@@ -1,11 +1,11 @@
 // gdn_norm.cu -- residual addition with the RMS norm, to the input's type or to
 // MXFP8 with its scales, and the backward pass.
 //
-// A row is held in registers, 16 elements to a thread, by `tpr` threads (a power
+// A row is held in registers, PER elements to a thread, by `tpr` threads (a power
 // of two): loaded once, reduced by shuffles (and through shared memory where a row
 // spans warps), scaled and written, while the next row's loads are in flight.  Rows of
 // few columns share a CTA.  Bound by memory: 32768 x 4096 bf16
-// with a residual to MXFP8 155 us, 90% of the measured copy rate (to bf16 162 us, 98%);
+// with a residual to MXFP8 151 us, 92% of the measured copy rate (to bf16 161 us, 98%);
 // backward of 16384 x 4096 89 us, 89%.
 #include <algorithm>
 
@@ -16,8 +16,7 @@ namespace gdn {
 namespace norm {
 namespace {
 
-constexpr int kPer = 16;           // elements of a row in one thread
-constexpr int kMaxD = 1024 * kPer;
+constexpr int kMaxD = 1024 * 16;
 
 // VEC elements of T as one 16-byte load (or one element where rows do not start
 // on 16 bytes).
@@ -65,10 +64,10 @@ struct Chunk<T, 1> {
 };
 
 // A thread's share of a row: NV chunks, chunk v at column (v tpr + tid) VEC.
-template <typename T, int VEC>
+template <typename T, int VEC, int PER>
 struct Share {
     using C = Chunk<T, VEC>;
-    static constexpr int NV = kPer / VEC;
+    static constexpr int NV = PER / VEC;
     typename C::Raw raw[NV];
     __device__ __forceinline__ void load(const void *base, long long at, int tid, int tpr, int D, bool live) {
 #pragma unroll
@@ -117,26 +116,30 @@ struct FwdArgs {
     int rows, D, tpr, ktiles;
 };
 
-template <typename T, int VEC, bool MX, int THREADS>
+template <typename T, int VEC, int PER, bool MX, int THREADS>
 __global__ void __launch_bounds__(THREADS) fwd_kernel(FwdArgs a) {
     using C = Chunk<T, VEC>;
-    constexpr int NV = kPer / VEC;
+    constexpr int NV = PER / VEC;
     __shared__ float red[2][32];
     pdl_enter();
 
     const int tid = threadIdx.x & (a.tpr - 1), per_cta = blockDim.x / a.tpr;
     const int group = threadIdx.x / a.tpr;
     const bool words = a.tpr >= 128 / VEC;           // a scale tile's four blocks are neighbouring lanes
-    Share<T, VEC> w, x, r;
+    Share<T, VEC, PER> w, x, r;
     w.load(a.w, 0, tid, a.tpr, a.D, true);
     // with MX scales the last tile's rows past the end are walked too: their scales are zeros
     const long long last = MX ? (a.rows + 127ll) / 128 * 128 : a.rows, step = (long long)gridDim.x * per_cta;
     long long row = (long long)blockIdx.x * per_cta + group, base = row * a.D;
-    x.load(a.x, base, tid, a.tpr, a.D, row < a.rows);
-    if (a.res) r.load(a.res, base, tid, a.tpr, a.D, row < a.rows);
+    auto fetch = [&](long long at, bool in) {
+        x.load(a.x, at, tid, a.tpr, a.D, in);
+        if (a.res) r.load(a.res, at, tid, a.tpr, a.D, in);
+    };
+    if (VEC > 1) fetch(base, row < a.rows);
     int turn = 0;
     for (; row - group < last; row += step, base += step * a.D, turn ^= 1) {
         const bool live = row < a.rows;
+        if (VEC == 1) fetch(base, live);
         // pairs of neighbouring columns (VEC 1: a column and one that is not there)
         constexpr int P = VEC > 1 ? VEC / 2 : 1;
         float2 s[NV][P], ss2 = both(0.f);
@@ -157,8 +160,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(FwdArgs a) {
 #pragma unroll
             for (int i = 0; i < P; ++i) ss2 = __ffma2_rn(s[v][i], s[v][i], ss2);
         }
-        x.load(a.x, base + step * a.D, tid, a.tpr, a.D, row + step < a.rows);
-        if (a.res) r.load(a.res, base + step * a.D, tid, a.tpr, a.D, row + step < a.rows);
+        if (VEC > 1) fetch(base + step * a.D, row + step < a.rows);
         const float rstd = rsqrtf(row_sum(ss2.x + ss2.y, a.tpr, red[turn]) * a.inv_d + a.eps);
         if (live && a.rstd && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -219,21 +221,21 @@ struct BwdArgs {
     int rows, D, tpr;
 };
 
-template <typename T, int VEC, int THREADS>
+template <typename T, int VEC, int PER, int THREADS>
 __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
     using C = Chunk<T, VEC>;
-    constexpr int NV = kPer / VEC;
+    constexpr int NV = PER / VEC;
     extern __shared__ float sums[];          // [rows per CTA][D], where a CTA holds several rows
     __shared__ float red[2][32];
     pdl_enter();
 
     const int tid = threadIdx.x & (a.tpr - 1), per_cta = blockDim.x / a.tpr;
     const int group = threadIdx.x / a.tpr;
-    Share<T, VEC> w, dy, s, up;
+    Share<T, VEC, PER> w, dy, s, up;
     w.load(a.w, 0, tid, a.tpr, a.D, true);
-    float dw[kPer];
+    float dw[PER];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) dw[i] = 0.f;
+    for (int i = 0; i < PER; ++i) dw[i] = 0.f;
     const long long step = (long long)gridDim.x * per_cta;
     long long row = (long long)blockIdx.x * per_cta + group;
     float rs;
@@ -244,14 +246,15 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
         if (a.dsum) up.load(a.dsum, at * a.D, tid, a.tpr, a.D, in);
         rs = in ? a.rstd[at] : 0.f;
     };
-    fetch(row);
+    if (VEC > 1) fetch(row);
     int turn = 0;
     for (; row - group < a.rows; row += step, turn ^= 1) {
         const bool live = row < a.rows;
+        if (VEC == 1) fetch(row);
         const long long base = row * a.D;
         const float rstd = rs;
-        float xh[kPer], wdy[kPer], dot = 0.f;
-        Share<T, VEC> dsum = up;
+        float xh[PER], wdy[PER], dot = 0.f;
+        Share<T, VEC, PER> dsum = up;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float g[VEC];
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
                 dot += wdy[k] * xh[k];
             }
         }
-        fetch(row + step);
+        if (VEC > 1) fetch(row + step);
         const float c = row_sum(dot, a.tpr, red[turn]) * a.inv_d;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -301,34 +304,49 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
     }
 }
 
-// Threads of a row: the least power of two that holds it, 16 elements each (8 at
-// least: two MX blocks of bf16 or one of fp32 in neighbouring lanes).
-int row_threads(int D) {
-    int t = 8;
-    while (t * kPer < D) t *= 2;
+// Whole 16-byte chunks in every row.
+bool vector_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
+
+// Elements to a thread: 16, or 8 of rows that are read one by one (a register each: with
+// 16, and the next row's on the way, one CTA fits an SM).  16000 x 4095 bf16 forward /
+// backward 148 / 211 us (142 / 255 with 16), 9224 x 7275 173 / 195 (168 / 490).
+int per_thread(int dtype, int D) { return vector_rows(dtype, D) || D > 8192 ? 16 : 8; }
+// Threads of a row: the least power of two that holds it; 8 with MX scales, so that a
+// scale tile's blocks have threads.
+int row_threads(int dtype, int D, bool mx) {
+    int t = mx ? 8 : 1;
+    while (t * per_thread(dtype, D) < D) t *= 2;
     return t;
 }
 int cta_threads(int tpr) { return std::max(tpr, 256); }
 
-// Whole 16-byte chunks in every row.
-bool vector_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
-
-// CTAs of the backward pass: as many as run at once (2 of 256 threads per SM), since
-// each leaves a row of partial sums of dweight.
-int bwd_ctas(int rows, int D, int sms) {
-    const int tpr = row_threads(D), threads = cta_threads(tpr), per = threads / tpr;
-    return std::max(1, std::min((rows + per - 1) / per, sms * std::max(1, 2 * 256 / threads)));
+// CTAs of the backward pass: as many as run at once (2 of 256 threads per SM, 3 where rows
+// are read one by one), since each leaves a row of partial sums of dweight.
+int bwd_ctas(int rows, int dtype, int D, int sms) {
+    const int tpr = row_threads(dtype, D, false), threads = cta_threads(tpr), per = threads / tpr;
+    return std::max(1, std::min((rows + per - 1) / per, sms * std::max(1, (vector_rows(dtype, D) ? 2 : 3) * 256 / threads)));
 }
 
-template <typename T, int VEC, bool MX>
+template <typename T, int VEC, int PER, bool MX>
 auto fwd_of(int threads) {
-    return threads <= 256   ? fwd_kernel<T, VEC, MX, 256>
-           : threads <= 512 ? fwd_kernel<T, VEC, MX, 512>
-                            : fwd_kernel<T, VEC, MX, 1024>;
+    return threads <= 256   ? fwd_kernel<T, VEC, PER, MX, 256>
+           : threads <= 512 ? fwd_kernel<T, VEC, PER, MX, 512>
+                            : fwd_kernel<T, VEC, PER, MX, 1024>;
 }
-template <typename T, int VEC>
+template <typename T, int VEC, int PER>
 auto bwd_of(int threads) {
-    return threads <= 256 ? bwd_kernel<T, VEC, 256> : threads <= 512 ? bwd_kernel<T, VEC, 512> : bwd_kernel<T, VEC, 1024>;
+    return threads <= 256   ? bwd_kernel<T, VEC, PER, 256>
+           : threads <= 512 ? bwd_kernel<T, VEC, PER, 512>
+                            : bwd_kernel<T, VEC, PER, 1024>;
+}
+// Rows read one by one; PER 16 has a row of over 8192 columns, hence 1024 threads.
+template <typename T>
+auto odd_fwd_of(int D, int threads) {
+    return D > 8192 ? fwd_kernel<T, 1, 16, false, 1024> : fwd_of<T, 1, 8, false>(threads);
+}
+template <typename T>
+auto odd_bwd_of(int D, int threads) {
+    return D > 8192 ? bwd_kernel<T, 1, 16, 1024> : bwd_of<T, 1, 8>(threads);
 }
 
 // The GPU's SM count enters the workspace's size, which is asked for without a
@@ -367,17 +385,17 @@ gdn_status gdn_rms_norm_fwd(const gdn_rms_norm_fwd_args *a, void *stream) {
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     norm::FwdArgs f{a->x, a->residual, a->weight, a->y, a->sum, a->scales, a->rstd, a->eps,
-                    1.f / (float)a->D, a->rows, a->D, norm::row_threads(a->D), (a->D + 127) / 128};
+                    1.f / (float)a->D, a->rows, a->D, norm::row_threads(a->dtype, a->D, a->mx != 0), (a->D + 127) / 128};
     const int threads = norm::cta_threads(f.tpr), per = threads / f.tpr;
     const long long rows = a->mx ? (a->rows + 127ll) / 128 * 128 : a->rows;
     const long long ctas = std::min<long long>((rows + per - 1) / per, (long long)dev.sms * (8 * 256 / threads));
     const bool vec = norm::vector_rows(a->dtype, a->D);
-    auto k = a->dtype == GDN_BF16 ? (a->mx ? norm::fwd_of<__nv_bfloat16, 8, true>(threads)
-                                     : vec ? norm::fwd_of<__nv_bfloat16, 8, false>(threads)
-                                           : norm::fwd_of<__nv_bfloat16, 1, false>(threads))
-                                  : (a->mx ? norm::fwd_of<float, 4, true>(threads)
-                                     : vec ? norm::fwd_of<float, 4, false>(threads)
-                                           : norm::fwd_of<float, 1, false>(threads));
+    auto k = a->dtype == GDN_BF16 ? (a->mx ? norm::fwd_of<__nv_bfloat16, 8, 16, true>(threads)
+                                     : vec ? norm::fwd_of<__nv_bfloat16, 8, 16, false>(threads)
+                                           : norm::odd_fwd_of<__nv_bfloat16>(a->D, threads))
+                                  : (a->mx ? norm::fwd_of<float, 4, 16, true>(threads)
+                                     : vec ? norm::fwd_of<float, 4, 16, false>(threads)
+                                           : norm::odd_fwd_of<float>(a->D, threads));
     cudaStream_t q = (cudaStream_t)stream;
     prof_before("rms_norm_fwd", q);
     const cudaError_t e = launch_pdl(k, dim3((unsigned)ctas), dim3(threads), 0, q, f);
@@ -391,7 +409,7 @@ size_t gdn_rms_norm_bwd_workspace_size(const gdn_rms_norm_bwd_args *a) {
         return 0;
     }
     if (norm::check(a->rows, a->D, a->dtype) != GDN_OK) return 0;
-    return std::max<size_t>(256, (size_t)norm::bwd_ctas(a->rows, a->D, norm::kMaxSms) * a->D * 4);
+    return std::max<size_t>(256, (size_t)norm::bwd_ctas(a->rows, a->dtype, a->D, norm::kMaxSms) * a->D * 4);
 }
 
 gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -408,14 +426,14 @@ gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *a, void *ws, size_t ws_
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    const int ctas = norm::bwd_ctas(a->rows, a->D, std::min(dev.sms, norm::kMaxSms));
-    const int tpr = norm::row_threads(a->D), threads = norm::cta_threads(tpr), per = threads / tpr;
+    const int ctas = norm::bwd_ctas(a->rows, a->dtype, a->D, std::min(dev.sms, norm::kMaxSms));
+    const int tpr = norm::row_threads(a->dtype, a->D, false), threads = norm::cta_threads(tpr), per = threads / tpr;
     const norm::BwdArgs b{a->dy, a->sum, a->weight, a->d_sum, a->rstd, a->ds, (float *)ws,
                           1.f / (float)a->D, a->rows, a->D, tpr};
     const bool vec = norm::vector_rows(a->dtype, a->D);
     auto k = a->dtype == GDN_BF16
-                 ? (vec ? norm::bwd_of<__nv_bfloat16, 8>(threads) : norm::bwd_of<__nv_bfloat16, 1>(threads))
-                 : (vec ? norm::bwd_of<float, 4>(threads) : norm::bwd_of<float, 1>(threads));
+                 ? (vec ? norm::bwd_of<__nv_bfloat16, 8, 16>(threads) : norm::odd_bwd_of<__nv_bfloat16>(a->D, threads))
+                 : (vec ? norm::bwd_of<float, 4, 16>(threads) : norm::odd_bwd_of<float>(a->D, threads));
     // rows that share a CTA: 256 / tpr of at most 16 tpr columns, 16 KB of sums
     const size_t smem = per > 1 ? (size_t)per * a->D * sizeof(float) : 0;
     cudaStream_t q = (cudaStream_t)stream;
