@@ -8,7 +8,8 @@
 // and issues the MMAs, and the fp32 tile leaves TMEM through shared memory so that rows of
 // C are written 128 features at a time.  Where tiles are too few for the GPU the CTAs of a
 // cluster share K: each leaves its fp32 tile in its shared memory, and after the cluster's
-// barrier each adds up its share of the rows, in rank order.
+// barrier each adds up its share of the rows, in rank order.  Bound by the weight's bytes:
+// 7 x 12288 x 4096 MXFP4 6.4 us, of which its 27 MB take 4.0 at the measured copy rate.
 #include <algorithm>
 
 #include "gdn_layer_internal.h"
@@ -231,6 +232,12 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
 // SM takes from L2 per MMA; the accumulators of two tiles share 448 TMEM columns, the
 // last 64 of the one being the first 64 of the other, so that the epilogue of a tile
 // runs under the next one's MMAs once it has taken those 64.
+//
+// 8192 x 12288 x 4096: 135 us in 4 bits (6.1 PFLOP/s, 3.2 times the measured bf16 rate), 241
+// us in 8 (3.4).  A stage's four MMAs take 512 cycles (247 ns); a stage takes 290 to 315 ns,
+// bound by the hand-over between the loading warps, the MMA warp and its commits, and a tile
+// 1.6 us more, in which its MMAs wait for the shared columns.  Tiles of 192 columns, which
+// share none, took as long (138 and 253 us).
 constexpr int kPairThreads = 224;                    // weights, MMA, four epilogue warps, tokens
 constexpr int kPairStages = 6;
 constexpr int kPairAcc = 192;                        // column of the second accumulator
