@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "gdn_layer_internal.h"
+#include "gdn_mx_strip.cuh"
 #include "tc_mx_ptx.cuh"
 
 namespace gdn {
@@ -233,24 +234,45 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
 // last 64 of the one being the first 64 of the other, so that the epilogue of a tile
 // runs under the next one's MMAs once it has taken those 64.
 //
-// 8192 x 12288 x 4096: 135 us in 4 bits (6.1 PFLOP/s, 3.2 times the measured bf16 rate), 241
-// us in 8 (3.4).  A stage's four MMAs take 512 cycles (247 ns); a stage takes 290 to 315 ns,
+// 8192 x 12288 x 4096: 135 us in 4 bits (6.1 PFLOP/s, 3.2 times the measured bf16 rate), 243
+// us in 8 (3.4); with the tokens' quantisation under the MMAs 143 and 265.  A stage's four MMAs take 512 cycles (247 ns); a stage takes 290 to 315 ns,
 // bound by the hand-over between the loading warps, the MMA warp and its commits, and a tile
 // 1.6 us more, in which its MMAs wait for the shared columns.  Tiles of 192 columns, which
 // share none, took as long (138 and 253 us).
 constexpr int kPairThreads = 224;                    // weights, MMA, four epilogue warps, tokens
+constexpr int kPairQuantThreads = 256;               // more, where the tokens come unquantised
 constexpr int kPairStages = 6;
 constexpr int kPairAcc = 192;                        // column of the second accumulator
 constexpr int kPairScales = 448;                     // columns of the scales: two sets of 24
 constexpr int kPairOut = 4096;                       // a warp's staged 32 x 128-byte block of C
 
+// The tokens' rows from `row0` on (whole tiles) that the product itself quantises, to where
+// it reads them, in strips of up to kStrip spans of a row, or of 2^log_rows rows where those
+// are short.  work[0] counts strips that warps have taken, work[1 + row / 128] those that
+// are done; both begin at 0.
+struct Unquantised {
+    const void *x;                                   // null: all rows are there
+    int fp32, row0, strips, log_rows;                // strips of a row
+    uint8_t *data, *scales;
+    uint32_t *work;
+};
+constexpr int kStrip = 16;
+
 struct PairArgs {
     int M, N, K, kblocks, ktiles;
     int m_tiles, n_tiles;
+    int rows_first;                                  // the order of tiles: rows of tiles are done one after the other
     int early_w;                                     // as in GemmArgs
+    Unquantised rest;
     int *status;
     long long spin_limit;
 };
+
+// Tile `i`: its row and column of tiles.
+__device__ __forceinline__ int2 pair_tile(const PairArgs &a, int i) {
+    const int inner = a.rows_first ? a.n_tiles : a.m_tiles, o = i / inner, n = i - o * inner;
+    return a.rows_first ? make_int2(o, n) : make_int2(n, o);
+}
 
 struct PairControl {
     uint64_t full[kPairStages], empty[kPairStages], acc_full, acc_free, done;
@@ -262,7 +284,7 @@ template <bool FP4>
 constexpr int pair_stage_bytes() { return 32768 + (FP4 ? 3072 : 2048); }
 
 template <bool FP4, typename TO>
-__global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_constant__ CUtensorMap map_x,
+__global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_kernel(const __grid_constant__ CUtensorMap map_x,
                                                              const __grid_constant__ CUtensorMap map_w,
                                                              const __grid_constant__ CUtensorMap map_sx,
                                                              const __grid_constant__ CUtensorMap map_sw,
@@ -327,13 +349,20 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
         };
         // the first tile's weights may come before the kernel ahead has written the tokens
         const int ahead = weights && a.early_w && pair < tiles ? min(kPairStages, a.kblocks) : 0;
-        for (int i = 0; i < ahead; ++i) load(i, 0, pair / a.m_tiles * 2, i);
+        for (int i = 0; i < ahead; ++i) load(i, 0, pair_tile(a, pair).y * 2, i);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int i = 0, s = 0;                            // stages asked for
         uint32_t parity = 1;                         // of the stage's last release; the first round has none
         bool ok = true;
+        int ready = a.rest.x ? a.rest.row0 / 128 : a.m_tiles * 2;    // rows quantised, in 128s
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            const int feat = tile / a.m_tiles * 2, row = (tile - feat / 2 * a.m_tiles) * 2 + rank;    // in 128s
+            const int2 at = pair_tile(a, tile);
+            const int row = at.x * 2 + rank, feat = at.y * 2;    // in 128s
+            if (!weights && row >= ready && row * 128 < a.M) {
+                ok = tc::word_spin(a.rest.work + 1 + row, (128u >> a.rest.log_rows) * a.rest.strips, a.spin_limit, a.status);
+                if (!ok) break;
+                ready = row + 1;
+            }
             for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
                 if (i >= kPairStages) {
                     ok = tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status);
@@ -392,6 +421,29 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
             }
             tc::mma_commit_pair(&ctl.done);
         }
+    } else if (warp >= kPairThreads / 32) {
+        // Quantises strips in the tiles' order.  A strip belongs to the warp that took it and
+        // no strip waits for anything, so that the loads' waits end whichever CTAs run.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const Unquantised &r = a.rest;
+        const int spans = (a.ktiles + 1) / 2;
+        const unsigned total = (unsigned)(((a.M + 127) / 128 * 128 - r.row0) >> r.log_rows) * r.strips;
+        unsigned next = lane == 0 ? atomicAdd(r.work, 1u) : 0u;
+        for (;;) {
+            const unsigned item = __shfl_sync(0xffffffffu, next, 0);
+            if (item >= total) break;
+            if (lane == 0) next = atomicAdd(r.work, 1u);
+            const int row = r.row0 + (int)(item / r.strips << r.log_rows), first = (int)(item % r.strips) * kStrip;
+            const int end = min(first + kStrip, spans);
+            for (int i = 0; i < 1 << r.log_rows; ++i)
+                if (r.fp32)
+                    quantize_strip<float, FP4, false>((const float *)r.x, r.data, r.scales, row + i, first, end, a.M,
+                                                      a.K, a.ktiles);
+                else
+                    quantize_strip<__nv_bfloat16, FP4, false>((const __nv_bfloat16 *)r.x, r.data, r.scales, row + i,
+                                                              first, end, a.M, a.K, a.ktiles);
+            tc::add_release(r.work + 1 + row / 128);
+        }
     } else {
         // epilogue: each warp takes its 32 rows, 64 (bf16) or 32 (fp32) columns at a time,
         // through a swizzled block of its own to a TMA store
@@ -403,7 +455,8 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
         for (int tile = pair; tile < tiles; tile += pairs, ++t) {
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_full, t & 1, a.spin_limit, a.status))) break;
             tc::tc_fence_after();
-            const int row = ((tile % a.m_tiles) * 2 + rank) * 128 + 32 * quarter, feat = tile / a.m_tiles * 256;
+            const int2 at = pair_tile(a, tile);
+            const int row = (at.x * 2 + rank) * 128 + 32 * quarter, feat = at.y * 256;
             const uint32_t acc = tmem + (t & 1 ? kPairAcc : 0);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -441,7 +494,7 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
         __syncwarp();
     }
     // every MMA done and every copy landed before TMEM is given back and a CTA goes
-    tc::mbar_drain(&ctl.done, 0);
+    if (warp < kPairThreads / 32) tc::mbar_drain(&ctl.done, 0);
     tc::tc_fence_before();
     tc::cluster_sync();
     if (threadIdx.x == 0 && rank == 0)
@@ -452,15 +505,27 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
     if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
+// Tiles are walked along the shorter side, whose operand then stays in L2 while the other
+// passes once; along rows of tiles too where the weight takes half of L2 at most, so that
+// the product can quantise rows under its MMAs.  MXFP8, K = 4096, rows first | columns
+// first: 32768 x 4096 312 us | 370, 1024 x 65536 209 | 169, 8192 x 12288 242 | 238.
+bool rows_first(const gdn_mx_matmul_args *a) {
+    const long long bytes = (long long)a->N * (a->format == GDN_MXFP4 ? a->K / 2 : a->K);
+    return a->N <= a->M || bytes <= 64ll << 20;
+}
+
 template <bool FP4, typename TO>
-gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, cudaStream_t q) {
+gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, const Unquantised &rest,
+                    cudaStream_t q) {
     PairArgs g{};
     g.M = a->M, g.N = a->N, g.K = a->K;
     g.kblocks = (a->K + (FP4 ? 255 : 127)) / (FP4 ? 256 : 128);
     g.ktiles = (a->K + 127) / 128;
     g.m_tiles = (a->M + 255) / 256;
     g.n_tiles = (a->N + 255) / 256;
+    g.rows_first = rows_first(a);
     g.early_w = early_w;
+    g.rest = rest;
     g.status = dev.status;
     g.spin_limit = dev.spin_limit;
     const long long bytes = FP4 ? a->K / 2 : a->K;
@@ -479,7 +544,7 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
         return cuda_fail(e, "shared memory of the product");
     const int pairs = (int)std::min<long long>((long long)g.m_tiles * g.n_tiles, dev.sms / 2);
     prof_before("mx_gemm_pair", q);
-    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), smem, 2, q, mx, mw, msx, msw, mc, g);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads + (rest.x ? kPairQuantThreads : 0)), smem, 2, q, mx, mw, msx, msw, mc, g);
     prof_after(q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "mx product launch");
 }
@@ -504,14 +569,28 @@ bool pair_fits(const gdn_mx_matmul_args *a, int sms) {
            tiles < (1ll << 30);
 }
 
-gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, cudaStream_t q) {
+// Rows to quantise ahead of the product: those of the pairs' first tiles (in 4 bits, whose
+// MMAs take half as long, of the first two), the product itself taking the rest under its
+// MMAs; or all of them where K, N or M is too short for the MMAs to cover that.  Us all ahead |
+// the rest under the MMAs: 8192 x 12288 x 4096 in 4 bits 156 | 143, 8 bits 275 | 265; 8192 x
+// 4096 x 4096 76 | 70, 105 | 98; 2048 x 12288 x 4096 49 | 47, 77 | 75; but 4096 x 16384 x 512
+// 46 | 53, 50 | 55; 65536 x 1024 x 1024 84 | 103, 95 | 109.
+int rows_ahead(const gdn_mx_matmul_args *a, int sms) {
+    const int n_tiles = (a->N + 255) / 256, waves = a->format == GDN_MXFP4 ? 2 : 1;
+    const int first = (sms / 2 + n_tiles - 1) / n_tiles * 256 * waves;
+    return pair_fits(a, sms) && rows_first(a) && a->K >= 2048 && n_tiles >= 16 && a->M >= 2 * first ? first : a->M;
+}
+
+gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w, const Unquantised &rest,
+               cudaStream_t q) {
     const bool fp4 = a->format == GDN_MXFP4;
     cudaError_t e = tc::encoder();
     if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled lookup");
     if (pair_fits(a, dev.sms)) {
-        if (a->out_dtype == GDN_FP32) return fp4 ? run_pair<true, float>(a, dev, early_w, q) : run_pair<false, float>(a, dev, early_w, q);
-        return fp4 ? run_pair<true, __nv_bfloat16>(a, dev, early_w, q)
-                   : run_pair<false, __nv_bfloat16>(a, dev, early_w, q);
+        if (a->out_dtype == GDN_FP32) return fp4 ? run_pair<true, float>(a, dev, early_w, rest, q)
+                                                    : run_pair<false, float>(a, dev, early_w, rest, q);
+        return fp4 ? run_pair<true, __nv_bfloat16>(a, dev, early_w, rest, q)
+                   : run_pair<false, __nv_bfloat16>(a, dev, early_w, rest, q);
     }
     GemmArgs g{};
     g.sx = a->a_scales;
@@ -565,7 +644,7 @@ using namespace gdn;
 
 // early_w: the kernel ahead in the stream began only when all before it, the writers of b
 // among them, had ended.
-static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, void *stream) {
+static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, const mx::Unquantised &rest, void *stream) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->M < 0 || a->N < 0 || a->K < 0)
         return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
@@ -588,23 +667,29 @@ static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, void *stream
                                               (cudaStream_t)stream);
         return e == cudaSuccess ? GDN_OK : cuda_fail(e, "clearing c");
     }
-    return mx::run(a, dev, early_w, (cudaStream_t)stream);
+    return mx::run(a, dev, early_w, rest, (cudaStream_t)stream);
 }
 
-extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) { return matmul(a, false, stream); }
+extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) {
+    return matmul(a, false, mx::Unquantised{}, stream);
+}
 
-// Bytes of X's elements in the workspace, its scales following.
+// Bytes of X's elements in the workspace; its scales follow, then the counters of the
+// product's own quantisation.
 static size_t linear_data_bytes(const gdn_mx_linear_args *a) {
     const size_t n = (size_t)a->M * a->K;
     return ((a->format == GDN_MXFP4 ? n / 2 : n) + 255) / 256 * 256;
 }
+
+// The counters: one, and one for each 128 rows.
+static int linear_words(const gdn_mx_linear_args *a) { return 1 + (int)((a->M + 127ll) / 128); }
 
 extern "C" size_t gdn_mx_linear_workspace_size(const gdn_mx_linear_args *a) {
     if (!a || a->M < 0 || a->K < 0) {
         fail(GDN_ERR_INVALID_ARG, "null args or bad sizes");
         return 0;
     }
-    return std::max<size_t>(256, linear_data_bytes(a) + gdn_mx_scale_bytes(a->M, a->K));
+    return std::max<size_t>(256, linear_data_bytes(a) + gdn_mx_scale_bytes(a->M, a->K) + 4 * (size_t)linear_words(a));
 }
 
 extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -614,9 +699,23 @@ extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_
     if (!ws || misaligned(ws) || ws_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     uint8_t *data = (uint8_t *)ws, *scales = data + linear_data_bytes(a);
-    const gdn_mx_quantize_args q{a->x, a->M, a->K, a->dtype, a->format, data, scales};
-    const gdn_status st = gdn_mx_quantize(&q, stream);
-    if (st != GDN_OK) return st;
     const gdn_mx_matmul_args m{data, scales, a->w, a->w_scales, a->M, a->N, a->K, a->format, a->out_dtype, a->c};
-    return matmul(&m, a->M > 0 && a->K > 0, stream);
+    gdn_mx_quantize_args q{a->x, a->M, a->K, a->dtype, a->format, data, scales};
+    mx::Unquantised rest{};
+    if (a->M >= 512 && a->N > 0 && a->K % 32 == 0) {           // at least two tiles of rows
+        LayerDevice dev;
+        const gdn_status st = layer_device(&dev);
+        if (st != GDN_OK) return st;
+        q.rows = mx::rows_ahead(&m, dev.sms);
+        if (q.rows < a->M) {
+            uint32_t *work = (uint32_t *)(scales + gdn_mx_scale_bytes(a->M, a->K));
+            const int spans = (a->K + 255) / 256;
+            int log_rows = 0;
+            while (spans << (log_rows + 1) <= mx::kStrip) ++log_rows;
+            rest = {a->x, a->dtype == GDN_FP32, q.rows, (spans + mx::kStrip - 1) / mx::kStrip, log_rows, data, scales, work};
+        }
+    }
+    const gdn_status st = mx_quantize(&q, rest.work, rest.x ? linear_words(a) : 0, stream);
+    if (st != GDN_OK) return st;
+    return matmul(&m, a->M > 0 && a->K > 0, rest, stream);
 }

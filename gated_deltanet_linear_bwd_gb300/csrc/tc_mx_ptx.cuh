@@ -149,6 +149,29 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, long lo
     return false;
 }
 
+// Waits until the word at `p`, which other CTAs add to with add_release, is `want`; their
+// writes before that may then be read by this warp's TMA loads.  The same answer in every
+// lane.
+__device__ __forceinline__ bool word_spin(const uint32_t *p, uint32_t want, long long limit, int *status) {
+    for (long long i = 0; i < limit; ++i) {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        if (__all_sync(0xffffffffu, v == want)) {
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            __syncwarp();
+            return true;
+        }
+    }
+    set_status(status, GDN_ERR_TIMEOUT);
+    return false;
+}
+// Adds 1 to the word at `p` behind every write of the warp, for the readers of word_spin.
+__device__ __forceinline__ void add_release(uint32_t *p) {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
+}
+
 // ------------------------------------------------------------------ CTA pairs
 // The same for cta_group::2: two CTAs of a cluster work on one 256-row tile.  Each
 // holds its 128 rows of A, half the rows of B, and 128 lanes of D; the even CTA issues

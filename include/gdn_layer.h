@@ -140,8 +140,9 @@ typedef struct gdn_mx_matmul_args {
 } gdn_mx_matmul_args;
 gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *args, void *stream);
 
-/* C [M, N] = X W^T with X [M, K] quantised to W's format on the way: gdn_mx_quantize
- * into the workspace, then gdn_mx_matmul, in one call. */
+/* C [M, N] = X W^T with X [M, K] quantised to W's format on the way, into the workspace:
+ * the results of gdn_mx_quantize and gdn_mx_matmul.  Of large products only the first rows
+ * are quantised ahead, the others under the product's own MMAs. */
 typedef struct gdn_mx_linear_args {
     const void *x;              /* [M, K], dtype                                     */
     const void *w;              /* [N, K] MX matrix                                  */

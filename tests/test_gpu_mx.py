@@ -192,3 +192,37 @@ def test_refusals():
             bad()
     with pytest.raises(lib().GdnError, match="aligned"):
         q(torch.zeros(1 + 64, device="cuda")[1:].view(1, 64))
+
+
+# mx_linear of sizes at which the product quantises most rows itself: whole and ragged tiles of
+# rows, an odd number of 128-row blocks, K of several strips and of a part of one, either type
+FUSED = [(5200, 4096, 2048), (5376, 4104, 4160), (3201, 8200, 2080), (5150, 4360, 8352)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("M,N,K", FUSED)
+def test_linear_is_quantisation_and_product(M, N, K, fmt, dtype):
+    x, w = draw(M, K, 7).to(DT[dtype]), lib().mx_quantize(draw(N, K, 8), fmt)
+    x[M - 3, 40], x[300, 5] = float("nan"), float("inf")
+    want = lib().mx_matmul(lib().mx_quantize(x, fmt), w, DT[dtype])
+    assert torch.isnan(want[M - 3]).all() and torch.isnan(want[300]).all()
+    for _ in range(3):
+        assert torch.equal(lib().mx_linear(x, w).nan_to_num(7.0), want.nan_to_num(7.0))
+    assert lib().gdn_sync_status(torch.cuda.current_stream().cuda_stream) == 0
+
+
+def test_linear_on_two_streams_at_once():
+    xs = [draw(4096, 2048, s) for s in (1, 2)]
+    w = lib().mx_quantize(draw(4104, 2048, 3), "mxfp8")
+    want = [lib().mx_matmul(lib().mx_quantize(x, "mxfp8"), w) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(lib().mx_linear(xs[i], w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, want[i]) for i in (0, 1) for c in got[i])
