@@ -252,6 +252,7 @@ struct Join {
 // Where a lane's channels are, and which of the two exist.
 struct Place {
     int warp, lane, rank, size, cluster, ch;
+    int from;                  // ch, or of a lane that has none the last channel there is
     bool in0, in1;
 };
 __device__ __forceinline__ Place place(const Shape &s) {
@@ -261,6 +262,7 @@ __device__ __forceinline__ Place place(const Shape &s) {
     p.cluster = blockIdx.x / p.size;
     p.ch = p.cluster % s.groups * kChannels + 2 * p.lane;
     p.in0 = p.ch < s.D, p.in1 = p.ch + 1 < s.D;
+    p.from = min(p.ch, s.D - 1);
     return p;
 }
 __device__ __forceinline__ float2 load_state(const float *base, long long at, const Place &p) {
@@ -314,7 +316,7 @@ struct FwdArgs {
 // Forward over TMA tiles (TMA true), or with plain loads for widths whose rows do not
 // start on 16 bytes.
 template <typename T, bool GATED, int W, int R, int STAGES, bool TMA>
-__global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUtensorMap map_x,
+__global__ void __launch_bounds__(32 * W, TMA ? 1 : 3) fwd_kernel(const __grid_constant__ CUtensorMap map_x,
                                                        const __grid_constant__ CUtensorMap map_g,
                                                        const FwdArgs a, const Shape s) {
     using Ring = linrec::Ring<T, W, R, 2, STAGES>;
@@ -361,9 +363,9 @@ __global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUt
         if (TMA && threadIdx.x == 0)
             for (int i = 0; i < STAGES - 1 && i < rounds && ok; ++i) ask(i);
         auto token = [&](int i) { return i * step + at.rank * kTile + at.warp * R; };
-        auto rows_of = [&](int i) {          // tokens this lane has of tile i
-            return ok && at.in0 ? (int)max(0ll, min((long long)R, len - token(i))) : 0;
-        };
+        // tokens this warp has of tile i, the same for lanes past the last channel, which walk
+        // TMA's zeros or the last channel: in two branches a warp would take twice as long
+        auto rows_of = [&](int i) { return ok ? (int)max(0ll, min((long long)R, len - token(i))) : 0; };
         auto cell = [&](int i, int input, int r) {
             return get2(*reinterpret_cast<const typename Raw2<T>::type *>(
                 &ring.tile[(base + i) % STAGES][input][at.warp * R + r][2 * at.lane]));
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUt
             const int rows = rows_of(i);
             auto go = [&](auto whole) {
                 if constexpr (!TMA) {
-                    const long long row0 = (bos + token(i)) * s.D + at.ch;
+                    const long long row0 = (bos + token(i)) * s.D + at.from;
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const bool in = whole.value || r < rows;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(32 * W) fwd_kernel(const __grid_constant__ CUt
         };
         // tile i's results from the value before this warp's first token
         auto emit = [&](int i, const float2 (&al)[R], const float2 (&xv)[TMA ? 1 : R], float2 h) {
-            const int rows = rows_of(i);
+            const int rows = at.in0 ? rows_of(i) : 0;
             auto go = [&](auto whole) {
                 T *out = reinterpret_cast<T *>(a.h) + (bos + token(i)) * s.D + at.ch;
 #pragma unroll
@@ -450,7 +452,7 @@ struct BwdArgs {
 // walk is token len - 1 - u, so a tile's rows lie in shared memory from its last to
 // its first; the tile of h is one token earlier than the others.
 template <typename T, bool GATED, int W, int R, int STAGES, bool TMA>
-__global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUtensorMap map_dh,
+__global__ void __launch_bounds__(32 * W, TMA ? 1 : 2) bwd_kernel(const __grid_constant__ CUtensorMap map_dh,
                                                        const __grid_constant__ CUtensorMap map_g,
                                                        const __grid_constant__ CUtensorMap map_h,
                                                        const BwdArgs a, const Shape s) {
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
         for (int i = 0; i < rounds; ++i, ++tiles) {
             const int st = tiles % STAGES;
             const long long u = i * step + at.rank * kTile + at.warp * R, top = len - 1 - u;
-            int rows = at.in0 ? (int)max(0ll, min((long long)R, len - u)) : 0;
+            int rows = (int)max(0ll, min((long long)R, len - u));
             if (TMA) {
                 if (ok) ok = tc::mbar_wait(&ring.full[st], (tiles / STAGES) & 1, s.spin_limit, s.status);
                 if (!ok) rows = 0;
@@ -516,8 +518,9 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
                     &ring.tile[st][input][kTile - 1 - at.warp * R - r][2 * at.lane]));
             };
             const long long row0 = (bos + top) * s.D + at.ch;
-            const T *gd = reinterpret_cast<const T *>(a.dh) + row0, *gg = reinterpret_cast<const T *>(a.g) + row0;
-            const T *gh = reinterpret_cast<const T *>(a.h) + row0;
+            const long long from = row0 - at.ch + at.from;
+            const T *gd = reinterpret_cast<const T *>(a.dh) + from, *gg = reinterpret_cast<const T *>(a.g) + from;
+            const T *gh = reinterpret_cast<const T *>(a.h) + from;
             float2 al[R], sp[GATED ? R : 1], dv[TMA ? 1 : R], gv[TMA ? 1 : R], hv[TMA ? 1 : R];
             float2 A = both(1.f), B = both(0.f);
             auto first = [&](auto whole) {
@@ -568,8 +571,9 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
                 }
             };
             if (s.reduce) continue;
-            if (rows == R && (lead || top >= R)) second(std::true_type());
-            else if (rows > 0) second(std::false_type());
+            const int mine = at.in0 ? rows : 0;
+            if (mine == R && (lead || top >= R)) second(std::true_type());
+            else if (mine > 0) second(std::false_type());
         }
         __syncthreads();
         if (at.rank == 0 && at.warp == 0) {
@@ -593,21 +597,35 @@ __global__ void __launch_bounds__(32 * W) bwd_kernel(const __grid_constant__ CUt
     }
 }
 
-// The parts' pairs joined: the value before each part, and after the last one.
-__global__ void __launch_bounds__(128) parts_kernel(const float2 *pair, float *start, const float *init,
-                                                    float *final, int N, int parts, int D) {
+// The parts' pairs joined: the value before each part, and after the last one.  A channel's
+// parts are shared out over the 32 warps of a block, which first meet with the pairs of
+// theirs: one thread for all of a channel's parts took 0.14 us for each.
+__global__ void __launch_bounds__(1024) parts_kernel(const float2 *pair, float *start, const float *init,
+                                                     float *final, int N, int parts, int D) {
+    __shared__ float2 all[32][33];
     pdl_enter();
-    const long long i = blockIdx.x * 128ll + threadIdx.x;
-    if (i >= (long long)N * D) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long i = blockIdx.x * 32ll + lane;
+    const bool in = i < (long long)N * D;
     const long long n = i / D, ch = i - n * D, at = n * parts * D + ch;
-    float v = init ? init[i] : 0.f;
-#pragma unroll 16
-    for (int k = 0; k < parts; ++k) {
-        const float2 q = pair[at + (long long)k * D];
-        start[at + (long long)k * D] = v;
-        v = q.x * v + q.y;
+    const int per = (parts + 31) / 32, first = warp * per, end = in ? min(first + per, parts) : 0;
+    float2 q = make_float2(1.f, 0.f);
+#pragma unroll 8
+    for (int k = first; k < end; ++k) {
+        const float2 r = pair[at + (long long)k * D];
+        q = make_float2(r.x * q.x, r.x * q.y + r.y);
     }
-    if (final) final[i] = v;
+    all[warp][lane] = q;
+    __syncthreads();
+    float v = in && init ? init[i] : 0.f;
+    for (int w = 0; w < warp; ++w) v = all[w][lane].x * v + all[w][lane].y;
+#pragma unroll 8
+    for (int k = first; k < end; ++k) {
+        const float2 r = pair[at + (long long)k * D];
+        start[at + (long long)k * D] = v;
+        v = r.x * v + r.y;
+    }
+    if (in && final && warp == 31) final[i] = v;
 }
 
 // One token: VEC neighbouring channels to a thread, which takes the same ones of every
@@ -700,7 +718,6 @@ struct Tiles {
 };
 
 constexpr int kSms = 152;          // of the GPU that the choices below are made for
-constexpr int kMaxParts = 128;
 
 // CTAs that share a sequence: doubled while the grid leaves slots of the GPU (two
 // CTAs per SM) empty and the sequences have a tile for each.
@@ -710,17 +727,25 @@ int cluster_of(long long clusters, long long mean_len) {
     return c;
 }
 
-// Parts of a sequence, or 1: as many as fill the GPU, where the two walks' tiles, 1.8 us
-// each, and the two more launches, 8 us, are less than the cluster's rounds, 2.5 us each.
-// Gated bf16 forward / backward, us: 65536 x 64 114 / 190 in clusters, 39 / 45 in parts;
-// 65536 x 1024 156 / 257 and 121 / 162; 8192 x 64 18 / 30 and 25 / 34.
-int parts_of(long long clusters, int cluster, long long mean_len) {
+// What the choice between clusters and parts goes by.
+struct Kind {
+    bool fp32, gated, back, tma;
+};
+
+// Parts of a sequence, or 1: as many as fill the GPU with a CTA each, of 128 tokens at
+// least, where two walks of them and the two more launches (5 us) take less than the
+// cluster's rounds, each of which is 1.6 times a tile of 128 tokens long.  The walks read twice, at
+// 7 TB/s in all.  Us in clusters | parts: 4096 x 64 gated bf16
+// forward 9.5 | 9.1, backward 15.8 | 12.1; 16384 x 64 30 | 12, 50 | 15, in fp32 65 | 17, 144 |
+// 24; 65536 x 1024 151 | 117, 252 | 157; but fp32 and not gated 187 | 204, 309 | 258.
+int parts_of(long long clusters, int cluster, long long mean_len, const Kind &k, double bytes) {
     if (cluster < kMaxCluster) return 1;
-    const long long parts = std::min<long long>({kMaxParts, 2 * kSms / clusters, mean_len / 256});
+    const long long parts = std::min(2 * kSms / clusters, mean_len / 128);
     if (parts < 2) return 1;
-    const double rounds = (double)((mean_len + 128 * cluster - 1) / (128 * cluster));
-    const double tiles = 2.0 * (double)((mean_len / parts + 127) / 128);
-    return tiles * 1.8 + 8 < rounds * 2.5 ? (int)parts : 1;
+    const double tile = (k.fp32 ? (k.gated ? 3.3 : 1.8) : k.tma ? 1.2 : 2.2) * (k.back ? 1.6 : 1.0);
+    const long long rounds = (mean_len + 1023) / 1024, tiles = 2 * ((mean_len + 128 * parts - 1) / (128 * parts));
+    const double walks = std::max((double)tiles * tile, bytes * (k.back ? 7 : 5) / 7e6);
+    return walks + 5 < (double)rounds * 1.6 * tile ? (int)parts : 1;
 }
 
 gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
@@ -734,7 +759,10 @@ gdn_status check(int B, int T, int D, int N, int dtype, bool packed) {
     return GDN_OK;
 }
 
-Shape shape_of(const int32_t *cu, int B, int T, int D, int N) {
+// Rows that start on 16 bytes, as TMA wants them.
+bool tma_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
+
+Shape shape_of(const int32_t *cu, int B, int T, int D, int N, const Kind &kind) {
     Shape s = {};
     s.cu = cu;
     s.T = T;
@@ -744,7 +772,8 @@ Shape shape_of(const int32_t *cu, int B, int T, int D, int N) {
     const long long mean = cu ? T / s.N : T;
     s.lanes_n = group_lanes(s.N, s.groups);
     s.cluster = cluster_of((long long)s.groups * s.lanes_n, mean);
-    s.parts = parts_of((long long)s.groups * s.lanes_n, s.cluster, mean);
+    s.parts = parts_of((long long)s.groups * s.lanes_n, s.cluster, mean, kind,
+                       (double)(cu ? T : (long long)T * s.N) * D * (kind.fp32 ? 4 : 2));
     if (s.parts > 1) {
         s.cluster = 1;
         s.lanes_n = group_lanes(s.N * s.parts, s.groups);
@@ -758,9 +787,6 @@ void place_parts(Shape &s, void *ws) {
     s.pair = (float2 *)ws;
     s.start = (float *)(s.pair + (size_t)s.N * s.parts * s.D);
 }
-
-// Rows that start on 16 bytes, as TMA wants them.
-bool tma_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch(const char *name, void (*kernel)(KArgs...), int warps, size_t smem, const Shape &s, cudaStream_t st,
@@ -790,7 +816,7 @@ cudaError_t in_parts(Shape s, const float *init, float *final, cudaStream_t q, W
     cudaError_t e = walk(s);
     if (e != cudaSuccess) return e;
     prof_before("linrec_parts", q);
-    e = launch_pdl(parts_kernel, dim3((unsigned)(((long long)s.N * s.D + 127) / 128)), dim3(128), 0, q,
+    e = launch_pdl(parts_kernel, dim3((unsigned)(((long long)s.N * s.D + 31) / 32)), dim3(1024), 0, q,
                    (const float2 *)s.pair, s.start, init, final, s.N, s.parts, s.D);
     prof_after(q);
     if (e != cudaSuccess) return e;
@@ -839,12 +865,21 @@ cudaError_t run_bwd(const BwdArgs &b, const Shape &s, bool tma, cudaStream_t q) 
 // The answer to a workspace query: 256 stands for none.
 size_t asked_for(size_t need) { return need == 0 ? 256 : std::max<size_t>(512, need); }
 
+Shape shape_of(const gdn_linrec_fwd_args *a) {
+    return shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N,
+                    {a->dtype == GDN_FP32, a->gate_scale != nullptr, false, tma_rows(a->dtype, a->D)});
+}
+Shape shape_of(const gdn_linrec_bwd_args *a) {
+    return shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N,
+                    {a->dtype == GDN_FP32, a->gate_scale != nullptr, true, tma_rows(a->dtype, a->D)});
+}
+
 // Workspace: parts, then a row of d(gate_scale) for each CTA of a channel group.
 size_t fwd_workspace(const gdn_linrec_fwd_args *a) {
-    return parts_bytes(shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N));
+    return parts_bytes(shape_of(a));
 }
 size_t bwd_workspace(const gdn_linrec_bwd_args *a) {
-    const Shape s = shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    const Shape s = shape_of(a);
     const bool sums = a->gate_scale && a->d_gate_scale;
     return parts_bytes(s) + (sums ? (size_t)s.lanes_n * s.cluster * s.D * sizeof(float) : 0);
 }
@@ -880,7 +915,7 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_fwd_args *a, void *ws, size_t ws_byte
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    linrec::Shape s = linrec::shape_of(a);
     s.status = dev.status;
     s.spin_limit = dev.spin_limit;
     linrec::place_parts(s, ws);
@@ -921,7 +956,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_bwd_args *a, void *ws, size_t ws_byte
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
-    linrec::Shape s = linrec::shape_of(a->cu_seqlens, a->B, a->T, a->D, a->N);
+    linrec::Shape s = linrec::shape_of(a);
     s.status = dev.status;
     s.spin_limit = dev.spin_limit;
     linrec::place_parts(s, ws);
