@@ -308,3 +308,22 @@ def test_bounded_waits_give_up_and_the_next_call_is_right(T, D):
         lib().gdn_set_spin_limit(-1)
     assert all(torch.equal(a, b) for a, b in zip(run(), want))
     assert lib().gdn_sync_status(stream) == 0
+
+
+@pytest.mark.parametrize("D", [64 * 20, 500])
+def test_packed_batches_of_several_waves(D):
+    """More sequences than one wave of CTAs: they are taken longest first, equal and empty ones
+    among them, by single CTAs or clusters; the results are those of each sequence alone."""
+    lengths = [3, 0, 700, 700, 64, 1, 0, 1500, 129, 700, 2, 256, 31, 1500, 90, 5, 128, 127, 640, 77]
+    p = Problem(0, 0, D, "bf16", True, lengths=lengths, seed=D)
+    h, ht = lib().gated_linear_recurrence_fwd(p.x, p.g, p.h0, p.cu, p.scale)
+    want, E, want_t, Et = reference_fwd(p)
+    close("h", h, want, E, "bf16")
+    close("final state", ht, want_t, Et, "fp32")
+    got = lib().gated_linear_recurrence_bwd(p.dh, p.g, h, p.dht, p.h0, p.cu, p.scale)
+    out, err = reference_bwd(p, h)
+    for name, t in zip(("dx", "dg", "dh0", "ds"), got):
+        close(name, t, out[name], err[name], "bf16" if name in ("dx", "dg") else "fp32")
+    again = lib().gated_linear_recurrence_bwd(p.dh, p.g, h, p.dht, p.h0, p.cu, p.scale)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert lib().gdn_sync_status(torch.cuda.current_stream().cuda_stream) == 0
