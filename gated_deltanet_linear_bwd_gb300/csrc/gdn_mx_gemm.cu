@@ -263,6 +263,7 @@ struct PairArgs {
     int m_tiles, n_tiles;
     int rows_first;                                  // the order of tiles: rows of tiles are done one after the other
     int early_w;                                     // as in GemmArgs
+    void *direct;                                    // C, where its rows start on no 16 bytes; null: TMA stores it
     Unquantised rest;
     int *status;
     long long spin_limit;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_ke
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_sx);
         tc::prefetch_map(&map_sw);
-        tc::prefetch_map(&map_c);
+        if (!a.direct) tc::prefetch_map(&map_c);
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
@@ -446,7 +447,9 @@ __global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_ke
         }
     } else {
         // epilogue: each warp takes its 32 rows, 64 (bf16) or 32 (fp32) columns at a time,
-        // through a swizzled block of its own to a TMA store
+        // through a swizzled block of its own to a TMA store, or, where C's rows start on no
+        // 16 bytes, to plain stores along them (2048 x 50257 x 2048 4 bits 126 us, single
+        // CTAs 196)
         asm volatile("griddepcontrol.wait;" ::: "memory");   // C may be written
         const int quarter = warp & 3;
         uint8_t *buf = stage_out + quarter * kPairOut;
@@ -480,6 +483,20 @@ __global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_ke
                         for (int k = 0; k < 8; ++k)
                             *reinterpret_cast<float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4)) =
                                 make_float4(v[32 * b + 4 * k], v[32 * b + 4 * k + 1], v[32 * b + 4 * k + 2], v[32 * b + 4 * k + 3]);
+                    }
+                    if (a.direct) {
+                        __syncwarp();
+                        const int c0 = feat + col + b * kCols, rows = min(32, a.M - row);
+                        TO *out = reinterpret_cast<TO *>(a.direct) + (long long)row * a.N + c0;
+                        for (int r = 0; r < rows; ++r, out += a.N)
+#pragma unroll
+                            for (int e = lane; e < kCols; e += 32) {
+                                const int at = e * (int)sizeof(TO), chunk = (at >> 4) ^ (r & 7);
+                                if (c0 + e < a.N)
+                                    out[e] = *reinterpret_cast<const TO *>(buf + r * 128 + (chunk << 4) + (at & 15));
+                            }
+                        __syncwarp();
+                        continue;
                     }
                     tc::fence_proxy_async();
                     __syncwarp();
@@ -530,13 +547,15 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
     g.spin_limit = dev.spin_limit;
     const long long bytes = FP4 ? a->K / 2 : a->K;
     const int st = FP4 ? 2 : 1;
-    CUtensorMap mx, mw, msx, msw, mc;
+    g.direct = (long long)a->N * (int)sizeof(TO) % 16 ? a->c : nullptr;
+    CUtensorMap mx, mw, msx, msw, mc = {};
     cudaError_t e;
     if ((e = tc::make_map_bytes(&mx, a->a, a->M, bytes, 128)) != cudaSuccess ||
         (e = tc::make_map_bytes(&mw, a->b, a->N, bytes, 128)) != cudaSuccess ||
         (e = tc::make_map_scales(&msx, a->a_scales, (a->M + 127) / 128, g.ktiles, st, 1)) != cudaSuccess ||
         (e = tc::make_map_scales(&msw, a->b_scales, (a->N + 127) / 128, g.ktiles, st, 2)) != cudaSuccess ||
-        (e = tc::make_map_rows(&mc, a->c, a->M, a->N, sizeof(TO), 128 / (int)sizeof(TO), 32, true)) != cudaSuccess)
+        (!g.direct &&
+         (e = tc::make_map_rows(&mc, a->c, a->M, a->N, sizeof(TO), 128 / (int)sizeof(TO), 32, true)) != cudaSuccess))
         return cuda_fail(e, "tensor map of a product");
     const size_t smem = kPairStages * pair_stage_bytes<FP4>() + 4 * kPairOut + sizeof(PairControl);
     auto k = gemm_pair_kernel<FP4, TO>;
@@ -556,17 +575,17 @@ int token_tile(int tokens) {
     return nt;
 }
 
-// Pairs take over from single CTAs where those fill the GPU without sharing K, unless few
-// tokens leave most of a pair's tile idle, and TMA can store C's rows (which start on 16
-// bytes).  Us of single CTAs | pairs in 4 bits at K = 4096: 256 x 4096 10.3 | 11.2, 384 x
-// 4096 13.2 | 10.8, 128 x 12288 13.2 | 11.3, 7 x 12288 7.1 | 11.5, 512 x 1024 7.4 | 10.6,
-// 1536 x 1024 14 | 10.8.
+// Pairs take over from single CTAs where those fill the GPU without sharing K (twice over
+// where TMA cannot store C's rows, which start on no 16 bytes), unless few tokens leave most
+// of a pair's tile idle.  Us of single CTAs | pairs in 4 bits at K = 4096: 256 x 4096 10.3 |
+// 11.2, 384 x 4096 13.2 | 10.8, 128 x 12288 13.2 | 11.3, 7 x 12288 7.1 | 11.5, 512 x 1024 7.4 |
+// 10.6, 1536 x 1024 14 | 10.8; 300 x 4097 10.9 | 13.2, 1000 x 4099 19 | 14, 512 x 12289 26 | 20.
 bool pair_fits(const gdn_mx_matmul_args *a, int sms) {
     const int nt = token_tile(a->M);
     const long long singles = (long long)((a->N + kFeat - 1) / kFeat) * ((a->M + nt - 1) / nt);
     const long long tiles = (long long)((a->M + 255) / 256) * ((a->N + 255) / 256);
-    return (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0 && nt > 32 && 2 * singles > sms &&
-           tiles < (1ll << 30);
+    const bool rows16 = (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0;
+    return nt > 32 && (rows16 ? 2 : 1) * singles > sms && tiles < (1ll << 30);
 }
 
 // Rows to quantise ahead of the product: those of the pairs' first tiles (in 4 bits, whose

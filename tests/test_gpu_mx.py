@@ -196,7 +196,7 @@ def test_refusals():
 
 # mx_linear of sizes at which the product quantises most rows itself: whole and ragged tiles of
 # rows, an odd number of 128-row blocks, K of several strips and of a part of one, either type
-FUSED = [(5200, 4096, 2048), (5376, 4104, 4160), (3201, 8200, 2080), (5150, 4360, 8352)]
+FUSED = [(5200, 4096, 2048), (5376, 4104, 4160), (3201, 8200, 2080), (5150, 4360, 8352), (5130, 4099, 2048)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -226,3 +226,15 @@ def test_linear_on_two_streams_at_once():
                 got[i].append(lib().mx_linear(xs[i], w))
     torch.cuda.synchronize()
     assert all(torch.equal(c, want[i]) for i in (0, 1) for c in got[i])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("M,N,K", [(2048, 2049, 512), (2307, 2571, 544), (1900, 5003, 96), (700, 12290, 288), (4097, 3337, 32)])
+def test_large_products_of_odd_widths(M, N, K, fmt):
+    """Rows of C that start on no 16 bytes (bf16 and fp32), from the kernel of large products."""
+    test_product(M, N, K, fmt)
+    x, w = draw(M, K, 1), lib().mx_quantize(draw(N, K, 2), fmt)
+    wide = lib().mx_quantize(draw(N, K, 2)[:N - N % 8], fmt)          # a width that TMA stores
+    a = lib().mx_quantize(x, fmt)
+    for dt in DT.values():
+        assert torch.equal(lib().mx_matmul(a, w, dt)[:, :N - N % 8], lib().mx_matmul(a, wide, dt))
