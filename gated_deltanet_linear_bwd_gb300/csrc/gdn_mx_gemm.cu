@@ -359,11 +359,11 @@ __global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_ke
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const int2 at = pair_tile(a, tile);
             const int row = at.x * 2 + rank, feat = at.y * 2;    // in 128s
-            if (!weights && row >= ready && row * 128 < a.M) {
-                ok = tc::word_spin(a.rest.work + 1 + row, (128u >> a.rest.log_rows) * a.rest.strips, a.spin_limit, a.status);
-                if (!ok) break;
-                ready = row + 1;
-            }
+            // a wait that gives up is reported and the last one; every stage is filled all the
+            // same, as the other loading warp has counted on it
+            if (!weights && row >= ready && row * 128 < a.M)
+                ready = tc::word_spin(a.rest.work + 1 + row, (128u >> a.rest.log_rows) * a.rest.strips, a.spin_limit,
+                                      a.status) ? row + 1 : 2 * a.m_tiles;
             for (int kb = 0; kb < a.kblocks; ++kb, ++i) {
                 if (i >= kPairStages) {
                     ok = tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status);

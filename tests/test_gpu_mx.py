@@ -238,3 +238,18 @@ def test_large_products_of_odd_widths(M, N, K, fmt):
     a = lib().mx_quantize(x, fmt)
     for dt in DT.values():
         assert torch.equal(lib().mx_matmul(a, w, dt)[:, :N - N % 8], lib().mx_matmul(a, wide, dt))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_linear_whose_waits_give_up_and_the_next_call_is_right(fmt):
+    x, w = draw(5200, 2048, 1), lib().mx_quantize(draw(4096, 2048, 2), fmt)
+    want = lib().mx_matmul(lib().mx_quantize(x, fmt), w)
+    stream = torch.cuda.current_stream().cuda_stream
+    try:
+        lib().gdn_set_spin_limit(0)
+        lib().mx_linear(x, w)
+        assert lib().gdn_sync_status(stream) == 5
+    finally:
+        lib().gdn_set_spin_limit(-1)
+    assert torch.equal(lib().mx_linear(x, w), want)
+    assert lib().gdn_sync_status(stream) == 0
