@@ -745,10 +745,12 @@ constexpr int kSms = 152;          // of the GPU that the choices below are made
 // CTAs per SM) empty and the sequences have a tile for each; of a packed batch, whose
 // longest sequence may be the last to end, up to twice that (us of 16 x (512 .. 8192) tokens
 // x 1000 gated bf16 forward, backward: 119, 193 in single CTAs, 79, 128 in pairs, 87, 138 in
-// fours; 16 x 4096 tokens each 74, 124 and 84, 133).
+// fours; 16 x 4096 tokens each 74, 124 and 84, 133).  Clusters of c leave about c SMs without
+// one (74 of 4 fit, 36 of 8), and one cluster too many takes a second wave: 2 x 8192 x 2432
+// fp32 147 us in 76 clusters of 4, 130 in as many of 2.
 int cluster_of(long long clusters, long long mean_len, bool packed) {
     int c = 1;
-    while (c < kMaxCluster && clusters * c <= (packed ? 2 : 1) * kSms && mean_len > (long long)c * 128) c *= 2;
+    while (c < kMaxCluster && clusters * c <= (packed ? 2 : 1) * (kSms - 2 * c) && mean_len > (long long)c * 128) c *= 2;
     return c;
 }
 
@@ -764,11 +766,12 @@ struct Kind {
 // forward 9.5 | 9.1, backward 15.8 | 12.1; 16384 x 64 30 | 12, 50 | 15, in fp32 65 | 17, 144 |
 // 24; 65536 x 1024 151 | 117, 252 | 157; but fp32 and not gated 187 | 204, 309 | 258.
 int parts_of(long long clusters, int cluster, long long mean_len, const Kind &k, double bytes) {
-    if (cluster < kMaxCluster) return 1;
+    if (cluster < 4) return 1;
     const long long parts = std::min(2 * kSms / clusters, mean_len / 128);
     if (parts < 2) return 1;
     const double tile = (k.fp32 ? (k.gated ? 3.3 : 1.8) : k.tma ? 1.2 : 2.2) * (k.back ? 1.6 : 1.0);
-    const long long rounds = (mean_len + 1023) / 1024, tiles = 2 * ((mean_len + 128 * parts - 1) / (128 * parts));
+    const long long rounds = (mean_len + 128 * cluster - 1) / (128 * cluster);
+    const long long tiles = 2 * ((mean_len + 128 * parts - 1) / (128 * parts));
     const double walks = std::max((double)tiles * tile, bytes * (k.back ? 7 : 5) / 7e6);
     return walks + 5 < (double)rounds * 1.6 * tile ? (int)parts : 1;
 }

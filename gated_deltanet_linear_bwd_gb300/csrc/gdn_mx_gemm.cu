@@ -625,13 +625,17 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w
     // cluster), while slots of the GPU are empty: two CTAs to an SM and up to 8 to a cluster
     // for few tokens; one and up to 4 for many, whose tiles take long to add up (4096 x
     // 4096, 128 tokens, 4 bits: 7.4 us with 4, 9.7 with 2, 13.5 with 8 at two to an SM).
+    // Clusters of c leave about c SMs without one (37 of 4 fit, 36 of 8 at two to an SM), and
+    // one cluster too many takes a second wave: 191 x 2432 x 4096 8 bits 14.7 us with 4, 11.7
+    // with 2; 20 x 4864 x 4096 in 38 of 4 10.1 us at one to an SM, 6.3 at two.
     const long long tiles = (long long)((a->N + kFeat - 1) / kFeat) * g.token_tiles;
     const bool few = g.nt <= 32;
     int splits = 1;
-    while (splits < (few ? kMaxSplits : 4) && 2 * splits <= g.kblocks && 2 * splits * tiles <= (few ? 2 : 1) * dev.sms)
+    while (splits < (few ? kMaxSplits : 4) && 2 * splits <= g.kblocks &&
+           2 * splits * tiles <= (few ? 2 : 1) * (dev.sms - 2 * splits))
         splits *= 2;
     const int per = (g.kblocks + splits - 1) / splits;
-    g.stages = std::max(1, std::min({kMaxStages, per, (tiles * splits <= dev.sms ? 200 : 100) * 1024 / g.stage_bytes}));
+    g.stages = std::max(1, std::min({kMaxStages, per, (tiles * splits <= dev.sms - splits ? 200 : 100) * 1024 / g.stage_bytes}));
     g.early_w = early_w;
     g.tmem_cols = 32;
     while (g.tmem_cols < g.nt + 16) g.tmem_cols *= 2;
