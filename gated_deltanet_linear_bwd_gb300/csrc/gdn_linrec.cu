@@ -73,15 +73,23 @@ __device__ __forceinline__ float bounded(float x) { return fminf(x, 3e38f); }
 // A token's gate: the decay a = exp(l) with l = g, or -s softplus(g); and for the
 // backward pass softplus(g) in units of kUnit and its derivative, the logistic function.
 //
-// fp32 tensors take the accurate functions.  For bf16 ones the two exponentials and
-// the logarithm are the hardware's (about 1e-7 in the log decay, far below the 2^-9
-// of the input's own rounding): with the accurate ones the pass is bound by
-// arithmetic (106 instructions for a token of two channels, 46% of the memory rate;
-// 40 in this form).  But a slow channel multiplies a thousand decays near 1 together,
-// and the hardware exponential's errors there lean one way (2e-8 on average, 2e-5 in
-// the fp32 state of such a channel).  So 2^y is its Taylor polynomial to the fifth
-// power for |y| < 1/8, off by (y ln 2)^6 / 720 < 6e-10 and otherwise by roundings
-// that point either way.
+// fp32 tensors take the accurate functions.  For bf16 ones the two exponentials and the
+// logarithm are the hardware's: with the accurate ones the pass is bound by arithmetic (106
+// instructions for a token of two channels, 46% of the memory rate; about 50 in this form).
+// What a slow channel needs of them is small relative errors of the log decay, however small
+// that is:
+// - It multiplies a thousand decays near 1 together, and the hardware exponential's errors
+//   there lean one way (2e-8 on average, 2e-5 in the fp32 state of such a channel).  So for
+//   |y| < 1/32 2^y is 1 + y q(y), q the polynomial through (2^y - 1) / y at the three Chebyshev
+//   points of -1/32 .. 1/32: off by 1.1e-7 of y, and by a rounding that points either way.
+// - softplus(g) ~ e^g of a steady logit of -15 decides what is left after 65536 tokens, and
+//   d(gate_scale) is a sum of such terms.  The logarithm of the rounded 1 + e^g loses it (1% at
+//   -12, all of it at -17).  So for e < 1/8 log2(1 + e) is e p(e), p the polynomial through
+//   log2(1 + e) / e at the four Chebyshev points of 0 .. 1/8: off by 3.1e-7 of itself, where the
+//   logarithm of a larger e is off by 2^-22 of at least 0.17.  e^g itself is off by 2^-23 |g| of
+//   itself, the rounding of its exponent.  (One polynomial of eight terms for all e needs no
+//   logarithm and took longer, the FMA pipe being the fuller one: 65536 x 2048 forward 163 us
+//   against 159, backward 273 against 263.)
 template <typename T, bool GATED>
 struct Gate {
     static constexpr float kUnit = 1.f;      // of softplus
@@ -108,16 +116,19 @@ struct Gate<__nv_bfloat16, GATED> {
     static __device__ __forceinline__ float2 decay(float2 g, float2 s, float2 &sp) {
         float2 y = mul2(g, both(kLog2e));
         if (GATED) {
-            const float2 u = add2(make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y))), both(1.f));
-            sp = add2(make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)), make_float2(lg2(u.x), lg2(u.y)));
+            const float2 e = make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y)));
+            const float2 u = add2(e, both(1.f));
+            float2 q = fma2(e, both(-2.9770274392e-1f), both(4.7618794121e-1f));
+            q = fma2(q, e, both(-7.2123178461e-1f));
+            q = mul2(fma2(q, e, both(1.4426945903f)), e);
+            sp = add2(make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)),
+                      make_float2(e.x < 0.125f ? q.x : lg2(u.x), e.y < 0.125f ? q.y : lg2(u.y)));
             y = mul2(sp, make_float2(-s.x, -s.y));
         }
-        float2 p = fma2(y, both(1.3333558146e-3f), both(9.6181291076e-3f));
-        p = fma2(p, y, both(5.5504108665e-2f));
-        p = fma2(p, y, both(2.4022650696e-1f));
+        float2 p = fma2(y, both(5.5505085252e-2f), both(2.4023355157e-1f));
         p = fma2(p, y, both(kLn2));
         p = fma2(p, y, both(1.f));
-        return make_float2(fabsf(y.x) < 0.125f ? p.x : ex2(y.x), fabsf(y.y) < 0.125f ? p.y : ex2(y.y));
+        return make_float2(fabsf(y.x) < 0.03125f ? p.x : ex2(y.x), fabsf(y.y) < 0.03125f ? p.y : ex2(y.y));
     }
     // the logistic function is e^g / (1 + e^g) = 2^(g log2 e - softplus(g)); an infinite g
     // as the largest number, whose softplus it is too
