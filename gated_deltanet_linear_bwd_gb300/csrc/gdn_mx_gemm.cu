@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kFeat = 128;         // features of a tile
 constexpr int kThreads = 192;      // producer, MMA and four epilogue warps
+constexpr int kTmemBarrier = 1;    // named: TMEM is there, and waits with a limit may begin
 constexpr int kMaxStages = 10;
 constexpr int kMaxSplits = 8;
 
@@ -33,7 +34,8 @@ struct GemmArgs {
     int kblocks, ktiles;           // 128-byte blocks of K, scale tiles along K
     int stages, stage_bytes, tmem_cols;
     int c_fp32;
-    int early_w;                   // the weight was complete before the kernel ahead of this one began
+    int early_w;                   // the kernel ahead of this one began when all before it, the weight's
+                                   // writers among them, had ended, and takes no TMEM
     int *status;
     long long spin_limit;
 };
@@ -93,14 +95,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         ctl.failed = 0;
         tc::fence_barrier_init();
     }
-    if (warp == 1) {
-        tc::tmem_alloc(&ctl.tmem, (uint32_t)a.tmem_cols);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
     __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem = ctl.tmem;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const uint32_t x_off = kFeat * 128, sw_off = x_off + a.nt * 128, sx_off = sw_off + kScaleTiles * 512;
@@ -123,22 +118,34 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         asm volatile("griddepcontrol.wait;" ::: "memory");
         int i = 0, s = 0;
         uint32_t parity = 1;                         // of the stage's last release; the first round has none
-        for (; i < n; ++i) {
-            if (i >= a.stages) {
-                if (!tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status)) {
-                    ctl.failed = 1;
-                    break;
-                }
-            }
+        auto fill = [&] {
             const uint32_t st = ring0 + s * a.stage_bytes, bar = full0 + 8 * s;
             if (i >= ahead) load_w(kb0 + i, st, bar);
             load_x(kb0 + i, st, bar);
             if (++s == a.stages) s = 0, parity ^= 1;
+        };
+        for (; i < min(n, a.stages); ++i) fill();
+        tc::named_sync(kTmemBarrier, kThreads);
+        for (; i < n; ++i) {
+            if (!tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status)) {
+                ctl.failed = 1;
+                break;
+            }
+            fill();
         }
         if (lane == 0) ctl.issued = i;
     } else if (warp == 1) {
+        // TMEM is taken once the kernel ahead has ended: if CTAs of that one have yet to take
+        // theirs, they would wait for this one's, and this kernel waits for their end.  With
+        // early_w the kernel ahead takes none, and those before it have ended.
+        if (!a.early_w) asm volatile("griddepcontrol.wait;" ::: "memory");
+        tc::tmem_alloc(&ctl.tmem, (uint32_t)a.tmem_cols);
+        tc::tmem_relinquish();
         asm volatile("griddepcontrol.wait;" ::: "memory");           // waits with a limit begin when work does
-        const uint32_t tsw = tmem + a.nt, tsx = tsw + 4 * kScaleTiles;
+        tc::tc_fence_before();
+        tc::named_sync(kTmemBarrier, kThreads);
+        tc::tc_fence_after();
+        const uint32_t tmem = ctl.tmem, tsw = tmem + a.nt, tsx = tsw + 4 * kScaleTiles;
         for (int kb = kb0; kb < kb1; ++kb) {
             const int i = kb - kb0, s = i % a.stages;
             if (!tc::mbar_spin(tc::smem_u32(&ctl.full[s]), (i / a.stages) & 1, a.spin_limit, a.status)) {
@@ -168,7 +175,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         }
         tc::mma_commit(&ctl.done);
     }
-    if (warp > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // C may be written
+    if (warp > 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");              // C may be written
+        tc::named_sync(kTmemBarrier, kThreads);
+    }
     __syncwarp();
     // every MMA done: the ring is free and the tile is whole
     if (!tc::mbar_wait(&ctl.done, 0, a.spin_limit, a.status)) {
@@ -177,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
     }
     tc::tc_fence_after();
     __syncthreads();
+    const uint32_t tmem = ctl.tmem;
     const bool ok = ctl.failed == 0;
     if (!ok && threadIdx.x == 0)   // a wait gave up: nothing may land after the CTA has gone
         for (int j = max(0, ctl.issued - a.stages); j < ctl.issued; ++j)
@@ -325,7 +336,10 @@ __global__ void __launch_bounds__(kPairThreads + kPairQuantThreads) gemm_pair_ke
         ctl.issued = 0;
         tc::fence_barrier_init();
     }
-    if (warp == 1) tc::tmem_alloc_pair(&ctl.tmem, 512);
+    if (warp == 1) {
+        if (!a.early_w) asm volatile("griddepcontrol.wait;" ::: "memory");   // as in gemm_kernel
+        tc::tmem_alloc_pair(&ctl.tmem, 512);
+    }
     tc::tc_fence_before();
     tc::cluster_sync();                              // both CTAs' barriers and TMEM are there
     tc::tc_fence_after();
@@ -665,8 +679,8 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w
 
 using namespace gdn;
 
-// early_w: the kernel ahead in the stream began only when all before it, the writers of b
-// among them, had ended.
+// early_w: the kernel ahead in the stream is the quantisation, which began only when all before
+// it, the writers of b among them, had ended, and takes no TMEM.
 static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, const mx::Unquantised &rest, void *stream) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->M < 0 || a->N < 0 || a->K < 0)

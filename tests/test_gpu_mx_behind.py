@@ -1,0 +1,31 @@
+"""Products right behind kernels that hold all of an SM's tensor memory, and the other way round: the
+delta rule's walks and products of already quantised matrices, of a K so short that a CTA of theirs
+needs little of an SM, one after the other in one stream."""
+import pytest
+import torch
+
+import gdn_synth
+from gpu_helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 1280, 64), (64, 9728, 64), (128, 2432, 256), (300, 515, 96), (2048, 2056, 64)])
+def test_products_behind_the_delta_rule(M, N, K):
+    gdn = lib()
+    d = gdn_synth.make("training", B=1, T=512, H=160).to("cuda")
+    a, b = gdn.mx_quantize(rand(M, K, seed=1), "mxfp8"), gdn.mx_quantize(rand(N, K, seed=2), "mxfp8")
+    want, want_o = gdn.mx_matmul(a, b), gdn.chunk_gated_delta_rule_fwd(d.q, d.k, d.v, d.g, d.beta)[0]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        o = gdn.chunk_gated_delta_rule_fwd(d.q, d.k, d.v, d.g, d.beta)[0]
+        c = gdn.mx_matmul(a, b)
+        grads = gdn.chunk_gated_delta_rule_bwd(d.q, d.k, d.v, d.g, d.beta, want_o)
+        e = gdn.mx_matmul(a, b)
+        assert torch.equal(c, want) and torch.equal(e, want) and torch.equal(o, want_o)
+    assert all(torch.isfinite(t).all() for t in grads if t is not None)
+    assert gdn.gdn_sync_status(torch.cuda.current_stream().cuda_stream) == 0
