@@ -582,6 +582,16 @@ gdn_status run_pair(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool ea
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "mx product launch");
 }
 
+// Shared memory that a CTA of a cluster takes at least, for its TMEM columns.  Such a CTA holds
+// its columns until the whole cluster has its own; if clusters, of this launch or of another
+// stream's, each held on one SM what another needed there, none would ever end.  So the CTAs that
+// fit an SM by their shared memory (228 KB, 1 KB of each CTA the system's) must fit its 512
+// columns: more than 228 KB / (512 + 32) for each, as columns come by 32.  The pairs take 220 KB
+// for 512.  CTAs of no cluster, here and in the delta rule, end whoever else waits.
+constexpr size_t cluster_smem(int tmem_cols) { return (size_t)tmem_cols * 432 - 1024; }
+static_assert(432 * (512 + 32) > 228 * 1024, "");
+static_assert(kPairStages * pair_stage_bytes<false>() + 4 * kPairOut >= cluster_smem(512), "");
+
 // Tokens of a tile: 16, or as many as there are up to 128.
 int token_tile(int tokens) {
     int nt = 16;
@@ -661,7 +671,8 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w
     if ((e = tc::make_map_bytes(&mapx, a->a, a->M, bytes, g.nt)) != cudaSuccess ||
         (e = tc::make_map_bytes(&mapw, a->b, a->N, bytes, kFeat)) != cudaSuccess)
         return cuda_fail(e, "tensor map of an operand");
-    const size_t smem = std::max(g.stages * g.stage_bytes, g.nt * kFeat * 4) + 1024;
+    size_t smem = std::max(g.stages * g.stage_bytes, g.nt * kFeat * 4) + 1024;
+    if (splits > 1) smem = std::max(smem, cluster_smem(g.tmem_cols));
     auto k = fp4 ? gemm_kernel<true> : gemm_kernel<false>;
     if ((e = allow_smem((const void *)k, smem)) != cudaSuccess)
         return cuda_fail(e, "shared memory of the product");
