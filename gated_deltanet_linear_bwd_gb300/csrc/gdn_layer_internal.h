@@ -48,6 +48,8 @@ cudaError_t allow_smem(const void *kernel, size_t bytes);
 // out[d] = sum over `rows` of partial[row][d], in a fixed order.
 cudaError_t column_sum(const float *partial, int rows, int D, float *out, cudaStream_t s);
 
+// The refusals of gdn_mx_quantize.
+gdn_status check_quantize(const gdn_mx_quantize_args *a);
 // gdn_mx_quantize that also clears `words` words at `work`.
 gdn_status mx_quantize(const gdn_mx_quantize_args *a, uint32_t *work, int words, void *stream);
 

@@ -690,9 +690,7 @@ gdn_status run(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w
 
 using namespace gdn;
 
-// early_w: the kernel ahead in the stream is the quantisation, which began only when all before
-// it, the writers of b among them, had ended, and takes no TMEM.
-static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, const mx::Unquantised &rest, void *stream) {
+static gdn_status check(const gdn_mx_matmul_args *a) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->M < 0 || a->N < 0 || a->K < 0)
         return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
@@ -707,9 +705,15 @@ static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, const mx::Un
     if (misaligned(a->a) || misaligned(a->a_scales) || misaligned(a->b) || misaligned(a->b_scales) ||
         misaligned(a->c))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
-    LayerDevice dev;
-    const gdn_status st = layer_device(&dev);
-    if (st != GDN_OK) return st;
+    return GDN_OK;
+}
+
+// A product whose arguments check() has passed.  early_w: the kernel ahead in the stream is the
+// quantisation, which began only when all before it, the writers of b among them, had ended, and
+// takes no TMEM.
+static gdn_status matmul(const gdn_mx_matmul_args *a, const LayerDevice &dev, bool early_w,
+                         const mx::Unquantised &rest, void *stream) {
+    if (a->M == 0 || a->N == 0) return GDN_OK;
     if (a->K == 0) {
         const cudaError_t e = cudaMemsetAsync(a->c, 0, (size_t)a->M * a->N * (a->out_dtype == GDN_FP32 ? 4 : 2),
                                               (cudaStream_t)stream);
@@ -719,7 +723,11 @@ static gdn_status matmul(const gdn_mx_matmul_args *a, bool early_w, const mx::Un
 }
 
 extern "C" gdn_status gdn_mx_matmul(const gdn_mx_matmul_args *a, void *stream) {
-    return matmul(a, false, mx::Unquantised{}, stream);
+    gdn_status st = check(a);
+    if (st != GDN_OK || a->M == 0 || a->N == 0) return st;
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    return matmul(a, dev, false, mx::Unquantised{}, stream);
 }
 
 // Bytes of X's elements in the workspace; its scales follow, then the counters of the
@@ -749,11 +757,14 @@ extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_
     uint8_t *data = (uint8_t *)ws, *scales = data + linear_data_bytes(a);
     const gdn_mx_matmul_args m{data, scales, a->w, a->w_scales, a->M, a->N, a->K, a->format, a->out_dtype, a->c};
     gdn_mx_quantize_args q{a->x, a->M, a->K, a->dtype, a->format, data, scales};
+    // everything is checked before the quantisation is launched
+    gdn_status st = check(&m);
+    if (st == GDN_OK) st = check_quantize(&q);
+    if (st != GDN_OK || a->M == 0 || a->N == 0) return st;
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
     mx::Unquantised rest{};
-    if (a->M >= 512 && a->N > 0 && a->K % 32 == 0) {           // at least two tiles of rows
-        LayerDevice dev;
-        const gdn_status st = layer_device(&dev);
-        if (st != GDN_OK) return st;
+    if (a->M >= 512) {                                         // at least two tiles of rows
         q.rows = mx::rows_ahead(&m, dev.sms);
         if (q.rows < a->M) {
             uint32_t *work = (uint32_t *)(scales + gdn_mx_scale_bytes(a->M, a->K));
@@ -763,7 +774,6 @@ extern "C" gdn_status gdn_mx_linear(const gdn_mx_linear_args *a, void *ws, size_
             rest = {a->x, a->dtype == GDN_FP32, q.rows, (spans + mx::kStrip - 1) / mx::kStrip, log_rows, data, scales, work};
         }
     }
-    const gdn_status st = mx_quantize(&q, rest.work, rest.x ? linear_words(a) : 0, stream);
-    if (st != GDN_OK) return st;
-    return matmul(&m, a->M > 0 && a->K > 0, rest, stream);
+    if ((st = mx_quantize(&q, rest.work, rest.x ? linear_words(a) : 0, stream)) != GDN_OK) return st;
+    return matmul(&m, dev, a->K > 0, rest, stream);
 }

@@ -104,14 +104,19 @@ gdn_status check(int rows, int K, int dtype, int format) {
 }  // namespace
 }  // namespace mx
 
-gdn_status mx_quantize(const gdn_mx_quantize_args *a, uint32_t *work, int words, void *stream) {
+gdn_status check_quantize(const gdn_mx_quantize_args *a) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
-    gdn_status st = mx::check(a->rows, a->K, a->dtype, a->format);
-    if (st != GDN_OK) return st;
-    if (a->rows == 0 || a->K == 0) return GDN_OK;
+    const gdn_status st = mx::check(a->rows, a->K, a->dtype, a->format);
+    if (st != GDN_OK || a->rows == 0 || a->K == 0) return st;
     if (!a->x || !a->data || !a->scales) return fail(GDN_ERR_INVALID_ARG, "x, data and scales are required");
     if (misaligned(a->x) || misaligned(a->data) || misaligned(a->scales))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    return GDN_OK;
+}
+
+gdn_status mx_quantize(const gdn_mx_quantize_args *a, uint32_t *work, int words, void *stream) {
+    gdn_status st = check_quantize(a);
+    if (st != GDN_OK || a->rows == 0 || a->K == 0) return st;
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     const int ktiles = (a->K + 127) / 128, spans = (ktiles + 1) / 2;

@@ -1,0 +1,22 @@
+"""Host-side refusals of the microscaled operators: bad arguments of the linear entry before it
+launches anything (here, without a GPU, anything that it would launch is another error)."""
+import pytest
+
+from test_abi_layer import abi, call  # noqa: F401  (a fixture)
+
+
+@pytest.mark.parametrize("bad,rc,msg", [
+    (dict(w=None), 1, "required"), (dict(w_scales=None), 1, "required"), (dict(c=None), 1, "required"),
+    (dict(w=4100), 1, "aligned"), (dict(w_scales=4104), 1, "aligned"), (dict(c=4098), 1, "aligned"),
+    (dict(x=4098), 1, "aligned"), (dict(N=-1), 1, "bad sizes"), (dict(out_dtype=7), 2, "out_dtype"),
+    (dict(format=2), 2, "format"), (dict(dtype=5), 2, "dtype"), (dict(out_dtype=7, M=1000), 2, "out_dtype"),
+    (dict(c=4098, M=1000), 1, "aligned"),
+])
+def test_linear_checks_everything_before_it_launches(abi, bad, rc, msg):
+    assert call(abi, "gdn_mx_linear", **bad) == rc
+    assert msg in abi._abi.gdn_last_error()
+
+
+def test_linear_of_no_rows_or_columns_launches_nothing(abi):
+    assert call(abi, "gdn_mx_linear", M=0) == 0
+    assert call(abi, "gdn_mx_linear", N=0) == 0
