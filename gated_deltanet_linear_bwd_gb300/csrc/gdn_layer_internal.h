@@ -53,6 +53,10 @@ gdn_status check_quantize(const gdn_mx_quantize_args *a);
 // gdn_mx_quantize that also clears `words` words at `work`.
 gdn_status mx_quantize(const gdn_mx_quantize_args *a, uint32_t *work, int words, void *stream);
 
+// Rows and columns of a microscaled matrix: what is rounded up to whole tiles, and walked past
+// by one, stays an int.
+constexpr int kMaxExtent = (int)((1ll << 31) - (1 << 16));
+
 inline bool misaligned(const void *p) { return ((uintptr_t)p & 15u) != 0; }
 
 }  // namespace gdn

@@ -107,10 +107,10 @@ __global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ 
         auto load_w = [&](int kb, uint32_t st, uint32_t bar) {       // arms the stage for all it gets
             const uint32_t sb = tile_bytes(kb);
             tc::expect_bytes(bar, (uint32_t)(kFeat + a.nt) * 128u + 2u * sb, true);
-            tc::load_operand(st, &map_w, kb * 128, f0, st + sw_off, sw + kb * (512 * kScaleTiles), sb, bar);
+            tc::load_operand(st, &map_w, kb * 128, f0, st + sw_off, sw + kb * (512ll * kScaleTiles), sb, bar);
         };
         auto load_x = [&](int kb, uint32_t st, uint32_t bar) {
-            tc::load_operand(st + x_off, &map_x, kb * 128, t0, st + sx_off, sx + kb * (512 * kScaleTiles), tile_bytes(kb), bar);
+            tc::load_operand(st + x_off, &map_x, kb * 128, t0, st + sx_off, sx + kb * (512ll * kScaleTiles), tile_bytes(kb), bar);
         };
         // a ring's worth of weights may come before the kernel ahead has written the tokens
         const int ahead = a.early_w ? min(n, a.stages) : 0;
@@ -694,6 +694,8 @@ static gdn_status check(const gdn_mx_matmul_args *a) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
     if (a->M < 0 || a->N < 0 || a->K < 0)
         return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d N=%d K=%d", a->M, a->N, a->K);
+    if (std::max({a->M, a->N, a->K}) > kMaxExtent)
+        return fail(GDN_ERR_INVALID_ARG, "problem too large: M=%d N=%d K=%d", a->M, a->N, a->K);
     if (a->K % 32 != 0) return fail(GDN_ERR_UNSUPPORTED, "K = %d (a multiple of 32)", a->K);
     if (a->format != GDN_MXFP8 && a->format != GDN_MXFP4)
         return fail(GDN_ERR_UNSUPPORTED, "format %d is not GDN_MXFP8 or GDN_MXFP4", a->format);
@@ -743,6 +745,10 @@ static int linear_words(const gdn_mx_linear_args *a) { return 1 + (int)((a->M + 
 extern "C" size_t gdn_mx_linear_workspace_size(const gdn_mx_linear_args *a) {
     if (!a || a->M < 0 || a->K < 0) {
         fail(GDN_ERR_INVALID_ARG, "null args or bad sizes");
+        return 0;
+    }
+    if (std::max(a->M, a->K) > kMaxExtent) {
+        fail(GDN_ERR_INVALID_ARG, "problem too large: M=%d K=%d", a->M, a->K);
         return 0;
     }
     return std::max<size_t>(256, linear_data_bytes(a) + gdn_mx_scale_bytes(a->M, a->K) + 4 * (size_t)linear_words(a));

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *data, co
 
 gdn_status check(int rows, int K, int dtype, int format) {
     if (rows < 0 || K < 0) return fail(GDN_ERR_INVALID_ARG, "bad sizes rows=%d K=%d", rows, K);
+    if (K > kMaxExtent) return fail(GDN_ERR_INVALID_ARG, "problem too large: K=%d", K);
     if (K % 32 != 0) return fail(GDN_ERR_UNSUPPORTED, "K = %d (a multiple of 32)", K);
     if (dtype != GDN_FP32 && dtype != GDN_BF16)
         return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", dtype);

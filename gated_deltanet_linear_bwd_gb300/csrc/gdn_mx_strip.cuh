@@ -68,7 +68,7 @@ __device__ __forceinline__ void quantize_strip(const T *x, uint8_t *data, uint8_
     const long long at = row * K + first * 256 + lane * 8;
     const T *px = x + at;
     uint8_t *pd = data + (FP4 ? at / 2 : at);
-    uint8_t *ps = scales + scale_offset(row, 0, ktiles) + (2 * first + (lane >> 4)) * 512;
+    uint8_t *ps = scales + scale_offset(row, 0, ktiles) + (2ll * first + (lane >> 4)) * 512;
     for (int span = first; span < end; span += kSpans) {
         const int col = span * 256 + lane * 8;
         auto inside = [&](int u) { return ROWS ? row + u < rows && col < K : row < rows && col + 256 * u < K; };

@@ -100,7 +100,9 @@ gdn_status gdn_linrec_step(const gdn_linrec_step_args *args, void *stream);
  * the scaled elements to nearest, ties to even: nothing saturates.  (The rounded-
  * down exponent that is the usual choice lets the largest element of a block
  * saturate, an error of up to 1/8 for e4m3 and 1/4 for e2m1 in the element that
- * matters most.)  A block that holds a NaN or an infinity gets a NaN scale. */
+ * matters most.)  A block that holds a NaN or an infinity gets a NaN scale.
+ *
+ * K, and M and N of a product, are at most 2^31 - 2^16. */
 enum { GDN_MXFP8 = 0, GDN_MXFP4 = 1 };
 
 /* Bytes of the scales of a [rows, K] matrix (0 for rows or K of none). */

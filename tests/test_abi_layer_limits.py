@@ -1,8 +1,10 @@
-"""Host-side refusals of the microscaled operators: bad arguments of the linear entry before it
-launches anything (here, without a GPU, anything that it would launch is another error)."""
+"""Host-side refusals of the microscaled operators: sizes near 2^31, and bad arguments of the linear
+entry before it launches anything (here, without a GPU, anything that it would launch is another error)."""
 import pytest
 
-from test_abi_layer import abi, call  # noqa: F401  (a fixture)
+from test_abi_layer import abi, call, raw  # noqa: F401  (a fixture)
+
+TOP = 2 ** 31 - 1
 
 
 @pytest.mark.parametrize("bad,rc,msg", [
@@ -20,3 +22,20 @@ def test_linear_checks_everything_before_it_launches(abi, bad, rc, msg):
 def test_linear_of_no_rows_or_columns_launches_nothing(abi):
     assert call(abi, "gdn_mx_linear", M=0) == 0
     assert call(abi, "gdn_mx_linear", N=0) == 0
+
+
+@pytest.mark.parametrize("name,big", [
+    ("gdn_mx_quantize", dict(K=2 ** 31 - 32)), ("gdn_mx_dequantize", dict(K=2 ** 31 - 32)),
+    ("gdn_mx_matmul", dict(M=TOP, N=1, K=32)), ("gdn_mx_matmul", dict(M=1, N=TOP - 100, K=32)),
+    ("gdn_mx_matmul", dict(K=2 ** 31 - 32)),
+    ("gdn_mx_linear", dict(M=TOP, N=1, K=32)), ("gdn_mx_linear", dict(M=1, N=TOP - 100, K=32)),
+    ("gdn_mx_linear", dict(K=2 ** 31 - 64)),
+])
+def test_sizes_whose_arithmetic_would_overflow_are_refused(abi, name, big):
+    assert call(abi, name, **big) == 1
+    assert "too large" in abi._abi.gdn_last_error()
+
+
+def test_no_workspace_is_named_for_them(abi):
+    assert abi.load().gdn_mx_linear_workspace_size(raw(abi, "gdn_mx_linear", M=TOP)) == 0
+    assert "too large" in abi._abi.gdn_last_error()
