@@ -324,7 +324,8 @@ int cta_threads(int tpr) { return std::max(tpr, 256); }
 // are read one by one), since each leaves a row of partial sums of dweight.
 int bwd_ctas(int rows, int dtype, int D, int sms) {
     const int tpr = row_threads(dtype, D, false), threads = cta_threads(tpr), per = threads / tpr;
-    return std::max(1, std::min((rows + per - 1) / per, sms * std::max(1, (vector_rows(dtype, D) ? 2 : 3) * 256 / threads)));
+    const long long most = (long long)sms * std::max(1, (vector_rows(dtype, D) ? 2 : 3) * 256 / threads);
+    return (int)std::max(1ll, std::min((rows + per - 1ll) / per, most));
 }
 
 template <typename T, int VEC, int PER, bool MX>

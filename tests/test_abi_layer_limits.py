@@ -39,3 +39,10 @@ def test_sizes_whose_arithmetic_would_overflow_are_refused(abi, name, big):
 def test_no_workspace_is_named_for_them(abi):
     assert abi.load().gdn_mx_linear_workspace_size(raw(abi, "gdn_mx_linear", M=TOP)) == 0
     assert "too large" in abi._abi.gdn_last_error()
+
+
+def test_the_norms_backward_of_very_many_rows_asks_for_as_many_sums_as_of_fewer(abi):
+    """A row of partial sums of d(weight) for each CTA: as many as the GPU holds, not as many as an int
+    that overflowed says."""
+    size = lambda rows: abi.ENTRIES["gdn_rms_norm_bwd"].workspace_size(raw(abi, "gdn_rms_norm_bwd", rows=rows, D=1))
+    assert size(TOP) == size(2 ** 30) > 1024
