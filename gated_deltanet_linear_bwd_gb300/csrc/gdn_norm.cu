@@ -325,7 +325,7 @@ int cta_threads(int tpr) { return std::max(tpr, 256); }
 int bwd_ctas(int rows, int dtype, int D, int sms) {
     const int tpr = row_threads(dtype, D, false), threads = cta_threads(tpr), per = threads / tpr;
     const long long most = (long long)sms * std::max(1, (vector_rows(dtype, D) ? 2 : 3) * 256 / threads);
-    return (int)std::max(1ll, std::min((rows + per - 1ll) / per, most));
+    return (int)std::max(1ll, std::min((rows - 1ll + per) / per, most));
 }
 
 template <typename T, int VEC, int PER, bool MX>
