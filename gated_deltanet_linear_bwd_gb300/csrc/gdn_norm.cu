@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(FwdArgs a) {
 #pragma unroll
                 for (int o = 1; o < 32 / VEC; o <<= 1)
                     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const int byte = mx::scale_byte<false>(amax);        // 0 where nothing is
+                // 0 where nothing is, whose zeros an infinite or NaN rstd makes NaN
+                const int byte = live && col < a.D ? mx::scale_byte<false>(amax) : 0;
                 if (words) {
                     uint32_t word = (uint32_t)byte << (8 * (col / 32 & 3));
 #pragma unroll
