@@ -25,6 +25,15 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _grad(t):
+    """A gradient as autograd hands it over, contiguous on a 16-byte boundary (a slice of
+    another tensor's may be neither); None stays None."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _need(name, t, dtype, shape, index):
     """_check for a tensor that has to be there: contiguous, on device `index`."""
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
@@ -124,7 +133,7 @@ class _GatedLinearRecurrence(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dh, dht):
         g, h, h0, scale, cu = ctx.saved_tensors
-        out = gated_linear_recurrence_bwd(dh.contiguous(), g, h, dht.contiguous(), h0, cu, scale,
+        out = gated_linear_recurrence_bwd(_grad(dh), g, h, _grad(dht), h0, cu, scale,
                                           want_dh0=h0 is not None)
         return out[0], out[1], out[2], out[3] if scale is not None else None, None
 
@@ -375,8 +384,7 @@ class _AddRmsNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
-        d, dw = add_rms_norm_bwd(dy.contiguous(), s, weight, rstd,
-                                 None if ds is None else ds.contiguous())
+        d, dw = add_rms_norm_bwd(_grad(dy), s, weight, rstd, _grad(ds))
         return d, dw.to(weight.dtype), d if ctx.with_residual else None, None
 
 

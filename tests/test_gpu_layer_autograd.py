@@ -1,0 +1,35 @@
+"""Gradients through the layer operators as autograd delivers and asks for them."""
+import pytest
+import torch
+
+from gpu_helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(*shape, seed=0, dtype=torch.float32):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lead", [1, 3])
+def test_gradients_may_arrive_on_any_address(lead, dtype):
+    """torch.cat along the first axis hands back slices of its gradient: contiguous, but on no
+    16-byte boundary where a row's bytes are no multiple of it."""
+    D = 101
+    x, w, g = rand(6, D, seed=1, dtype=dtype), rand(D, seed=2, dtype=dtype), rand(1, 6, D, seed=3, dtype=dtype)
+    z, up = rand(lead, D, seed=4, dtype=dtype), rand(lead + 6, D, seed=5, dtype=dtype)
+    zt, upt = rand(lead, D, seed=6), rand(lead + 1, D, seed=7)
+    assert up[lead:].data_ptr() % 16
+
+    def grads(join):
+        a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+        y, s = lib().add_rms_norm(a, b, x)
+        h, ht = lib().gated_linear_recurrence(a[None], g, output_final_state=True)
+        return torch.autograd.grad(join(y, s, h[0], ht), (a, b))
+
+    whole = lambda t, rest: torch.cat([rest, t], 0)
+    got = grads(lambda y, s, h, ht: sum((whole(t, z) * up).sum() for t in (y, s, h)) + (whole(ht, zt) * upt).sum())
+    aligned, aligned_t = up[lead:].clone(), upt[lead:].clone()
+    want = grads(lambda y, s, h, ht: sum((t * aligned).sum() for t in (y, s, h)) + (ht * aligned_t).sum())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
