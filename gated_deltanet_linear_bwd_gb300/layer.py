@@ -234,7 +234,7 @@ def _mx_index(name, t, index=None):
 def mx_quantize(x, fmt="mxfp4"):
     """x [..., K] (bf16 or fp32) as an MxTensor of [rows, K]: for each row and 32
     columns the least power-of-two scale with which nothing saturates, elements
-    rounded to nearest even."""
+    rounded to nearest even.  No gradient passes to x."""
     if x.dim() < 1:
         raise ValueError("expected [..., K]")
     _, code, index = _first("x", x)
@@ -270,7 +270,8 @@ def mx_from_parts(data, exponents, fmt):
 
 
 def mx_matmul(a, b, out_dtype=torch.bfloat16):
-    """a b^T of MxTensors a [M, K] and b [N, K] of one format: [M, N], summed in fp32."""
+    """a b^T of MxTensors a [M, K] and b [N, K] of one format: [M, N], summed in fp32.
+    No gradients pass through MxTensors."""
     index = _mx_index("a", a)
     _mx_index("b", b, index)
     if a.fmt != b.fmt or a.shape[1] != b.shape[1]:
@@ -285,12 +286,27 @@ def mx_matmul(a, b, out_dtype=torch.bfloat16):
     return c
 
 
+class _NoBackward(torch.autograd.Function):
+    """mx_linear of a tensor that requires a gradient: the same result, and an error for the
+    loss that reaches it."""
+    @staticmethod
+    def forward(ctx, x, weight, out_dtype):
+        return mx_linear(x, weight, out_dtype)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("mx_linear has no backward pass: call it under torch.no_grad(), or on x.detach()")
+
+
 def mx_linear(x, weight, out_dtype=None):
     """x weight^T for x [..., K] (bf16 or fp32, quantised here to the weight's format,
     or an MxTensor of it) and a weight MxTensor [N, K].  Returns [..., N] in x's type
-    (bf16 for an MxTensor), or in `out_dtype`."""
+    (bf16 for an MxTensor), or in `out_dtype`.  Forward only: a gradient that reaches it
+    raises RuntimeError."""
     if type(x) is MxTensor:
         return mx_matmul(x, weight, out_dtype or torch.bfloat16)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _NoBackward.apply(x, weight, out_dtype)
     dtype, code, index = _first("x", x)
     _mx_index("weight", weight, index)
     N, K = weight._shape

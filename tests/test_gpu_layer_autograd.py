@@ -33,3 +33,20 @@ def test_gradients_may_arrive_on_any_address(lead, dtype):
     aligned, aligned_t = up[lead:].clone(), upt[lead:].clone()
     want = grads(lambda y, s, h, ht: sum((t * aligned).sum() for t in (y, s, h)) + (ht * aligned_t).sum())
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("lead", [(8,), (2, 4)])
+def test_a_loss_through_a_microscaled_product_is_refused(lead):
+    """The product has no backward pass: a gradient that reaches it raises instead of ending there
+    without a word.  Calls that ask for none are what they were."""
+    x, w = rand(*lead, 64, seed=1, dtype=torch.bfloat16), lib().mx_quantize(rand(32, 64, seed=2), "mxfp8")
+    want = lib().mx_linear(x, w)
+    assert not want.requires_grad
+    y = x.clone().requires_grad_()
+    with torch.no_grad():
+        out = lib().mx_linear(y, w)
+    assert torch.equal(out, want) and not out.requires_grad
+    out = lib().mx_linear(y, w, torch.float32)
+    assert torch.equal(out.detach(), lib().mx_linear(x, w, torch.float32))
+    with pytest.raises(RuntimeError, match="no backward"):
+        out.sum().backward()
