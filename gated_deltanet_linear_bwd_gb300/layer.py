@@ -5,6 +5,7 @@ allocate outputs and workspace with torch on the tensors' device and pass raw
 pointers on the current stream; every computation runs in libgdn.so.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _abi_layer
 from .api import _DT, _check
@@ -131,6 +132,7 @@ class _GatedLinearRecurrence(torch.autograd.Function):
         return h, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dht):
         g, h, h0, scale, cu = ctx.saved_tensors
         out = gated_linear_recurrence_bwd(_grad(dh), g, h, _grad(dht), h0, cu, scale,
@@ -398,6 +400,7 @@ class _AddRmsNorm(torch.autograd.Function):
         return (y, s) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, rstd = ctx.saved_tensors
         d, dw = add_rms_norm_bwd(_grad(dy), s, weight, rstd, _grad(ds))

@@ -50,3 +50,14 @@ def test_a_loss_through_a_microscaled_product_is_refused(lead):
     assert torch.equal(out.detach(), lib().mx_linear(x, w, torch.float32))
     with pytest.raises(RuntimeError, match="no backward"):
         out.sum().backward()
+
+
+def test_second_derivatives_are_refused():
+    """The backward passes are not differentiable themselves: backward() through them raises, also
+    where another path from the input has a second derivative."""
+    x, w = rand(4, 64, seed=1).requires_grad_(), rand(64, seed=2)
+    g = rand(1, 4, 64, seed=3)
+    for f in (lambda: lib().add_rms_norm(x, w), lambda: lib().gated_linear_recurrence(x[None], g)[0]):
+        (d,) = torch.autograd.grad(f().square().sum() + x.pow(3).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            d.sum().backward()
