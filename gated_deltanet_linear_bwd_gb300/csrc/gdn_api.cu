@@ -11,7 +11,6 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "gdn.h"
@@ -23,17 +22,15 @@ namespace gdn {
 // One sticky status word per device (module memory, not an allocation).
 static __device__ int g_status_word;
 
-static thread_local std::string t_last_error;
+static thread_local char t_last_error[512];   // no allocation: a refusal may not fail itself
 static constexpr long long kDefaultSpinLimit = 1ll << 21;
 static std::atomic<long long> g_spin_limit{kDefaultSpinLimit};
 
 gdn_status fail(gdn_status code, const char *fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    vsnprintf(t_last_error, sizeof t_last_error, fmt, ap);
     va_end(ap);
-    t_last_error = buf;
     return code;
 }
 
@@ -318,7 +315,7 @@ extern "C" {
 
 int32_t gdn_abi_version(void) { return GDN_ABI_VERSION; }
 
-const char *gdn_last_error(void) { return t_last_error.c_str(); }
+const char *gdn_last_error(void) { return t_last_error; }
 
 void gdn_set_spin_limit(int64_t polls) { g_spin_limit.store(polls < 0 ? kDefaultSpinLimit : polls); }
 

@@ -1,8 +1,7 @@
 // gdn_layer_util.cu -- what the layer operators share: the sum over rows that their
 // weight gradients end with, and the shared-memory limits of their kernels.
-#include <map>
+#include <algorithm>
 #include <mutex>
-#include <utility>
 
 #include "gdn_layer_internal.h"
 
@@ -32,17 +31,26 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial, 
 }  // namespace
 
 cudaError_t allow_smem(const void *kernel, size_t bytes) {
+    // what has been granted; a kernel for which no entry is left is granted it on every call
+    struct Grant {
+        const void *kernel;
+        int dev;
+        size_t bytes;
+    };
     static std::mutex mu;
-    static std::map<std::pair<const void *, int>, size_t> granted;
+    static Grant granted[256];
+    static int n = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    size_t &has = granted[{kernel, dev}];
-    if (has >= bytes) return cudaSuccess;
+    Grant *g = std::find_if(granted, granted + n, [&](const Grant &h) { return h.kernel == kernel && h.dev == dev; });
+    if (g < granted + n && g->bytes >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) has = bytes;
-    return e;
+    if (e != cudaSuccess) return e;
+    if (g < granted + n) g->bytes = bytes;
+    else if (n < 256) granted[n++] = {kernel, dev, bytes};
+    return cudaSuccess;
 }
 
 cudaError_t column_sum(const float *partial, int rows, int D, float *out, cudaStream_t s) {
