@@ -599,17 +599,16 @@ int token_tile(int tokens) {
     return nt;
 }
 
-// Pairs take over from single CTAs where those fill the GPU without sharing K (twice over
-// where TMA cannot store C's rows, which start on no 16 bytes), unless few tokens leave most
-// of a pair's tile idle.  Us of single CTAs | pairs in 4 bits at K = 4096: 256 x 4096 10.3 |
-// 11.2, 384 x 4096 13.2 | 10.8, 128 x 12288 13.2 | 11.3, 7 x 12288 7.1 | 11.5, 512 x 1024 7.4 |
-// 10.6, 1536 x 1024 14 | 10.8; 300 x 4097 10.9 | 13.2, 1000 x 4099 19 | 14, 512 x 12289 26 | 20.
+// Pairs take over from single CTAs where those are more than one wave, unless few tokens leave
+// most of a pair's tile idle.  Us of single CTAs | pairs at K = 4096 in 4 bits: 384 x 4096 10.7 |
+// 11.8, 128 x 16384 10.8 | 12.1, 512 x 12288 21.8 | 18.0; in 8 bits 384 x 4096 15.4 | 16.0, 128 x
+// 16384 15.7 | 17.4, 512 x 12288 31.8 | 27.3; rows of C that start on no 16 bytes, 4 bits: 300 x
+// 4097 10.6 | 13.8, 1000 x 4099 14.5 | 14.4, 512 x 12289 23.2 | 20.6; few tokens, 7 x 12288 6.7 | 16.2.
 bool pair_fits(const gdn_mx_matmul_args *a, int sms) {
     const int nt = token_tile(a->M);
     const long long singles = (long long)((a->N + kFeat - 1) / kFeat) * ((a->M + nt - 1) / nt);
     const long long tiles = (long long)((a->M + 255) / 256) * ((a->N + 255) / 256);
-    const bool rows16 = (long long)a->N * (a->out_dtype == GDN_FP32 ? 4 : 2) % 16 == 0;
-    return nt > 32 && (rows16 ? 2 : 1) * singles > sms && tiles < (1ll << 30);
+    return nt > 32 && singles > sms && tiles < (1ll << 30);
 }
 
 // Rows to quantise ahead of the product: those of the pairs' first tiles (in 4 bits, whose
