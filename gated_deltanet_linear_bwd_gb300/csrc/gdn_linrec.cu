@@ -15,10 +15,10 @@
 // has 8 CTAs at most; long sequences of few channels are instead cut into parts that are
 // walked twice, first for their pairs alone, then, the pairs joined, for the results.
 //
-// Bound by memory: 16 x (512 .. 8192) tokens x 4096 gated bf16 forward 257 us, 98% of
-// the measured copy rate; 4 x 4096 x 4096 backward 114 us, 87% (the gate's arithmetic
-// takes the issue slots); 65536 x 2048 in clusters of 8 157 us, 76% (the rounds' length:
-// each waits for the slowest of 8 CTAs).
+// Bound by memory and, gated, nearly as much by the gate's arithmetic: 16 x (512 .. 8192) tokens
+// x 4096 gated bf16 forward 262 us, 96% of the measured copy rate; 4 x 4096 x 4096 backward 118
+// us, 84%; 65536 x 2048 in clusters of 8 159 us, 75% (the rounds' length: each waits for the
+// slowest of 8 CTAs).
 #include <algorithm>
 #include <type_traits>
 
@@ -75,7 +75,7 @@ __device__ __forceinline__ float bounded(float x) { return fminf(x, 3e38f); }
 //
 // fp32 tensors take the accurate functions.  For bf16 ones the two exponentials and the
 // logarithm are the hardware's: with the accurate ones the pass is bound by arithmetic (106
-// instructions for a token of two channels, 46% of the memory rate; about 50 in this form).
+// instructions for a token of two channels, 46% of the memory rate; 44 in this form).
 // What a slow channel needs of them is small relative errors of the log decay, however small
 // that is:
 // - It multiplies a thousand decays near 1 together, and the hardware exponential's errors
@@ -170,7 +170,7 @@ __device__ __forceinline__ void range(const Shape &s, int n, long long &bos, lon
 
 // The sequence of the `j`-th CTAs of a packed batch whose CTAs come in several waves: the
 // j-th longest, so that no long one is left for the end.  16 x (512 .. 8192) tokens x 4096
-// gated bf16 forward, backward, the longest last: 299, 527 us in order, 258, 459 so.
+// gated bf16 forward, backward, the longest last: 303, 535 us in order, 262, 447 so.
 constexpr int kMaxOrdered = 128;
 __device__ __forceinline__ int sequence_of(const Shape &s, int j, void *scratch) {
     if (!s.longest_first) return j;
@@ -741,8 +741,8 @@ int group_lanes(int N, int groups) {
 
 // Warps, tokens to a warp and stages: about 100 KB of tiles to a CTA, two CTAs to an SM.
 // Every warp reads every warp's pair, so that few warps with many tokens each do best:
-// forward, 65536 x 2048 gated bf16, 8 warps of 16 tokens 194 us, 4 of 32 163 us, 16 of 8
-// 490 us; backward, 4 x 4096 x 4096, 8 of 8 126 us, 4 of 16 114 us, 6 of 10 130 us.
+// forward, 65536 x 2048 gated bf16, 8 warps of 16 tokens 198 us, 4 of 32 160 us, 16 of 8
+// 437 us; backward, 4 x 4096 x 4096, 8 of 8 130 us, 4 of 16 119 us, 6 of 10 132 us.
 template <typename T>
 struct Tiles {
     static constexpr bool kHalf = sizeof(T) == 2;
@@ -755,10 +755,10 @@ constexpr int kSms = 152;          // of the GPU that the choices below are made
 // CTAs that share a sequence: doubled while the grid leaves slots of the GPU (two
 // CTAs per SM) empty and the sequences have a tile for each; of a packed batch, whose
 // longest sequence may be the last to end, up to twice that (us of 16 x (512 .. 8192) tokens
-// x 1000 gated bf16 forward, backward: 119, 193 in single CTAs, 79, 128 in pairs, 87, 138 in
-// fours; 16 x 4096 tokens each 74, 124 and 84, 133).  Clusters of c leave about c SMs without
+// x 1000 gated bf16 forward, backward: 124, 202 in single CTAs, 81, 129 in pairs, 89, 139 in
+// fours; 16 x 4096 tokens each 77, 121 in single CTAs, 86, 136 in pairs).  Clusters of c leave about c SMs without
 // one (74 of 4 fit, 36 of 8), and one cluster too many takes a second wave: 2 x 8192 x 2432
-// fp32 147 us in 76 clusters of 4, 130 in as many of 2.
+// fp32 146 us in 76 clusters of 4, 130 in as many of 2.
 int cluster_of(long long clusters, long long mean_len, bool packed) {
     int c = 1;
     while (c < kMaxCluster && clusters * c <= (packed ? 2 : 1) * (kSms - 2 * c) && mean_len > (long long)c * 128) c *= 2;
@@ -774,8 +774,8 @@ struct Kind {
 // least, where two walks of them and the two more launches (5 us) take less than the
 // cluster's rounds, each of which is 1.6 times a tile of 128 tokens long.  The walks read twice, at
 // 7 TB/s in all.  Us in clusters | parts: 4096 x 64 gated bf16
-// forward 9.5 | 9.1, backward 15.8 | 12.1; 16384 x 64 30 | 12, 50 | 15, in fp32 65 | 17, 144 |
-// 24; 65536 x 1024 151 | 117, 252 | 157; but fp32 and not gated 187 | 204, 309 | 258.
+// forward 9.9 | 9.5, backward 16.3 | 12.4; 16384 x 64 31 | 12, 51 | 15, in fp32 67 | 17, 141 |
+// 24; 65536 x 1024 157 | 119, 260 | 173; but fp32 and not gated 186 | 204, 312 | 293.
 int parts_of(long long clusters, int cluster, long long mean_len, const Kind &k, double bytes) {
     if (cluster < 4) return 1;
     const long long parts = std::min(2 * kSms / clusters, mean_len / 128);

@@ -308,9 +308,10 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(BwdArgs a) {
 // Whole 16-byte chunks in every row.
 bool vector_rows(int dtype, int D) { return D % (dtype == GDN_BF16 ? 8 : 4) == 0; }
 
-// Elements to a thread: 16, or 8 of rows that are read one by one (a register each: with
-// 16, and the next row's on the way, one CTA fits an SM).  16000 x 4095 bf16 forward /
-// backward 148 / 211 us (142 / 255 with 16), 9224 x 7275 173 / 195 (168 / 490).
+// Elements to a thread: 16, or 8 of rows that are read one by one (a register each).  Us with 8 |
+// 16: 16000 x 4095 bf16 forward 164 | 208, backward 229 | 168; 60000 x 1001 128 | 187, 151 | 153; in
+// fp32 8000 x 4095 126 | 138, 132 | 155, 30000 x 1001 102 | 127, 89 | 142.  (The backward pass of wide
+// bf16 rows is the exception, and of rows of over 4096 columns, 9224 x 7275 228 | 201.)
 int per_thread(int dtype, int D) { return vector_rows(dtype, D) || D > 8192 ? 16 : 8; }
 // Threads of a row: the least power of two that holds it; 8 with MX scales, so that a
 // scale tile's blocks have threads.
