@@ -1,0 +1,90 @@
+// gdn_vec.cuh -- what the convolution and the state space scan share: neighbouring
+// elements as one load, activations, and the token ranges of sequences.
+#pragma once
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+// VEC neighbouring elements of T at an address that is a multiple of their size.
+template <int BYTES>
+struct RawBytes;
+template <>
+struct RawBytes<2> {
+    using type = uint16_t;
+};
+template <>
+struct RawBytes<4> {
+    using type = uint32_t;
+};
+template <>
+struct RawBytes<8> {
+    using type = uint2;
+};
+template <>
+struct RawBytes<16> {
+    using type = uint4;
+};
+template <typename T, int VEC>
+struct Vec {
+    using Raw = typename RawBytes<VEC * (int)sizeof(T)>::type;
+    static __device__ __forceinline__ Raw raw(const T *p) { return *reinterpret_cast<const Raw *>(p); }
+    static __device__ __forceinline__ void get(const Raw &r, float *v) {
+        const T *e = reinterpret_cast<const T *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f(e[i]);
+    }
+    static __device__ __forceinline__ void load(const T *p, float *v) { get(raw(p), v); }
+    static __device__ __forceinline__ void store(T *p, const float *v) {
+        Raw r;
+        T *e = reinterpret_cast<T *>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) from_f(e + i, v[i]);
+        *reinterpret_cast<Raw *>(p) = r;
+    }
+};
+
+// The logistic function.  fp32 tensors take the accurate functions; of bf16 ones, whose results
+// are rounded to 2^-9 of themselves, the hardware's exponential and reciprocal (2^-21).
+template <typename T>
+__device__ __forceinline__ float logistic(float x) {
+    if (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
+    return __fdividef(1.f, 1.f + __expf(-x));
+}
+// d(x logistic(x)) / dx, s = logistic(x).
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f + x * (1.f - s)); }
+
+// Sequences: rows of T tokens, or (cu) a packed batch of T tokens in all.
+struct Seqs {
+    const int32_t *cu;
+    long long T;
+    int N;
+};
+
+// Token range of sequence n; false for an impossible one, whose tokens are then left alone.
+__device__ __forceinline__ bool seq_tokens(const Seqs &s, int n, long long &bos, long long &len) {
+    if (!s.cu) {
+        bos = (long long)n * s.T;
+        len = s.T;
+        return true;
+    }
+    const long long lo = s.cu[n], hi = s.cu[n + 1];
+    const bool bad = lo < 0 || hi < lo || hi > s.T || (n == 0 && lo != 0) || (n == s.N - 1 && hi != s.T);
+    bos = bad ? 0 : lo;
+    len = bad ? 0 : hi - lo;
+    return !bad;
+}
+
+// The sequence of token t (of a packed batch the last that begins at or before it).
+__device__ __forceinline__ int seq_of(const Seqs &s, long long t) {
+    if (!s.cu) return (int)(t / s.T);
+    int lo = 0, hi = s.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s.cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace gdn

@@ -1,8 +1,8 @@
 /*
  * gdn_layer.h -- C ABI of libgdn.so for the operators a recurrent layer needs
  * around the gated delta rule of gdn.h: the residual addition with the RMS
- * norm, microscaled (MX) quantisation and products, and a per-channel gated
- * linear recurrence.
+ * norm, microscaled (MX) quantisation and products, a per-channel gated linear
+ * recurrence, and the short causal convolution.
  *
  * The conventions are those of gdn.h: device pointers on the current device,
  * contiguous row-major tensors whose bases are 16-byte aligned, every call
@@ -197,6 +197,61 @@ typedef struct gdn_rms_norm_bwd_args {
 size_t gdn_rms_norm_bwd_workspace_size(const gdn_rms_norm_bwd_args *args);
 gdn_status gdn_rms_norm_bwd(const gdn_rms_norm_bwd_args *args, void *workspace,
                             size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Short causal convolution along the tokens, per channel, with its activation:
+ *
+ *     pre_t = bias + sum over k of weight[k] xp_{t + k},   y = act(pre)
+ *
+ * xp being the W - 1 inputs before the sequence (initial_state, or zeros) and then x.
+ * The state after a sequence is the last W - 1 rows of xp, whatever its length. */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2 };
+
+typedef struct gdn_conv_fwd_args {
+    const void *x;              /* [B, T, D], dtype                                  */
+    const void *weight;         /* [D, W], dtype: the last tap is the token's own    */
+    const void *bias;           /* [D], dtype, NULL = none                           */
+    const void *initial_state;  /* [N, W - 1, D], dtype, oldest first; NULL = zeros  */
+    const int32_t *cu_seqlens;  /* as in gdn_linrec_fwd_args                         */
+    int32_t B, T, D, N, W;      /* W is 2, 3 or 4                                    */
+    int32_t dtype;              /* GDN_FP32 or GDN_BF16                              */
+    int32_t activation;         /* GDN_ACT_NONE or GDN_ACT_SILU                      */
+    void *y;                    /* [B, T, D], dtype                                  */
+    void *final_state;          /* [N, W - 1, D], dtype, NULL = not written          */
+} gdn_conv_fwd_args;
+gdn_status gdn_conv_fwd(const gdn_conv_fwd_args *args, void *stream);
+
+/* Backward, dpre = dy act'(pre):  dxp_i = sum over k of weight[k] dpre_{i - k}, the last W - 1
+ * rows with d_final_state added to them;  dweight[k] = sum over tokens of dpre_t xp_{t + k};
+ * dbias = sum of dpre.  dx and d_initial_state are the two parts of dxp. */
+typedef struct gdn_conv_bwd_args {
+    const void *d_y;            /* [B, T, D], dtype                                  */
+    const void *x, *weight, *bias, *initial_state;                 /* the forward's  */
+    const int32_t *cu_seqlens;
+    const void *d_final_state;  /* [N, W - 1, D], dtype, NULL = zeros                */
+    int32_t B, T, D, N, W;
+    int32_t dtype, activation;
+    void *dx;                   /* [B, T, D], dtype                                  */
+    float *dweight;             /* [D, W]                                            */
+    float *dbias;               /* [D], NULL = not written                           */
+    void *d_initial_state;      /* [N, W - 1, D], dtype, NULL = not written          */
+} gdn_conv_bwd_args;
+/* 256 or more, as gdn_linrec_bwd_workspace_size. */
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_bwd_args *args);
+gdn_status gdn_conv_bwd(const gdn_conv_bwd_args *args, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* One token for each of N sequences. */
+typedef struct gdn_conv_step_args {
+    const void *x;              /* [N, D], dtype                                     */
+    const void *weight, *bias;
+    const void *state;          /* [N, W - 1, D], dtype                              */
+    int32_t N, D, W;
+    int32_t dtype, activation;
+    void *y;                    /* [N, D], dtype                                     */
+    void *out_state;            /* [N, W - 1, D], dtype: may be `state` itself       */
+} gdn_conv_step_args;
+gdn_status gdn_conv_step(const gdn_conv_step_args *args, void *stream);
 
 #ifdef __cplusplus
 }
