@@ -16,7 +16,8 @@ from .layer import (MxTensor, add_rms_norm, add_rms_norm_bwd, add_rms_norm_fwd,
                     gated_linear_recurrence_fwd, gated_linear_recurrence_step, mx_dequantize,
                     mx_from_parts, mx_linear, mx_matmul, mx_quantize)
 from .state_space import (causal_convolution, causal_convolution_bwd, causal_convolution_fwd,
-                          causal_convolution_step)
+                          causal_convolution_step, state_space_scan, state_space_scan_bwd,
+                          state_space_scan_fwd, state_space_step)
 
 _abi.load()
 _abi_layer.load()
@@ -31,4 +32,5 @@ __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_
            "gated_linear_recurrence_bwd", "gated_linear_recurrence_step",
            "add_rms_norm", "add_rms_norm_fwd", "add_rms_norm_bwd",
            "MxTensor", "mx_quantize", "mx_dequantize", "mx_from_parts", "mx_matmul", "mx_linear",
-           "causal_convolution", "causal_convolution_fwd", "causal_convolution_bwd", "causal_convolution_step"]
+           "causal_convolution", "causal_convolution_fwd", "causal_convolution_bwd", "causal_convolution_step",
+           "state_space_scan", "state_space_scan_fwd", "state_space_scan_bwd", "state_space_step"]

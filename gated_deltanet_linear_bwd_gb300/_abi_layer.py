@@ -74,15 +74,37 @@ class gdn_conv_step_args(ctypes.Structure):
                 ("W", _i32), ("dtype", _i32), ("activation", _i32), ("y", _vp), ("out_state", _vp)]
 
 
+class gdn_ssm_fwd_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("dt", _vp), ("a", _vp), ("b", _vp), ("c", _vp), ("skip", _vp), ("z", _vp),
+                ("dt_bias", _vp), ("initial_state", _vp), ("cu_seqlens", _vp), ("B", _i32), ("T", _i32),
+                ("D", _i32), ("S", _i32), ("N", _i32), ("dtype", _i32), ("y", _vp), ("final_state", _vp)]
+
+
+class gdn_ssm_bwd_args(ctypes.Structure):
+    _fields_ = [("d_y", _vp), ("x", _vp), ("dt", _vp), ("a", _vp), ("b", _vp), ("c", _vp), ("skip", _vp),
+                ("z", _vp), ("dt_bias", _vp), ("initial_state", _vp), ("cu_seqlens", _vp),
+                ("d_final_state", _vp), ("B", _i32), ("T", _i32), ("D", _i32), ("S", _i32), ("N", _i32),
+                ("dtype", _i32), ("dx", _vp), ("ddt", _vp), ("da", _vp), ("db", _vp), ("dc", _vp),
+                ("dskip", _vp), ("dz", _vp), ("ddt_bias", _vp), ("d_initial_state", _vp)]
+
+
+class gdn_ssm_step_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("dt", _vp), ("a", _vp), ("b", _vp), ("c", _vp), ("skip", _vp), ("z", _vp),
+                ("dt_bias", _vp), ("state", _vp), ("N", _i32), ("D", _i32), ("S", _i32), ("dtype", _i32),
+                ("y", _vp), ("out_state", _vp)]
+
+
 GDN_MXFP8, GDN_MXFP4 = 0, 1
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
 
 _PLAIN = {"gdn_linrec_step": gdn_linrec_step_args,
           "gdn_mx_quantize": gdn_mx_quantize_args, "gdn_mx_dequantize": gdn_mx_dequantize_args,
           "gdn_mx_matmul": gdn_mx_matmul_args, "gdn_rms_norm_fwd": gdn_rms_norm_fwd_args,
-          "gdn_conv_fwd": gdn_conv_fwd_args, "gdn_conv_step": gdn_conv_step_args}
+          "gdn_conv_fwd": gdn_conv_fwd_args, "gdn_conv_step": gdn_conv_step_args,
+          "gdn_ssm_step": gdn_ssm_step_args}
 _WITH_WORKSPACE = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_mx_linear": gdn_mx_linear_args,
-                   "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args, "gdn_conv_bwd": gdn_conv_bwd_args}
+                   "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args, "gdn_conv_bwd": gdn_conv_bwd_args,
+                   "gdn_ssm_fwd": gdn_ssm_fwd_args, "gdn_ssm_bwd": gdn_ssm_bwd_args}
 STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
 EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \
     tuple(n + "_workspace_size" for n in _WITH_WORKSPACE) + ("gdn_mx_scale_bytes",)

@@ -1,0 +1,1051 @@
+// gdn_ssm.cu -- selective state space scan, its backward pass and its one-token step.
+//
+// Per channel d and state s of S, with the step delta = softplus(dt + dt_bias) (or dt):
+//
+//     h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t,   y_t = (<c_t, h_t> + skip x_t) silu(z_t)
+//
+// A channel's states are shared out to LP lanes, four to each, which stay in registers while the
+// lanes walk the tokens; x, dt, b and c come through shared memory a tile at a time, the step's
+// softplus taken once for all lanes.  <c, h> of LP tokens is added up over the lanes together.
+//
+// Where sequences and channels are too few for the GPU, sequences are cut into parts that are
+// walked twice: first for a part's end state from zero and the sum of its steps (whose exponential
+// is the part's decay), then, these joined, for the outputs.  The backward pass always cuts into
+// segments of 64 tokens, whose start states and end gradients one joined walk gives.
+#include <algorithm>
+#include <type_traits>
+
+#include "gdn_layer_internal.h"
+#include "gdn_vec.cuh"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
+constexpr int kMaxStates = 64;
+constexpr int kItems = 8 * kThreads;               // (token, channel) pairs of a tile: eight to a thread
+constexpr int kSegment = 64;                       // tokens of the backward pass's segments
+constexpr int kSub = 8;                            // tokens whose decays it holds in registers
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The decays 2^y.  What matters is a small error that leans neither way, as a slow state multiplies
+// thousands of decays near 1 together.  The hardware's exponential leans down by 0.5e-8 .. 3e-8 of
+// itself there: a constant added to y, free in the product's instruction, takes 1.2e-8 of that away
+// (a step of 0 still gives exactly 1).  fp32 tensors take for |y| < 1/32 the polynomial 1 + y q(y), q
+// through (2^y - 1) / y at the three Chebyshev points of -1/32 .. 1/32 (1.1e-7 of y).
+template <typename T>
+__device__ __forceinline__ float2 decay(float step, float2 a2) {
+    if (sizeof(T) == 2) {
+        const float2 y = __ffma2_rn(both(step), a2, both(1.73e-8f));
+        return make_float2(ex2(y.x), ex2(y.y));
+    }
+    const float2 y = __fmul2_rn(both(step), a2);
+    float2 p = __ffma2_rn(y, both(5.5505085252e-2f), both(2.4023355157e-1f));
+    p = __ffma2_rn(p, y, both(0.6931471805599453f));
+    p = __ffma2_rn(p, y, both(1.f));
+    return make_float2(fabsf(y.x) < 0.03125f ? p.x : ex2(y.x), fabsf(y.y) < 0.03125f ? p.y : ex2(y.y));
+}
+
+// Sequences cut into parts of `part` tokens.  A part's slot is cu[n] / part + n + its number in the
+// sequence, which no two share, so that a packed batch needs no table: sequence n + 1's first slot is
+// at least sequence n's number of parts (one at least) behind sequence n's.
+struct Cut {
+    Seqs s;
+    int part, per;                                 // per: parts of a row
+    int slots;
+    int *status;
+};
+struct Part {
+    int n;
+    long long first;                               // its first token
+    int len;                                       // tokens, 0 only for an empty sequence
+    bool begins, ends;                             // the sequence
+};
+// False where no part has the slot.
+__device__ __forceinline__ bool part_of(const Cut &c, int slot, Part &p) {
+    long long bos, len, off;
+    if (!c.s.cu) {
+        p.n = slot / c.per;
+        bos = (long long)p.n * c.s.T;
+        len = c.s.T;
+        off = (long long)(slot - p.n * c.per) * c.part;
+    } else {
+        int lo = 0, hi = c.s.N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((long long)c.s.cu[mid] / c.part + mid <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        p.n = lo;
+        if (!seq_tokens(c.s, lo, bos, len)) {
+            if (threadIdx.x == 0) set_status(c.status, GDN_ERR_BAD_SEQLENS);
+            return false;
+        }
+        off = (slot - bos / c.part - lo) * c.part;
+    }
+    if (off < 0 || (off > 0 && off >= len)) return false;
+    p.first = bos + off;
+    p.len = (int)min((long long)c.part, len - off);
+    p.begins = off == 0;
+    p.ends = off + p.len == len;
+    return true;
+}
+// The first slot and the number of parts of sequence n.
+__device__ __forceinline__ int parts_of(const Cut &c, int n, int &count) {
+    long long bos, len;
+    if (!seq_tokens(c.s, n, bos, len)) {
+        count = 0;
+        return 0;
+    }
+    count = (int)max(1ll, (len + c.part - 1) / c.part);
+    return c.s.cu ? (int)(bos / c.part) + n : n * c.per;
+}
+
+// Eight neighbouring channels of a token; VECT: rows that start on 16 bytes.
+template <typename T>
+struct Eight {
+    uint4 r[sizeof(T) / 2];
+    __device__ __forceinline__ float at(int i) const { return to_f(reinterpret_cast<const T *>(r)[i]); }
+};
+template <typename T, bool VECT>
+__device__ __forceinline__ Eight<T> load8(const void *base, long long token, int ch, int D, bool live) {
+    Eight<T> e;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.r[i] = make_uint4(0, 0, 0, 0);
+    if (!base || !live) return e;
+    const T *p = (const T *)base + token * D + ch;
+    if (VECT) {
+        if (ch < D) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.r[i] = reinterpret_cast<const uint4 *>(p)[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (ch + i < D) reinterpret_cast<T *>(e.r)[i] = p[i];
+    }
+    return e;
+}
+template <typename T, bool VECT>
+__device__ __forceinline__ void store8(void *base, long long token, int ch, int D, const float *v) {
+    T *p = (T *)base + token * D + ch;
+    if (VECT) {
+        if (ch < D) {
+            uint4 r[sizeof(T) / 2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) from_f(reinterpret_cast<T *>(r) + i, v[i]);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (ch + i < D) from_f(p + i, v[i]);
+    }
+}
+// Eight neighbouring parameters; zeros past the end and without any.
+__device__ __forceinline__ void params8(const float *p, int ch, int D, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p && ch + i < D ? p[ch + i] : 0.f;
+}
+
+// A lane's four states of a [.., D, S] tensor.
+__device__ __forceinline__ void load_states(const float *base, long long row, int S, int s0, bool in, float2 (&v)[2]) {
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = base && in && s0 + i < S ? base[row * S + s0 + i] : 0.f;
+    v[0] = make_float2(f[0], f[1]);
+    v[1] = make_float2(f[2], f[3]);
+}
+__device__ __forceinline__ void store_states(float *base, long long row, int S, int s0, bool in, const float2 (&v)[2]) {
+    if (!in) return;
+    float *p = base + row * S + s0;
+    if ((S & 3) == 0) {
+        if (s0 < S) *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        return;
+    }
+    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (s0 + i < S) p[i] = f[i];
+}
+
+// Adds up NV values over NL lanes that are STRIDE apart, `lane` being this one's place among them.
+// While values are left to share, each round leaves half of them to either half of the lanes;
+// then v[0 .. max(1, NV / NL)) are the sums of the values from the returned index on, and lanes that
+// share one all have it.
+template <int NV, int NL, int STRIDE>
+__device__ __forceinline__ int share_sum(float *v, int lane) {
+    int from = 0;
+    int n = NV;
+#pragma unroll
+    for (int o = NL / 2; o > 0; o /= 2) {
+        if (n > 1) {
+            const int half = n / 2;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int k = 0; k < NV / 2; ++k)
+                if (k < half) {
+                    const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+                    v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o * STRIDE);
+                }
+            if (up) from += half;
+            n = half;
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STRIDE);
+        }
+    }
+    return from;
+}
+
+// ------------------------------------------------------------------ forward, and parts' pairs
+struct Inputs {
+    const void *x, *dt, *b, *c, *z, *dy;
+    const float *a, *skip, *dt_bias;
+    int D, S, groups;                              // groups of channels
+};
+struct FwdArgs {
+    Inputs in;
+    const float *h0;
+    void *y;
+    float *ht;
+    const float *start;                            // [slots][D][S] states before the parts; null: h0
+    float *end, *back, *steps;                     // pairs: [slots][D][S], [slots][D][S], [slots][D]
+    Cut cut;
+    int longest_first;
+};
+// The outputs; a part's end state from zero and the sum of its steps; and with those the gradient
+// that its tokens leave to the state before it.
+enum Mode { kOutputs, kPairs, kBothPairs };
+
+// Shared memory of a tile: TT = 8 LP tokens of CH = 256 / LP channels.
+template <int LP>
+struct Tile {
+    static constexpr int CH = kThreads / LP, TT = 8 * LP;
+    static constexpr int YS = CH + (LP == 16 ? 4 : 32 / LP);    // the row of a lane's token in other banks
+    float2 du[kItems];                             // step, step x
+    float y[TT * YS];                              // <c, h>, or the gradient before the gate
+    float4 b[TT * LP], c[TT * LP];
+};
+
+// The j-th longest of up to 256 sequences: long ones are not left for the end.
+__device__ __forceinline__ int longest(const Seqs &s, int j, int *scratch) {
+    const int t = threadIdx.x;
+    if (t < s.N) scratch[t] = s.cu[t + 1] - s.cu[t];
+    __syncthreads();
+    if (t < s.N) {
+        const int mine = scratch[t];
+        int rank = 0;
+        for (int u = 0; u < s.N; ++u) rank += scratch[u] > mine || (scratch[u] == mine && u < t);
+        if (rank == j) scratch[kThreads] = t;
+    }
+    __syncthreads();
+    const int n = scratch[kThreads];
+    __syncthreads();
+    return n;
+}
+
+template <typename T, int LP>
+__device__ __forceinline__ void load_bc(float4 *to, const void *from, long long token, int tokens, int live, int S) {
+    // [tokens][S] as [tokens][4 LP], zeros behind
+    for (int k = threadIdx.x; k < tokens * 4 * LP; k += blockDim.x) {
+        const int t = k / (4 * LP), s = k % (4 * LP);
+        reinterpret_cast<float *>(to)[k] = t < live && s < S ? to_f(((const T *)from)[(token + t) * S + s]) : 0.f;
+    }
+}
+
+template <typename T, int LP, bool VECT, int MODE>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(FwdArgs a) {
+    using L = Tile<LP>;
+    extern __shared__ __align__(16) uint8_t shared[];
+    L &tile = *reinterpret_cast<L *>(shared);
+    pdl_enter();
+
+    const int group = blockIdx.x % a.in.groups;
+    int slot = blockIdx.x / a.in.groups;
+    if (a.longest_first) slot = longest(a.cut.s, slot, reinterpret_cast<int *>(shared));
+    Part part;
+    if (!part_of(a.cut, slot, part)) return;
+    const int D = a.in.D, S = a.in.S;
+    // as one of the lanes: a channel and four states of it
+    const int s = threadIdx.x % LP, c = threadIdx.x / LP, ch = group * L::CH + c;
+    const bool in = ch < D;
+    // as one that loads and stores: eight channels of a token
+    const int mt = threadIdx.x * 8 / L::CH, mc = threadIdx.x * 8 % L::CH, mch = group * L::CH + mc;
+    float bias[8], skip[8];
+    params8(a.in.dt_bias, mch, D, bias);
+    params8(a.in.skip, mch, D, skip);
+
+    float2 a2[2], h[2], P[2] = {both(1.f), both(1.f)}, acc[2] = {both(0.f), both(0.f)};
+    load_states(a.in.a, ch, S, 4 * s, in, a2);
+    a2[0] = __fmul2_rn(a2[0], both(kLog2e));
+    a2[1] = __fmul2_rn(a2[1], both(kLog2e));
+    h[0] = h[1] = both(0.f);
+    if (MODE == kOutputs) {
+        if (a.start) load_states(a.start, (long long)slot * D + ch, S, 4 * s, in, h);
+        else load_states(a.h0, (long long)part.n * D + ch, S, 4 * s, in, h);
+    }
+    float steps = 0.f;
+
+    Eight<T> x, dt, z, dy;
+    const auto fetch = [&](int at) {
+        const bool live = at + mt < part.len;
+        x = load8<T, VECT>(a.in.x, part.first + at + mt, mch, D, live);
+        dt = load8<T, VECT>(a.in.dt, part.first + at + mt, mch, D, live);
+        if (MODE != kPairs) z = load8<T, VECT>(a.in.z, part.first + at + mt, mch, D, live);
+        if (MODE == kBothPairs) dy = load8<T, VECT>(a.in.dy, part.first + at + mt, mch, D, live);
+    };
+    fetch(0);
+    for (int at = 0; at < part.len; at += L::TT) {
+        const int tokens = min(L::TT, part.len - at);
+        const bool live = mt < tokens;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float raw = dt.at(i) + bias[i];
+            const float step = !live ? 0.f : a.in.dt_bias ? softplus<T>(raw) : raw;
+            tile.du[mt * L::CH + mc + i] = make_float2(step, step * x.at(i));
+            if (MODE == kBothPairs) {
+                const float zi = z.at(i);
+                tile.y[mt * L::YS + mc + i] = a.in.z ? dy.at(i) * zi * logistic<T>(zi) : dy.at(i);
+            }
+        }
+        load_bc<T, LP>(tile.b, a.in.b, part.first + at, L::TT, tokens, S);
+        if (MODE != kPairs) load_bc<T, LP>(tile.c, a.in.c, part.first + at, L::TT, tokens, S);
+        const Eight<T> cx = x, cz = z;
+        fetch(at + L::TT);
+        __syncthreads();
+        for (int t = 0; t < tokens; t += LP) {
+            float v[LP];
+#pragma unroll
+            for (int k = 0; k < LP; ++k) {
+                const float2 du = tile.du[(t + k) * L::CH + c];
+                const float4 b = tile.b[(t + k) * LP + s];
+                const float2 e0 = decay<T>(du.x, a2[0]), e1 = decay<T>(du.x, a2[1]);
+                h[0] = __ffma2_rn(e0, h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
+                h[1] = __ffma2_rn(e1, h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
+                if (MODE != kOutputs) steps += du.x;
+                if (MODE != kPairs) {
+                    const float4 cc = tile.c[(t + k) * LP + s];
+                    if (MODE == kOutputs) {
+                        float2 d = __fmul2_rn(make_float2(cc.x, cc.y), h[0]);
+                        d = __ffma2_rn(make_float2(cc.z, cc.w), h[1], d);
+                        v[k] = d.x + d.y;
+                    } else {
+                        const float ds = tile.y[(t + k) * L::YS + c];
+                        P[0] = __fmul2_rn(P[0], e0);
+                        P[1] = __fmul2_rn(P[1], e1);
+                        acc[0] = __ffma2_rn(P[0], __fmul2_rn(both(ds), make_float2(cc.x, cc.y)), acc[0]);
+                        acc[1] = __ffma2_rn(P[1], __fmul2_rn(both(ds), make_float2(cc.z, cc.w)), acc[1]);
+                    }
+                }
+            }
+            if (MODE == kOutputs) {
+                share_sum<LP, LP, 1>(v, s);        // token t + s is this lane's
+                tile.y[(t + s) * L::YS + c] = v[0];
+            }
+        }
+        __syncthreads();
+        if (MODE == kOutputs && live) {
+            float out[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                out[i] = fmaf(skip[i], cx.at(i), tile.y[mt * L::YS + mc + i]);
+                if (a.in.z) out[i] *= cz.at(i) * logistic<T>(cz.at(i));
+            }
+            store8<T, VECT>(a.y, part.first + at + mt, mch, D, out);
+        }
+    }
+    if (MODE == kOutputs) {
+        if (part.ends && a.ht) store_states(a.ht, (long long)part.n * D + ch, S, 4 * s, in, h);
+    } else {
+        store_states(a.end, (long long)slot * D + ch, S, 4 * s, in, h);
+        if (MODE == kBothPairs) store_states(a.back, (long long)slot * D + ch, S, 4 * s, in, acc);
+        if (in && s == 0) a.steps[(long long)slot * D + ch] = steps;
+    }
+}
+
+// Parts joined: end[slot] becomes the state before the part, back[slot] (if given) the gradient that
+// reaches its last state from behind.  A thread takes one state of a channel of a sequence.
+struct JoinArgs {
+    const float *a, *steps, *h0, *dht;
+    float *end, *back, *dh0;
+    int D, S;
+    Cut cut;
+};
+__global__ void __launch_bounds__(256) join_kernel(JoinArgs a) {
+    pdl_enter();
+    const long long states = (long long)a.D * a.S, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int n = blockIdx.y;
+    if (i >= states) return;
+    const int d = (int)(i / a.S);
+    int count;
+    const int first = parts_of(a.cut, n, count);
+    const float a2 = a.a[i] * kLog2e;
+    constexpr int kAhead = 8;
+    float v = a.h0 ? a.h0[n * states + i] : 0.f;
+    for (int j = 0; j < count; j += kAhead) {
+        float e[kAhead], st[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j + k < count) {
+                e[k] = a.end[(first + j + k) * states + i];
+                st[k] = a.steps[(long long)(first + j + k) * a.D + d];
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j + k < count) {
+                a.end[(first + j + k) * states + i] = v;
+                v = fmaf(ex2(st[k] * a2), v, e[k]);
+            }
+    }
+    if (!a.back) return;
+    v = a.dht ? a.dht[n * states + i] : 0.f;
+    for (int j = count; j > 0; j -= kAhead) {
+        float e[kAhead], st[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j - 1 - k >= 0) {
+                e[k] = a.back[(first + j - 1 - k) * states + i];
+                st[k] = a.steps[(long long)(first + j - 1 - k) * a.D + d];
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j - 1 - k >= 0) {
+                a.back[(first + j - 1 - k) * states + i] = v;
+                v = fmaf(ex2(st[k] * a2), v, e[k]);
+            }
+    }
+    if (a.dh0 && count > 0) a.dh0[n * states + i] = v;
+}
+
+// ------------------------------------------------------------------ backward
+struct BwdArgs {
+    Inputs in;
+    float *start;                                  // [slots][D][S] states before the segments; then da's parts
+    const float *behind;                           // [slots][D][S] gradients from behind them
+    void *dx, *ddt, *dz;
+    float *dskip, *dbias;                          // [slots][D] each segment's part
+    float *dbc;                                    // [lanes][tokens][2 S]: of groups of channels
+    void *db, *dc;                                 // written here where one lane has all channels
+    long long tokens;
+    int lanes;                                     // CTAs that share a segment's channels
+    Cut cut;
+};
+
+template <int LP>
+struct Segment {
+    static constexpr int CH = LP <= 4 ? 64 : 256 / LP, NT = CH * LP, WARPS = NT / 32;
+    static constexpr int SP = 4 * LP, V = 2 * SP;  // states, and gradients of b and c of a token
+    static constexpr int BUFS = LP <= 4 ? 2 : 1;
+    static constexpr int YS = CH + (LP == 16 ? 4 : 32 / LP);
+    float2 du[kSegment * CH];                      // step, step x; then <e, b>, <e a, p>
+    float ds[kSegment * YS];                       // gradient before the gate; then <c, h>
+    float4 b[kSegment * LP], c[kSegment * LP];
+    float4 saved[(kSegment / kSub - 1) * NT];      // states before the sub-segments; then sums of dskip, dbias
+    float red[BUFS][WARPS][kSub][V];
+    float acc[kSegment * V];
+};
+
+template <typename T, int LP, bool VECT>
+__global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::NT : 1) bwd_kernel(BwdArgs a) {
+    using G = Segment<LP>;
+    extern __shared__ __align__(16) uint8_t shared[];
+    G &m = *reinterpret_cast<G *>(shared);
+    pdl_enter();
+
+    const int slot = blockIdx.x / a.lanes, lane_no = blockIdx.x - slot * a.lanes;
+    const int D = a.in.D, S = a.in.S, tid = threadIdx.x;
+    const int g0 = (int)((long long)a.in.groups * lane_no / a.lanes), g1 = (int)((long long)a.in.groups * (lane_no + 1) / a.lanes);
+    const int s = tid % LP, c = tid / LP, warp = tid / 32;
+    Part part;
+    const bool there = part_of(a.cut, slot, part) && part.len > 0;
+    if (!there) {                                  // its parts of the sums
+        for (int g = g0; g < g1; ++g) {
+            const int ch = g * G::CH + c;
+            const float2 none[2] = {both(0.f), both(0.f)};
+            store_states(a.start, (long long)slot * D + ch, S, 4 * s, ch < D, none);
+            if (ch < D && s == 0) {
+                if (a.dskip) a.dskip[(long long)slot * D + ch] = 0.f;
+                if (a.dbias) a.dbias[(long long)slot * D + ch] = 0.f;
+            }
+        }
+        return;
+    }
+    const int len = part.len, subs = (len + kSub - 1) / kSub;
+    load_bc<T, LP>(m.b, a.in.b, part.first, kSegment, len, S);
+    load_bc<T, LP>(m.c, a.in.c, part.first, kSegment, len, S);
+    for (int k = tid; k < kSegment * G::V; k += G::NT) m.acc[k] = 0.f;
+
+    for (int g = g0; g < g1; ++g) {
+        const int ch = g * G::CH + c;
+        const bool in = ch < D;
+        float bias[8];
+        const int mc = tid * 8 % G::CH, mch = g * G::CH + mc;
+        params8(a.in.dt_bias, mch, D, bias);
+        for (int k = tid * 8; k < kSegment * G::CH; k += 8 * G::NT) {
+            const int t = k / G::CH;
+            const bool live = t < len;
+            const Eight<T> x = load8<T, VECT>(a.in.x, part.first + t, mch, D, live);
+            const Eight<T> dt = load8<T, VECT>(a.in.dt, part.first + t, mch, D, live);
+            const Eight<T> z = load8<T, VECT>(a.in.z, part.first + t, mch, D, live);
+            const Eight<T> dy = load8<T, VECT>(a.in.dy, part.first + t, mch, D, live);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float raw = dt.at(i) + bias[i], zi = z.at(i);
+                const float step = !live ? 0.f : a.in.dt_bias ? softplus<T>(raw) : raw;
+                m.du[t * G::CH + mc + i] = make_float2(step, step * x.at(i));
+                m.ds[t * G::YS + mc + i] = a.in.z ? dy.at(i) * zi * logistic<T>(zi) : dy.at(i);
+            }
+        }
+        float2 an[2], a2[2], hs[2], carry[2], da[2] = {both(0.f), both(0.f)};
+        const long long row = (long long)slot * D + ch;
+        load_states(a.in.a, ch, S, 4 * s, in, an);
+        load_states(a.start, row, S, 4 * s, in, hs);
+        load_states(a.behind, row, S, 4 * s, in, carry);
+        a2[0] = __fmul2_rn(an[0], both(kLog2e));
+        a2[1] = __fmul2_rn(an[1], both(kLog2e));
+        __syncthreads();
+
+        // the states before every sub-segment
+        {
+            float2 h[2] = {hs[0], hs[1]};
+            for (int q = 0; q + 1 < subs; ++q) {
+#pragma unroll
+                for (int k = 0; k < kSub; ++k) {
+                    const int t = q * kSub + k;
+                    const float2 du = m.du[t * G::CH + c];
+                    const float4 b = m.b[t * LP + s];
+                    h[0] = __ffma2_rn(decay<T>(du.x, a2[0]), h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
+                    h[1] = __ffma2_rn(decay<T>(du.x, a2[1]), h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
+                }
+                m.saved[q * G::NT + tid] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+            }
+        }
+        for (int q = subs - 1; q >= 0; --q) {
+            float2 h[2] = {hs[0], hs[1]}, e[kSub][2], p[kSub][2];
+            if (q > 0) {
+                const float4 v = m.saved[(q - 1) * G::NT + tid];
+                h[0] = make_float2(v.x, v.y);
+                h[1] = make_float2(v.z, v.w);
+            }
+#pragma unroll
+            for (int k = 0; k < kSub; ++k) {
+                const int t = q * kSub + k;
+                const float2 du = m.du[t * G::CH + c];
+                const float4 b = m.b[t * LP + s];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    e[k][i] = decay<T>(du.x, a2[i]);
+                    p[k][i] = __fmul2_rn(e[k][i], h[i]);
+                    h[i] = __ffma2_rn(both(du.y), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y), p[k][i]);
+                }
+            }
+            float hc[kSub], eb[kSub], ep[kSub];    // <c, h>, <e, b>, <e a, p> of this lane's states
+            float *red = &m.red[G::BUFS == 2 ? q & 1 : 0][warp][0][0];
+            if (G::BUFS == 1) __syncthreads();     // the sub-segment before has been added up
+#pragma unroll
+            for (int k = kSub - 1; k >= 0; --k) {
+                const int t = q * kSub + k;
+                const float2 du = m.du[t * G::CH + c];
+                const float ds = m.ds[t * G::YS + c];
+                const float4 b4 = m.b[t * LP + s], c4 = m.c[t * LP + s];
+                float2 vh = both(0.f), vb = both(0.f), vp = both(0.f);
+                float2 gbc[4];                     // gradients of b and c
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 b = i ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+                    const float2 cc = i ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+                    const float2 hh = __ffma2_rn(both(du.y), b, p[k][i]);
+                    gbc[2 + i] = __fmul2_rn(both(ds), hh);
+                    vh = __ffma2_rn(cc, hh, vh);
+                    const float2 grad = __ffma2_rn(cc, both(ds), carry[i]);
+                    gbc[i] = __fmul2_rn(grad, both(du.y));
+                    vb = __ffma2_rn(grad, b, vb);
+                    const float2 lost = __fmul2_rn(grad, p[k][i]);
+                    da[i] = __ffma2_rn(lost, both(du.x), da[i]);
+                    vp = __ffma2_rn(lost, an[i], vp);
+                    carry[i] = __fmul2_rn(e[k][i], grad);
+                }
+                hc[k] = vh.x + vh.y;
+                eb[k] = vb.x + vb.y;
+                ep[k] = vp.x + vp.y;
+                float v[8] = {gbc[0].x, gbc[0].y, gbc[1].x, gbc[1].y, gbc[2].x, gbc[2].y, gbc[3].x, gbc[3].y};
+                constexpr int NL = 32 / LP, LEFT = NL >= 8 ? 1 : 8 / NL;
+                const int lane = (tid & 31) / LP, from = share_sum<8, NL, LP>(v, lane);
+                if (NL <= 8 || (lane & (NL / 8 - 1)) == 0) {
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) {
+                        const int w = from + i;    // 0 - 3: b's, 4 - 7: c's
+                        red[k * G::V + (w >> 2) * G::SP + 4 * s + (w & 3)] = v[i];
+                    }
+                }
+            }
+            // over the channel's lanes; every lane has read its tokens' steps and gradients
+            {
+                constexpr int LEFT = LP >= 8 ? 1 : 8 / LP;
+                int from = share_sum<8, LP, 1>(hc, s);
+                share_sum<8, LP, 1>(eb, s);
+                share_sum<8, LP, 1>(ep, s);
+                __syncwarp();
+                if (LP <= 8 || (s & (LP / 8 - 1)) == 0) {
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) {
+                        const int t = q * kSub + from + i;
+                        m.du[t * G::CH + c] = make_float2(eb[i], ep[i]);
+                        m.ds[t * G::YS + c] = hc[i];
+                    }
+                }
+            }
+            __syncthreads();
+            for (int k = tid; k < kSub * G::V; k += G::NT) {
+                float v = m.acc[q * kSub * G::V + k];
+#pragma unroll
+                for (int w = 0; w < G::WARPS; ++w) v += (&m.red[G::BUFS == 2 ? q & 1 : 0][w][0][0])[k];
+                m.acc[q * kSub * G::V + k] = v;
+            }
+        }
+        store_states(a.start, row, S, 4 * s, in, da);
+        __syncthreads();                           // every channel's sums are there
+
+        float skip[8], gs[8], gb[8];
+        params8(a.in.skip, mch, D, skip);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gs[i] = gb[i] = 0.f;
+        for (int k = tid * 8; k < len * G::CH; k += 8 * G::NT) {
+            const int t = k / G::CH;
+            const Eight<T> x = load8<T, VECT>(a.in.x, part.first + t, mch, D, true);
+            const Eight<T> dt = load8<T, VECT>(a.in.dt, part.first + t, mch, D, true);
+            const Eight<T> z = load8<T, VECT>(a.in.z, part.first + t, mch, D, true);
+            const Eight<T> dy = load8<T, VECT>(a.in.dy, part.first + t, mch, D, true);
+            float dx[8], ddt[8], dz[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float raw = dt.at(i) + bias[i], zi = z.at(i), xi = x.at(i);
+                const float step = a.in.dt_bias ? softplus<T>(raw) : raw;
+                const float2 sums = m.du[t * G::CH + mc + i];
+                float ds = dy.at(i);
+                if (a.in.z) {
+                    const float sg = logistic<T>(zi);
+                    dz[i] = ds * fmaf(skip[i], xi, m.ds[t * G::YS + mc + i]) * silu_slope(zi, sg);
+                    ds *= zi * sg;
+                }
+                dx[i] = fmaf(skip[i], ds, step * sums.x);
+                ddt[i] = fmaf(xi, sums.x, sums.y);
+                if (a.in.dt_bias) ddt[i] *= logistic<T>(raw);
+                gs[i] = fmaf(ds, xi, gs[i]);
+                gb[i] += ddt[i];
+            }
+            store8<T, VECT>(a.dx, part.first + t, mch, D, dx);
+            store8<T, VECT>(a.ddt, part.first + t, mch, D, ddt);
+            if (a.in.z) store8<T, VECT>(a.dz, part.first + t, mch, D, dz);
+        }
+        // over the threads that took the same channels
+        float *sums = reinterpret_cast<float *>(m.saved);
+        constexpr int ROWS = 8 * G::NT / G::CH;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sums[(tid * 8 / G::CH) * G::CH + mc + i] = gs[i];
+            sums[(ROWS + tid * 8 / G::CH) * G::CH + mc + i] = gb[i];
+        }
+        __syncthreads();
+        for (int k = tid; k < 2 * G::CH; k += G::NT) {
+            const int what = k / G::CH, at = k % G::CH;
+            float v = 0.f;
+            for (int r = 0; r < ROWS; ++r) v += sums[(what * ROWS + r) * G::CH + at];
+            float *out = what ? a.dbias : a.dskip;
+            if (out && g * G::CH + at < D) out[(long long)slot * D + g * G::CH + at] = v;
+        }
+        __syncthreads();                           // before the next channels' tile
+    }
+    for (int k = tid; k < len * 2 * S; k += G::NT) {
+        const int t = k / (2 * S), w = k % (2 * S);
+        const float v = m.acc[t * G::V + (w >= S ? G::SP + w - S : w)];
+        if (a.lanes == 1) from_f((T *)(w >= S ? a.dc : a.db) + (part.first + t) * S + (w >= S ? w - S : w), v);
+        else a.dbc[((long long)lane_no * a.tokens + part.first + t) * 2 * S + w] = v;
+    }
+}
+
+// db and dc from the lanes' parts; tokens that no sequence has are left alone.
+template <typename T>
+__global__ void __launch_bounds__(256) dbc_kernel(const float *parts, int lanes, long long tokens, int S, Seqs s,
+                                                  T *db, T *dc) {
+    pdl_enter();
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < tokens * 2 * S;
+         i += (long long)gridDim.x * blockDim.x) {
+        const long long t = i / (2 * S);
+        const int w = (int)(i - t * 2 * S);
+        if (s.cu) {
+            long long bos, len;
+            if (!seq_tokens(s, seq_of(s, t), bos, len)) continue;
+        }
+        float v = 0.f;
+        for (int l = 0; l < lanes; ++l) v += parts[(long long)l * tokens * 2 * S + i];
+        from_f((w >= S ? dc : db) + t * S + (w >= S ? w - S : w), v);
+    }
+}
+
+// ------------------------------------------------------------------ one token
+struct StepArgs {
+    Inputs in;
+    const float *state;
+    void *y;
+    float *out;
+    int N;
+};
+template <typename T, int LP>
+__global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
+    pdl_enter();
+    const int D = a.in.D, S = a.in.S, s = threadIdx.x % LP;
+    const long long rows = (long long)a.N * D;
+    for (long long r0 = (long long)blockIdx.x * (kThreads / LP); r0 < rows; r0 += (long long)gridDim.x * (kThreads / LP)) {
+        const long long row = r0 + threadIdx.x / LP;
+        const bool in = row < rows;
+        const long long n = in ? row / D : 0;
+        const int ch = in ? (int)(row - n * D) : 0;
+        float2 h[2], an[2];
+        load_states(a.state, row, S, 4 * s, in, h);
+        load_states(a.in.a, ch, S, 4 * s, in, an);
+        float step = 0.f, x = 0.f;
+        if (in) {
+            x = to_f(((const T *)a.in.x)[row]);
+            step = to_f(((const T *)a.in.dt)[row]);
+            if (a.in.dt_bias) step = softplus<T>(step + a.in.dt_bias[ch]);
+        }
+        float b[4], cc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool has = in && 4 * s + i < S;
+            b[i] = has ? to_f(((const T *)a.in.b)[n * S + 4 * s + i]) : 0.f;
+            cc[i] = has ? to_f(((const T *)a.in.c)[n * S + 4 * s + i]) : 0.f;
+        }
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 e = decay<T>(step, __fmul2_rn(an[i], both(kLog2e)));
+            h[i] = __ffma2_rn(e, h[i], __fmul2_rn(both(step * x), make_float2(b[2 * i], b[2 * i + 1])));
+            y += h[i].x * cc[2 * i] + h[i].y * cc[2 * i + 1];
+        }
+        store_states(a.out, row, S, 4 * s, in, h);
+#pragma unroll
+        for (int o = LP / 2; o > 0; o /= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (in && s == 0) {
+            if (a.in.skip) y = fmaf(a.in.skip[ch], x, y);
+            if (a.in.z) {
+                const float z = to_f(((const T *)a.in.z)[row]);
+                y *= z * logistic<T>(z);
+            }
+            from_f((T *)a.y + row, y);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+// Lanes of a channel: four states to each.
+int lanes_of(int S) {
+    int lp = 1;
+    while (4 * lp < S) lp *= 2;
+    return lp;
+}
+template <typename F>
+auto by_lanes(int lp, F f) {
+    switch (lp) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 8: return f(std::integral_constant<int, 8>());
+        default: return f(std::integral_constant<int, 16>());
+    }
+}
+template <typename F>
+auto by_type(int dtype, F f) {
+    return dtype == GDN_BF16 ? f((__nv_bfloat16 *)nullptr) : f((float *)nullptr);
+}
+template <typename F>
+auto by_alignment(int D, F f) {
+    return D % 8 == 0 ? f(std::true_type()) : f(std::false_type());
+}
+
+constexpr int kSms = 152;          // of the GPU that the choices below are made for
+constexpr int kMaxOrdered = kThreads;
+
+gdn_status check(int B, int T, int D, int S, int N, int dtype, bool packed) {
+    if (B < 1 || T < 0 || D < 1 || S < 1)
+        return fail(GDN_ERR_INVALID_ARG, "bad sizes B=%d T=%d D=%d S=%d", B, T, D, S);
+    if (S > kMaxStates) return fail(GDN_ERR_UNSUPPORTED, "S = %d (at most %d)", S, kMaxStates);
+    if (dtype != GDN_FP32 && dtype != GDN_BF16)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_FP32 or GDN_BF16", dtype);
+    if (packed && (B != 1 || N < 1))
+        return fail(GDN_ERR_INVALID_ARG, "cu_seqlens needs B == 1 and N >= 1 (B=%d N=%d)", B, N);
+    // a CTA for 16 channels and 64 tokens or a sequence at least, numbered by an int; sequences by a
+    // grid's second dimension
+    const long long n = packed ? N : B, tokens = (long long)B * T;
+    if (tokens >= (1ll << 31) - (1 << 16) || D > (1 << 23) || n > 65535 ||
+        (tokens / kSegment + 2 * n) * ((D + 15) / 16) >= (1ll << 31))
+        return fail(GDN_ERR_INVALID_ARG, "problem too large");
+    return GDN_OK;
+}
+
+Cut cut_of(const int32_t *cu, int B, int T, int N, int part) {
+    Cut c{};
+    c.s = {cu, T, cu ? N : B};
+    c.part = part;
+    c.per = std::max(1, (int)(((long long)T + part - 1) / part));
+    c.slots = cu ? (int)((long long)T / part) + N : B * c.per;
+    return c;
+}
+
+// Tokens of a part of the forward pass, T + 1 for sequences left whole.
+int fwd_part(int B, int T, int D, int S, int N, bool packed) {
+    const int lp = lanes_of(S), ch = kThreads / lp;
+    const long long n = packed ? N : B, ctas = n * ((D + ch - 1) / ch), mean = packed ? T / n : T;
+    const long long parts = std::min<long long>(4 * kSms / std::max(1ll, ctas), mean / 128);
+    if (parts < 3) return T + 1;
+    return (int)((mean + parts - 1) / parts + 7) / 8 * 8;
+}
+
+struct FwdPlan {
+    Cut cut;
+    bool parts;
+    size_t states, steps;          // floats of each
+};
+FwdPlan plan_of(const gdn_ssm_fwd_args *a) {
+    FwdPlan p{};
+    const int part = fwd_part(a->B, a->T, a->D, a->S, a->N, a->cu_seqlens != nullptr);
+    p.parts = part <= a->T;
+    p.cut = cut_of(a->cu_seqlens, a->B, a->T, a->N, part);
+    if (p.parts) {
+        p.states = (size_t)p.cut.slots * a->D * a->S;
+        p.steps = (size_t)p.cut.slots * a->D;
+    }
+    return p;
+}
+
+struct BwdPlan {
+    Cut cut;
+    int lanes;
+    size_t states, rows, dbc;      // floats: of states (twice), of a row (three times), of db and dc
+};
+BwdPlan plan_of(const gdn_ssm_bwd_args *a) {
+    BwdPlan p{};
+    p.cut = cut_of(a->cu_seqlens, a->B, a->T, a->N, kSegment);
+    const int lp = lanes_of(a->S), ch = lp <= 4 ? 64 : 256 / lp, groups = (a->D + ch - 1) / ch;
+    // CTAs for about four waves, so that the last one is short
+    const long long want = (8ll * kSms + p.cut.slots - 1) / p.cut.slots;
+    p.lanes = (int)std::max(1ll, std::min<long long>(groups, want));
+    p.states = (size_t)p.cut.slots * a->D * a->S;
+    p.rows = (size_t)p.cut.slots * a->D;
+    p.dbc = p.lanes > 1 ? (size_t)p.lanes * a->B * a->T * 2 * a->S : 0;
+    return p;
+}
+size_t padded(size_t floats) { return (floats + 3) / 4 * 4; }
+size_t fwd_bytes(const FwdPlan &p) { return 4 * (padded(p.states) + padded(p.steps)); }
+size_t bwd_bytes(const BwdPlan &p) { return 4 * (2 * padded(p.states) + 3 * padded(p.rows) + padded(p.dbc)); }
+size_t asked_for(size_t need) { return need == 0 ? 256 : std::max<size_t>(512, need); }
+
+template <int MODE>
+cudaError_t launch_fwd(const char *name, FwdArgs f, int dtype, cudaStream_t q) {
+    return by_type(dtype, [&](auto *t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        return by_lanes(lanes_of(f.in.S), [&](auto lp) {
+            return by_alignment(f.in.D, [&](auto vect) {
+                constexpr int LP = decltype(lp)::value;
+                auto k = fwd_kernel<T, LP, decltype(vect)::value, MODE>;
+                cudaError_t e = allow_smem((const void *)k, sizeof(Tile<LP>));
+                if (e != cudaSuccess) return e;
+                f.in.groups = (f.in.D + Tile<LP>::CH - 1) / Tile<LP>::CH;
+                prof_before(name, q);
+                e = launch_pdl(k, dim3((unsigned)((long long)f.in.groups * f.cut.slots)), dim3(kThreads),
+                               sizeof(Tile<LP>), q, f);
+                prof_after(q);
+                return e;
+            });
+        });
+    });
+}
+
+cudaError_t launch_join(const JoinArgs &j, cudaStream_t q) {
+    const long long states = (long long)j.D * j.S;
+    prof_before("ssm_join", q);
+    const cudaError_t e = launch_pdl(join_kernel, dim3((unsigned)((states + 255) / 256), j.cut.s.N), dim3(256), 0, q, j);
+    prof_after(q);
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_bwd(BwdArgs b, cudaStream_t q) {
+    cudaError_t e = by_lanes(lanes_of(b.in.S), [&](auto lp) {
+        return by_alignment(b.in.D, [&](auto vect) {
+            constexpr int LP = decltype(lp)::value;
+            using G = Segment<LP>;
+            auto k = bwd_kernel<T, LP, decltype(vect)::value>;
+            cudaError_t r = allow_smem((const void *)k, sizeof(G));
+            if (r != cudaSuccess) return r;
+            b.in.groups = (b.in.D + G::CH - 1) / G::CH;
+            prof_before("ssm_bwd", q);
+            r = launch_pdl(k, dim3((unsigned)((long long)b.lanes * b.cut.slots)), dim3(G::NT), sizeof(G), q, b);
+            prof_after(q);
+            return r;
+        });
+    });
+    if (e != cudaSuccess || b.lanes == 1 || b.tokens == 0) return e;
+    const long long n = b.tokens * 2 * b.in.S;
+    prof_before("ssm_dbc", q);
+    e = launch_pdl(dbc_kernel<T>, dim3((unsigned)std::min<long long>((n + 255) / 256, 1 << 16)), dim3(256), 0, q,
+                   (const float *)b.dbc, b.lanes, b.tokens, b.in.S, b.cut.s, (T *)b.db, (T *)b.dc);
+    prof_after(q);
+    return e;
+}
+
+}  // namespace
+}  // namespace ssm
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_ssm_fwd_workspace_size(const gdn_ssm_fwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (ssm::check(a->B, a->T, a->D, a->S, a->N, a->dtype, a->cu_seqlens != nullptr) != GDN_OK) return 0;
+    return ssm::asked_for(ssm::fwd_bytes(ssm::plan_of(a)));
+}
+
+gdn_status gdn_ssm_fwd(const gdn_ssm_fwd_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = ssm::check(a->B, a->T, a->D, a->S, a->N, a->dtype, a->cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (!a->a || (a->T > 0 && (!a->x || !a->dt || !a->b || !a->c || !a->y)))
+        return fail(GDN_ERR_INVALID_ARG, "x, dt, a, b, c and y are required");
+    if (misaligned(a->x) || misaligned(a->dt) || misaligned(a->a) || misaligned(a->b) || misaligned(a->c) ||
+        misaligned(a->skip) || misaligned(a->z) || misaligned(a->dt_bias) || misaligned(a->initial_state) ||
+        misaligned(a->cu_seqlens) || misaligned(a->y) || misaligned(a->final_state))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    ssm::FwdPlan p = ssm::plan_of(a);
+    const size_t need = ssm::fwd_bytes(p);
+    if (need > 0 && (!ws || misaligned(ws) || ws_bytes < need))
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    p.cut.status = dev.status;
+    cudaStream_t q = (cudaStream_t)stream;
+    ssm::FwdArgs f{};
+    f.in = {a->x, a->dt, a->b, a->c, a->z, nullptr, a->a, a->skip, a->dt_bias, a->D, a->S, 0};
+    f.h0 = a->initial_state;
+    f.y = a->y;
+    f.ht = a->final_state;
+    f.cut = p.cut;
+    f.longest_first = a->cu_seqlens && !p.parts && a->N <= ssm::kMaxOrdered;
+    cudaError_t e = cudaSuccess;
+    if (p.parts) {
+        f.end = (float *)ws;
+        f.steps = f.end + ssm::padded(p.states);
+        e = ssm::launch_fwd<ssm::kPairs>("ssm_pairs", f, a->dtype, q);
+        if (e == cudaSuccess)
+            e = ssm::launch_join({a->a, f.steps, a->initial_state, nullptr, f.end, nullptr, nullptr, a->D, a->S, p.cut}, q);
+        f.start = f.end;
+    }
+    if (e == cudaSuccess) e = ssm::launch_fwd<ssm::kOutputs>("ssm_fwd", f, a->dtype, q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "state space scan launch");
+}
+
+size_t gdn_ssm_bwd_workspace_size(const gdn_ssm_bwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (ssm::check(a->B, a->T, a->D, a->S, a->N, a->dtype, a->cu_seqlens != nullptr) != GDN_OK) return 0;
+    return ssm::asked_for(ssm::bwd_bytes(ssm::plan_of(a)));
+}
+
+gdn_status gdn_ssm_bwd(const gdn_ssm_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = ssm::check(a->B, a->T, a->D, a->S, a->N, a->dtype, a->cu_seqlens != nullptr);
+    if (st != GDN_OK) return st;
+    if (!a->a || !a->da ||
+        (a->T > 0 && (!a->d_y || !a->x || !a->dt || !a->b || !a->c || !a->dx || !a->ddt || !a->db || !a->dc ||
+                      (a->z && !a->dz))))
+        return fail(GDN_ERR_INVALID_ARG, "d_y, x, dt, a, b, c, dx, ddt, da, db, dc and (with z) dz are required");
+    if (misaligned(a->d_y) || misaligned(a->x) || misaligned(a->dt) || misaligned(a->a) || misaligned(a->b) ||
+        misaligned(a->c) || misaligned(a->skip) || misaligned(a->z) || misaligned(a->dt_bias) ||
+        misaligned(a->initial_state) || misaligned(a->cu_seqlens) || misaligned(a->d_final_state) ||
+        misaligned(a->dx) || misaligned(a->ddt) || misaligned(a->da) || misaligned(a->db) || misaligned(a->dc) ||
+        misaligned(a->dskip) || misaligned(a->dz) || misaligned(a->ddt_bias) || misaligned(a->d_initial_state))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    ssm::BwdPlan p = ssm::plan_of(a);
+    const size_t need = ssm::bwd_bytes(p);
+    if (!ws || misaligned(ws) || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    p.cut.status = dev.status;
+    cudaStream_t q = (cudaStream_t)stream;
+    ssm::FwdArgs f{};
+    f.in = {a->x, a->dt, a->b, a->c, a->z, a->d_y, a->a, a->skip, a->dt_bias, a->D, a->S, 0};
+    f.cut = p.cut;
+    f.end = (float *)ws;
+    f.back = f.end + ssm::padded(p.states);
+    f.steps = f.back + ssm::padded(p.states);
+    cudaError_t e = ssm::launch_fwd<ssm::kBothPairs>("ssm_bwd_pairs", f, a->dtype, q);
+    if (e == cudaSuccess)
+        e = ssm::launch_join({a->a, f.steps, a->initial_state, a->d_final_state, f.end, f.back, a->d_initial_state,
+                              a->D, a->S, p.cut}, q);
+    ssm::BwdArgs b{};
+    b.in = f.in;
+    b.start = f.end;
+    b.behind = f.back;
+    b.dx = a->dx, b.ddt = a->ddt, b.dz = a->dz, b.db = a->db, b.dc = a->dc;
+    float *rows = f.steps + ssm::padded(p.rows);
+    const bool skip = a->skip && a->dskip, bias = a->dt_bias && a->ddt_bias;
+    b.dskip = skip ? rows : nullptr;
+    b.dbias = bias ? rows + ssm::padded(p.rows) : nullptr;
+    b.dbc = rows + 2 * ssm::padded(p.rows);
+    b.tokens = (long long)a->B * a->T;
+    b.lanes = p.lanes;
+    b.cut = p.cut;
+    if (e == cudaSuccess)
+        e = a->dtype == GDN_BF16 ? ssm::launch_bwd<__nv_bfloat16>(b, q) : ssm::launch_bwd<float>(b, q);
+    if (e == cudaSuccess) e = column_sum(b.start, p.cut.slots, a->D * a->S, a->da, q);
+    if (e == cudaSuccess && skip) e = column_sum(b.dskip, p.cut.slots, a->D, a->dskip, q);
+    if (e == cudaSuccess && bias) e = column_sum(b.dbias, p.cut.slots, a->D, a->ddt_bias, q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "state space scan backward launch");
+}
+
+gdn_status gdn_ssm_step(const gdn_ssm_step_args *a, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    if (a->N < 0) return fail(GDN_ERR_INVALID_ARG, "bad sizes N=%d D=%d S=%d", a->N, a->D, a->S);
+    gdn_status st = ssm::check(1, 1, a->D, a->S, 1, a->dtype, false);
+    if (st != GDN_OK) return st;
+    if (a->N > (1 << 30)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
+    if (a->N == 0) return GDN_OK;
+    if (!a->x || !a->dt || !a->a || !a->b || !a->c || !a->state || !a->y || !a->out_state)
+        return fail(GDN_ERR_INVALID_ARG, "x, dt, a, b, c, state, y and out_state are required");
+    if (misaligned(a->x) || misaligned(a->dt) || misaligned(a->a) || misaligned(a->b) || misaligned(a->c) ||
+        misaligned(a->skip) || misaligned(a->z) || misaligned(a->dt_bias) || misaligned(a->state) ||
+        misaligned(a->y) || misaligned(a->out_state))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    cudaStream_t q = (cudaStream_t)stream;
+    ssm::StepArgs s{{a->x, a->dt, a->b, a->c, a->z, nullptr, a->a, a->skip, a->dt_bias, a->D, a->S, 0},
+                    a->state, a->y, a->out_state, a->N};
+    prof_before("ssm_step", q);
+    const cudaError_t e = ssm::by_type(a->dtype, [&](auto *t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        return ssm::by_lanes(ssm::lanes_of(a->S), [&](auto lp) {
+            constexpr int LP = decltype(lp)::value, rows = ssm::kThreads / LP;
+            const long long ctas = ((long long)a->N * a->D + rows - 1) / rows;
+            return launch_pdl(ssm::step_kernel<T, LP>, dim3((unsigned)std::min<long long>(ctas, 16ll * dev.sms)),
+                              dim3(ssm::kThreads), 0, q, s);
+        });
+    });
+    prof_after(q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "state space step launch");
+}
+
+}  // extern "C"

@@ -54,6 +54,25 @@ __device__ __forceinline__ float logistic(float x) {
 // d(x logistic(x)) / dx, s = logistic(x).
 __device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f + x * (1.f - s)); }
 
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// log(1 + e^x).  Of bf16 tensors with the hardware's exponential and logarithm, but for e = e^-|x| <
+// 1/8, where the logarithm of the rounded 1 + e would lose what a small step is made of: there e p(e),
+// p the polynomial through log2(1 + e) / e at the four Chebyshev points of 0 .. 1/8 (3.1e-7 of itself).
+template <typename T>
+__device__ __forceinline__ float softplus(float x) {
+    if (sizeof(T) == 4) return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+    const float e = ex2(-fabsf(x) * 1.4426950408889634f);
+    float p = fmaf(e, -2.9770274392e-1f, 4.7618794121e-1f);
+    p = fmaf(p, e, -7.2123178461e-1f);
+    p = fmaf(p, e, 1.4426945903f) * e;
+    return fmaf(e < 0.125f ? p : __log2f(1.f + e), 0.6931471805599453f, fmaxf(x, 0.f));
+}
+
 // Sequences: rows of T tokens, or (cu) a packed batch of T tokens in all.
 struct Seqs {
     const int32_t *cu;

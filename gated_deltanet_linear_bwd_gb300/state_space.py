@@ -1,4 +1,5 @@
-"""Torch-facing wrappers of the short causal convolution, in the manner of layer.py: they check
+"""Torch-facing wrappers of the short causal convolution and the selective state space scan, in the
+manner of layer.py: they check
 arguments, allocate outputs and workspace with torch on the tensors' device and pass raw pointers
 on the current stream; every computation runs in libgdn.so.
 """
@@ -9,6 +10,7 @@ from . import _abi_layer
 from .layer import _F32, _empty, _empty_like, _first, _grad, _need, _ptr, _raw_stream, _with_workspace
 
 _conv_fwd, _conv_bwd, _conv_step = (_abi_layer.ENTRIES["gdn_" + name] for name in ("conv_fwd", "conv_bwd", "conv_step"))
+_ssm_fwd, _ssm_bwd, _ssm_step = (_abi_layer.ENTRIES["gdn_" + name] for name in ("ssm_fwd", "ssm_bwd", "ssm_step"))
 
 _ACTIVATIONS = {None: _abi_layer.GDN_ACT_NONE, "silu": _abi_layer.GDN_ACT_SILU}
 
@@ -134,4 +136,109 @@ def causal_convolution_step(x, weight, state, bias=None, activation="silu", out_
     y = _empty_like(x)
     _conv_step(_conv_step.pack(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), N, D, W, code, act,
                                y.data_ptr(), out_state.data_ptr()), _raw_stream(index))
+    return y
+
+
+# ------------------------------------------------------------------ selective state space scan
+def _scan_inputs(dtype, lead, D, index, dt, a, b, c, skip, z, dt_bias):
+    """Checks what the scan and the step share; the number of states."""
+    if a.dim() != 2:
+        raise ValueError(f"a has shape {tuple(a.shape)}, expected [D, S]")
+    S = a.shape[1]
+    if not 1 <= S <= 64:
+        raise ValueError(f"a has {S} states (1 to 64)")
+    _need("dt", dt, dtype, (*lead, D), index)
+    _need("a", a, _F32, (D, S), index)
+    _need("b", b, dtype, (*lead, S), index)
+    _need("c", c, dtype, (*lead, S), index)
+    if skip is not None:
+        _need("skip", skip, _F32, (D,), index)
+    if z is not None:
+        _need("z", z, dtype, (*lead, D), index)
+    if dt_bias is not None:
+        _need("dt_bias", dt_bias, _F32, (D,), index)
+    return S
+
+
+def state_space_scan_fwd(x, dt, a, b, c, skip=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None,
+                         output_final_state=True):
+    """h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t and y_t = (<c_t, h_t> + skip x_t) silu(z_t), for
+    each channel of x, dt, z [B, T, D] and its S states (1 to 64); b, c [B, T, S] in x's type (bf16 or
+    fp32), a [D, S] and skip [D] fp32.  delta = dt, or softplus(dt + dt_bias) with `dt_bias` ([D]
+    fp32).  States are [N, D, S] fp32; with `cu_seqlens` ([N + 1] int32) B is 1 and the tokens are N
+    packed sequences.  Returns (y, final_state or None)."""
+    dtype, code, index, B, T, D, N = _sequences("x", x, cu_seqlens)
+    S = _scan_inputs(dtype, (B, T), D, index, dt, a, b, c, skip, z, dt_bias)
+    if initial_state is not None:
+        _need("initial_state", initial_state, _F32, (N, D, S), index)
+    y = _empty_like(x)
+    ht = _empty((N, D, S), dtype=_F32, device=x.device) if output_final_state else None
+    _with_workspace(_ssm_fwd, _ssm_fwd.pack(
+        x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _ptr(skip), _ptr(z), _ptr(dt_bias),
+        _ptr(initial_state), _ptr(cu_seqlens), B, T, D, S, N, code, y.data_ptr(), _ptr(ht)), x.device, index)
+    return y, ht
+
+
+def state_space_scan_bwd(dy, x, dt, a, b, c, skip=None, z=None, dt_bias=None, dht=None, initial_state=None,
+                         cu_seqlens=None, want_dh0=True):
+    """Backward of state_space_scan_fwd from its inputs: (dx, ddt, da, db, dc, dskip, dz, ddt_bias,
+    d(initial_state)), None for what was not given (or not wanted); da, dskip, ddt_bias and
+    d(initial_state) fp32, the others in x's type.  `dht` is the gradient of the final state."""
+    dtype, code, index, B, T, D, N = _sequences("dy", dy, cu_seqlens)
+    _need("x", x, dtype, dy.shape, index)
+    S = _scan_inputs(dtype, (B, T), D, index, dt, a, b, c, skip, z, dt_bias)
+    if initial_state is not None:
+        _need("initial_state", initial_state, _F32, (N, D, S), index)
+    if dht is not None:
+        _need("dht", dht, _F32, (N, D, S), index)
+    dx, ddt, da, db, dc = (_empty_like(t) for t in (x, dt, a, b, c))
+    dskip, dz, dbias = (None if t is None else _empty_like(t) for t in (skip, z, dt_bias))
+    dh0 = _empty((N, D, S), dtype=_F32, device=x.device) if want_dh0 else None
+    _with_workspace(_ssm_bwd, _ssm_bwd.pack(
+        dy.data_ptr(), x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _ptr(skip), _ptr(z),
+        _ptr(dt_bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(dht), B, T, D, S, N, code, dx.data_ptr(),
+        ddt.data_ptr(), da.data_ptr(), db.data_ptr(), dc.data_ptr(), _ptr(dskip), _ptr(dz), _ptr(dbias), _ptr(dh0)),
+        x.device, index)
+    return dx, ddt, da, db, dc, dskip, dz, dbias, dh0
+
+
+class _StateSpaceScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, a, b, c, skip, z, dt_bias, initial_state, cu_seqlens):
+        y, ht = state_space_scan_fwd(x, dt, a, b, c, skip, z, dt_bias, initial_state, cu_seqlens)
+        ctx.save_for_backward(x, dt, a, b, c, skip, z, dt_bias, initial_state, cu_seqlens)
+        return y, ht
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dht):
+        *inputs, h0, cu = ctx.saved_tensors
+        return *state_space_scan_bwd(_grad(dy), *inputs, dht=_grad(dht), initial_state=h0, cu_seqlens=cu,
+                                     want_dh0=h0 is not None), None
+
+
+def state_space_scan(x, dt, a, b, c, skip=None, z=None, dt_bias=None, initial_state=None, cu_seqlens=None,
+                     output_final_state=False):
+    """state_space_scan_fwd, differentiable in all but cu_seqlens: (y, final_state or None)."""
+    y, ht = _StateSpaceScan.apply(x, dt, a, b, c, skip, z, dt_bias, initial_state, cu_seqlens)
+    return y, (ht if output_final_state else None)
+
+
+def state_space_step(x, dt, a, b, c, state, skip=None, z=None, dt_bias=None, out_state=None):
+    """One token for each of N sequences: x, dt, z [N, D], b, c [N, S], state [N, D, S] fp32.
+    Returns y [N, D]; the new state goes to `out_state`, or over `state`."""
+    if x.dim() != 2:
+        raise ValueError(f"expected [N, D] tensors, got shape {tuple(x.shape)}")
+    dtype, code, index = _first("x", x)
+    N, D = x.shape
+    S = _scan_inputs(dtype, (N,), D, index, dt, a, b, c, skip, z, dt_bias)
+    _need("state", state, _F32, (N, D, S), index)
+    if out_state is None:
+        out_state = state
+    else:
+        _need("out_state", out_state, _F32, (N, D, S), index)
+    y = _empty_like(x)
+    _ssm_step(_ssm_step.pack(
+        x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _ptr(skip), _ptr(z), _ptr(dt_bias),
+        state.data_ptr(), N, D, S, code, y.data_ptr(), out_state.data_ptr()), _raw_stream(index))
     return y

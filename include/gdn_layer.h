@@ -2,7 +2,7 @@
  * gdn_layer.h -- C ABI of libgdn.so for the operators a recurrent layer needs
  * around the gated delta rule of gdn.h: the residual addition with the RMS
  * norm, microscaled (MX) quantisation and products, a per-channel gated linear
- * recurrence, and the short causal convolution.
+ * recurrence, the short causal convolution, and the selective state space scan.
  *
  * The conventions are those of gdn.h: device pointers on the current device,
  * contiguous row-major tensors whose bases are 16-byte aligned, every call
@@ -252,6 +252,82 @@ typedef struct gdn_conv_step_args {
     void *out_state;            /* [N, W - 1, D], dtype: may be `state` itself       */
 } gdn_conv_step_args;
 gdn_status gdn_conv_step(const gdn_conv_step_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Selective state space scan: per channel d and state s,
+ *
+ *     h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t,   y_t = (<c_t, h_t> + skip x_t) silu(z_t)
+ *
+ * with the step delta = dt, or softplus(dt + dt_bias) when dt_bias is given; b_t and c_t belong to
+ * the token, a and skip to the channel.  delta >= 0 and a <= 0 are expected (a step of 0 leaves the
+ * state as it is): decays are multiplied together, and a product of growing factors can overflow
+ * where the recurrence itself would not.  States are fp32. */
+typedef struct gdn_ssm_fwd_args {
+    const void *x;              /* [B, T, D], dtype                                  */
+    const void *dt;             /* [B, T, D], dtype: steps, or their logits          */
+    const float *a;             /* [D, S]                                            */
+    const void *b, *c;          /* [B, T, S], dtype                                  */
+    const float *skip;          /* [D], NULL = none                                  */
+    const void *z;              /* [B, T, D], dtype, NULL = no gate                  */
+    const float *dt_bias;       /* [D], or NULL                                      */
+    const float *initial_state; /* [N, D, S], NULL = zeros                           */
+    const int32_t *cu_seqlens;  /* as in gdn_linrec_fwd_args                         */
+    int32_t B, T, D, S, N;      /* 1 <= S <= 64; at most 65535 sequences             */
+    int32_t dtype;              /* GDN_FP32 or GDN_BF16                              */
+    void *y;                    /* [B, T, D], dtype                                  */
+    float *final_state;         /* [N, D, S], NULL = not written                     */
+} gdn_ssm_fwd_args;
+
+/* Backward, ds_t = dy_t silu(z_t) and e_t = c_t ds_t + exp(delta_{t+1} a) e_{t+1} (d_final_state
+ * behind the last token), p_t = exp(delta_t a) h_{t-1}:
+ *     db_t = sum over d of e delta x;  dc_t = sum over d of ds h;  dx = skip ds + delta <e, b>;
+ *     ddelta = x <e, b> + <e, a p>;  da = sum over t of e delta p;  dskip = sum of ds x;
+ *     dz = dy (<c, h> + skip x) silu'(z);  d_initial_state = exp(delta_0 a) e_0.
+ * ddt is ddelta, or the logits' gradient when dt_bias is given. */
+typedef struct gdn_ssm_bwd_args {
+    const void *d_y;            /* [B, T, D], dtype                                  */
+    const void *x, *dt;         /* the forward's                                     */
+    const float *a;
+    const void *b, *c;
+    const float *skip;
+    const void *z;
+    const float *dt_bias, *initial_state;
+    const int32_t *cu_seqlens;
+    const float *d_final_state; /* [N, D, S], NULL = zeros                           */
+    int32_t B, T, D, S, N;
+    int32_t dtype;
+    void *dx, *ddt;             /* [B, T, D], dtype                                  */
+    float *da;                  /* [D, S]                                            */
+    void *db, *dc;              /* [B, T, S], dtype                                  */
+    float *dskip;               /* [D], NULL = not written (ignored without skip)    */
+    void *dz;                   /* [B, T, D], dtype: required with z                 */
+    float *ddt_bias;            /* [D], NULL = not written (ignored without dt_bias) */
+    float *d_initial_state;     /* [N, D, S], NULL = not written                     */
+} gdn_ssm_bwd_args;
+
+/* One token for each of N sequences. */
+typedef struct gdn_ssm_step_args {
+    const void *x, *dt;         /* [N, D], dtype                                     */
+    const float *a;
+    const void *b, *c;          /* [N, S], dtype                                     */
+    const float *skip;
+    const void *z;              /* [N, D], dtype, NULL = no gate                     */
+    const float *dt_bias;
+    const float *state;         /* [N, D, S]                                         */
+    int32_t N, D, S;
+    int32_t dtype;
+    void *y;                    /* [N, D], dtype                                     */
+    float *out_state;           /* [N, D, S]: may be `state` itself                  */
+} gdn_ssm_step_args;
+
+/* Bytes of workspace, as gdn_linrec_fwd_workspace_size. */
+size_t gdn_ssm_fwd_workspace_size(const gdn_ssm_fwd_args *args);
+gdn_status gdn_ssm_fwd(const gdn_ssm_fwd_args *args, void *workspace, size_t workspace_bytes,
+                       void *stream);
+size_t gdn_ssm_bwd_workspace_size(const gdn_ssm_bwd_args *args);
+gdn_status gdn_ssm_bwd(const gdn_ssm_bwd_args *args, void *workspace, size_t workspace_bytes,
+                       void *stream);
+gdn_status gdn_ssm_step(const gdn_ssm_step_args *args, void *stream);
 
 #ifdef __cplusplus
 }

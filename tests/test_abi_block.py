@@ -8,6 +8,10 @@ OK = dict(
     gdn_conv_fwd=dict(x=4096, weight=4096, y=4096, B=2, T=5, D=64, W=4),
     gdn_conv_bwd=dict(d_y=4096, x=4096, weight=4096, dx=4096, dweight=4096, B=2, T=5, D=64, W=4),
     gdn_conv_step=dict(x=4096, weight=4096, state=4096, y=4096, out_state=4096, N=2, D=64, W=4),
+    gdn_ssm_fwd=dict(x=4096, dt=4096, a=4096, b=4096, c=4096, y=4096, B=1, T=5000, D=64, S=16),
+    gdn_ssm_bwd=dict(d_y=4096, x=4096, dt=4096, a=4096, b=4096, c=4096, dx=4096, ddt=4096, da=4096, db=4096, dc=4096,
+                     B=2, T=5, D=64, S=16),
+    gdn_ssm_step=dict(x=4096, dt=4096, a=4096, b=4096, c=4096, state=4096, y=4096, out_state=4096, N=2, D=64, S=16),
 )
 
 
@@ -49,6 +53,24 @@ def call(abi, name, **kw):
     ("gdn_conv_step", dict(state=None), 1, "required"),
     ("gdn_conv_step", dict(out_state=4100), 1, "aligned"),
     ("gdn_conv_step", dict(activation=3), 2, "activation"),
+    ("gdn_ssm_fwd", dict(S=0), 1, "bad sizes"),
+    ("gdn_ssm_fwd", dict(S=65), 2, "S = 65"),
+    ("gdn_ssm_fwd", dict(T=-1), 1, "bad sizes"),
+    ("gdn_ssm_fwd", dict(dtype=3), 2, "dtype"),
+    ("gdn_ssm_fwd", dict(a=None), 1, "required"),
+    ("gdn_ssm_fwd", dict(c=None), 1, "required"),
+    ("gdn_ssm_fwd", dict(z=4104), 1, "aligned"),
+    ("gdn_ssm_fwd", dict(cu_seqlens=4096, B=2, N=1), 1, "cu_seqlens"),
+    ("gdn_ssm_fwd", dict(B=70000), 1, "too large"),
+    ("gdn_ssm_fwd", dict(T=TOP), 1, "too large"),
+    ("gdn_ssm_fwd", dict(T=1 << 30, D=1 << 20), 1, "too large"),
+    ("gdn_ssm_bwd", dict(da=None), 1, "required"),
+    ("gdn_ssm_bwd", dict(z=4096), 1, "required"),
+    ("gdn_ssm_bwd", dict(d_final_state=4100), 1, "aligned"),
+    ("gdn_ssm_step", dict(N=-1), 1, "bad sizes"),
+    ("gdn_ssm_step", dict(out_state=None), 1, "required"),
+    ("gdn_ssm_step", dict(state=4104), 1, "aligned"),
+    ("gdn_ssm_step", dict(N=TOP), 1, "too large"),
 ])
 def test_bad_arguments_are_rejected_on_the_host(abi, name, bad, rc, msg):
     assert call(abi, name, **bad) == rc
@@ -71,6 +93,7 @@ def test_null_arguments_and_small_workspaces(abi):
 
 def test_empty_problems_are_host_side_no_ops(abi):
     assert call(abi, "gdn_conv_step", N=0) == 0
+    assert call(abi, "gdn_ssm_step", N=0) == 0
     assert abi.ENTRIES["gdn_conv_bwd"].workspace_size(raw(abi, "gdn_conv_bwd", T=0)) == 256
 
 
