@@ -779,6 +779,17 @@ cudaError_t set_smem(F kernel, size_t bytes) {
 }
 }  // namespace
 
+// Encodes a map.  On a host thread that has made no CUDA call of consequence yet (autograd's own, say)
+// no context is current, and the driver refuses: then the current device's is made current first.
+template <typename... Args>
+static CUresult encode(Args... args) {
+    CUresult r = g_encode(args...);
+    if (r != CUDA_ERROR_INVALID_CONTEXT) return r;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+    return g_encode(args...);
+}
+
 cudaError_t encoder() {
     if (g_encode) return cudaSuccess;
     void *fn = nullptr;
@@ -798,7 +809,7 @@ cudaError_t make_map(CUtensorMap *m, const void *base, long long tokens, int H) 
     const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)H * kD * 2};
     const cuuint32_t box[3] = {64, 1, 64};
     const cuuint32_t es[3] = {1, 1, 1};
-    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
                                 dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -813,7 +824,7 @@ cudaError_t make_map_tiles(CUtensorMap *m, const void *base, long long rows_tota
     const cuuint64_t strides[1] = {64 * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
-    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
                                 dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -828,7 +839,7 @@ cudaError_t make_map_bytes(CUtensorMap *m, const void *base, long long rows, lon
     const cuuint64_t strides[1] = {(cuuint64_t)bytes};
     const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
-    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
                                 dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -842,7 +853,7 @@ cudaError_t make_map_scales(CUtensorMap *m, const void *base, int row_tiles, int
     const cuuint64_t strides[2] = {512, (cuuint64_t)k_tiles * 512};
     const cuuint32_t box[3] = {128, (cuuint32_t)kt, (cuuint32_t)rt};
     const cuuint32_t es[3] = {1, 1, 1};
-    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims,
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims,
                                 strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -857,7 +868,7 @@ cudaError_t make_map_rows(CUtensorMap *m, const void *base, long long rows, long
     const cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
-    const CUresult r = g_encode(
+    const CUresult r = encode(
         m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
         const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
