@@ -11,6 +11,7 @@ from ._abi import (GDN_BF16, GDN_CP_AUTO, GDN_CP_FORCE, GDN_CP_OFF, GDN_FP32, Gd
                    gdn_recurrent_step, gdn_set_spin_limit, gdn_sync_status)
 from .api import (chunk_gated_delta_rule, chunk_gated_delta_rule_bwd,
                   chunk_gated_delta_rule_fwd, recurrent_step)
+from .feed_forward import gated_feed_forward, gated_feed_forward_bwd, gated_feed_forward_fwd
 from .layer import (MxTensor, add_rms_norm, add_rms_norm_bwd, add_rms_norm_fwd,
                     gated_linear_recurrence, gated_linear_recurrence_bwd,
                     gated_linear_recurrence_fwd, gated_linear_recurrence_step, mx_dequantize,
@@ -33,4 +34,5 @@ __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_
            "add_rms_norm", "add_rms_norm_fwd", "add_rms_norm_bwd",
            "MxTensor", "mx_quantize", "mx_dequantize", "mx_from_parts", "mx_matmul", "mx_linear",
            "causal_convolution", "causal_convolution_fwd", "causal_convolution_bwd", "causal_convolution_step",
-           "state_space_scan", "state_space_scan_fwd", "state_space_scan_bwd", "state_space_step"]
+           "state_space_scan", "state_space_scan_fwd", "state_space_scan_bwd", "state_space_step",
+           "gated_feed_forward", "gated_feed_forward_fwd", "gated_feed_forward_bwd"]

@@ -94,6 +94,17 @@ class gdn_ssm_step_args(ctypes.Structure):
                 ("y", _vp), ("out_state", _vp)]
 
 
+class gdn_ffn_fwd_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("w_gate", _vp), ("w_up", _vp), ("w_down", _vp), ("M", _i32), ("K", _i32),
+                ("F", _i32), ("dtype", _i32), ("activation", _i32), ("y", _vp), ("gate", _vp), ("up", _vp)]
+
+
+class gdn_ffn_bwd_args(ctypes.Structure):
+    _fields_ = [("d_y", _vp), ("x", _vp), ("w_gate", _vp), ("w_up", _vp), ("w_down", _vp), ("gate", _vp),
+                ("up", _vp), ("M", _i32), ("K", _i32), ("F", _i32), ("dtype", _i32), ("activation", _i32),
+                ("dx", _vp), ("dw_gate", _vp), ("dw_up", _vp), ("dw_down", _vp)]
+
+
 GDN_MXFP8, GDN_MXFP4 = 0, 1
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
 
@@ -104,7 +115,8 @@ _PLAIN = {"gdn_linrec_step": gdn_linrec_step_args,
           "gdn_ssm_step": gdn_ssm_step_args}
 _WITH_WORKSPACE = {"gdn_linrec_fwd": gdn_linrec_fwd_args, "gdn_linrec_bwd": gdn_linrec_bwd_args, "gdn_mx_linear": gdn_mx_linear_args,
                    "gdn_rms_norm_bwd": gdn_rms_norm_bwd_args, "gdn_conv_bwd": gdn_conv_bwd_args,
-                   "gdn_ssm_fwd": gdn_ssm_fwd_args, "gdn_ssm_bwd": gdn_ssm_bwd_args}
+                   "gdn_ssm_fwd": gdn_ssm_fwd_args, "gdn_ssm_bwd": gdn_ssm_bwd_args,
+                   "gdn_ffn_fwd": gdn_ffn_fwd_args, "gdn_ffn_bwd": gdn_ffn_bwd_args}
 STRUCTS = tuple(_PLAIN.values()) + tuple(_WITH_WORKSPACE.values())
 EXPORTS = tuple(_PLAIN) + tuple(_WITH_WORKSPACE) + \
     tuple(n + "_workspace_size" for n in _WITH_WORKSPACE) + ("gdn_mx_scale_bytes",)

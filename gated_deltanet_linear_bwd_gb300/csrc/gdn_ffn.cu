@@ -1,0 +1,477 @@
+// gdn_ffn.cu -- gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T and its backward pass, bf16
+// products on tcgen05 with their elementwise work in the epilogues:
+//
+//     forward    g = x Wg^T, u = x Wu^T, h = act(g) u          one product of 2 F features
+//                y = h Wd^T
+//     backward   dh = dy Wd;  dg = dh u act'(g), du = dh act(g), h = act(g) u
+//                dx = dg Wg + du Wu                             one contraction over 2 F
+//                dWg = dg^T x, dWu = du^T x, dWd = dy^T h       one launch
+//
+// Sums are fp32 in TMEM.  h, dg and du pass to the next product as bf16, the tensor cores' operand
+// type: each is rounded once, by 2^-8 of itself at most.  Such roundings are of either sign, so that a
+// sum of products with them is off by about as much as its own rounding to bf16 is.
+#include <algorithm>
+
+#include "gdn_layer_internal.h"
+#include "gdn_vec.cuh"
+#include "tc_bf16_ptx.cuh"
+
+namespace gdn {
+namespace ffn {
+namespace {
+
+// The activation f(g) and its derivative; gelu is its tanh form, g logistic(2 c (g + 0.044715 g^3))
+// with c = sqrt(2 / pi).
+constexpr float kGelu2c = 1.5957691216057308f, kGeluCube = 0.044715f;
+template <bool GELU>
+__device__ __forceinline__ float activation(float g) {
+    return g * logistic<__nv_bfloat16>(GELU ? kGelu2c * g * fmaf(kGeluCube, g * g, 1.f) : g);
+}
+template <bool GELU>
+__device__ __forceinline__ float activation(float g, float &slope) {
+    if (!GELU) {
+        const float s = logistic<__nv_bfloat16>(g);
+        slope = silu_slope(g, s);
+        return g * s;
+    }
+    const float g2 = g * g, s = logistic<__nv_bfloat16>(kGelu2c * g * fmaf(kGeluCube, g2, 1.f));
+    slope = fmaf(g * s * (1.f - s), kGelu2c * fmaf(3.f * kGeluCube, g2, 1.f), s);
+    return g * s;
+}
+
+// ------------------------------------------------------------------ CTA pairs
+// Tiles of 256 x 256 by two CTAs (cta_group::2), persistent over the tiles of up to three products;
+// each CTA holds 128 rows of A and half the columns' rows of B.  Two accumulators of 256 columns fill
+// TMEM, so that a tile's epilogue runs under the next tile's MMAs.
+enum Mode {
+    kGated,      // A x, B gate's rows in the one CTA and up's in the other: a tile is 256 tokens x 128 features
+    kDown,       // A h, B w_down
+    kSlopes,     // A dy, B w_down across its rows: dh, from which dg, du and h
+    kInput,      // A dg, then du, B w_gate, then w_up, across their rows: dx
+    kWeights,    // three products of A and B across their rows: dWg, dWu, dWd
+};
+constexpr bool a_mn(int mode) { return mode == kWeights; }
+constexpr bool b_mn(int mode) { return mode >= kSlopes; }
+
+constexpr int kPairThreads = 224;                    // B, MMA, four epilogue warps, A
+constexpr int kStages = 6, kStage = 32768;
+constexpr int kBlock = 4096;                         // a warp's staged 32 rows x 128 bytes
+constexpr int kProducts = 3;
+
+struct Maps {
+    CUtensorMap a[kProducts], b[kProducts], c[kProducts];
+};
+struct PairArgs {
+    int rows, m_tiles[kProducts], n_tiles[kProducts], first[kProducts + 1];   // tiles of the products
+    int cols[kProducts];                             // of C (kGated: features)
+    int kblocks, parts;                              // blocks of 64 of a part of the contraction; kInput has two
+    int c_rows[kProducts];
+    const __nv_bfloat16 *gate, *up;                  // kSlopes
+    int save;                                        // kGated: gate and up are stored too
+    int gelu;
+    int *status;
+    long long spin_limit;
+};
+struct Control {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_free[2], done;
+    uint32_t tmem;
+    int issued;
+};
+
+// A tile's product and its row and column of tiles: eight rows of tiles at a time, column after
+// column, so that what the pairs work on together is near a square.
+constexpr int kBand = 8;
+__device__ __forceinline__ int3 tile_at(const PairArgs &a, int i) {
+    int p = 0;
+    while (p + 1 < kProducts && i >= a.first[p + 1]) ++p;
+    i -= a.first[p];
+    const int band = i / (kBand * a.n_tiles[p]), in = i - band * kBand * a.n_tiles[p];
+    const int high = min(kBand, a.m_tiles[p] - band * kBand);
+    return make_int3(p, band * kBand + in % high, in / high);
+}
+
+// A warp's 32 x 64 block of bf16 from registers to C, by TMA; two blocks are used in turn.
+struct Stager {
+    uint8_t *base;
+    int used;
+    __device__ __forceinline__ uint8_t *next(int lane) {
+        if (used >= 2) {
+            if (lane == 0) tc::bulk_wait_read_but_newest();
+            __syncwarp();
+        }
+        return base + (used & 1) * kBlock;
+    }
+    __device__ __forceinline__ void send(const CUtensorMap *map, uint8_t *block, int col, int row, bool in, int lane) {
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            if (in) tc::tma_store_2d(map, block, col, row);
+            tc::bulk_commit();                       // an empty group, where the block lies outside
+        }
+        ++used;
+    }
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ Maps maps,
+                                                            const __grid_constant__ PairArgs a) {
+    constexpr bool A_MN = a_mn(MODE), B_MN = b_mn(MODE);
+    extern __shared__ __align__(1024) uint8_t ring[];
+    uint8_t *stage_out = ring + kStages * kStage;
+    Control &ctl = *reinterpret_cast<Control *>(stage_out + 8 * kBlock);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = a.first[kProducts];
+    const int kblocks = a.kblocks * a.parts;
+
+    if (tc::smem_u32(ring) & 1023u) {                // the swizzle's unit; every CTA alike
+        if (threadIdx.x == 0) set_status(a.status, GDN_ERR_CUDA);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&ctl.full[s], 1);
+            tc::mbar_init(&ctl.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&ctl.acc_full[i], 1);
+            tc::mbar_init(&ctl.acc_free[i], 8);      // the epilogue warps of both CTAs
+        }
+        tc::mbar_init(&ctl.done, 1);
+        ctl.issued = 0;
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");           // the kernel ahead may hold TMEM
+        tc::tmem_alloc_pair(&ctl.tmem, 512);
+    }
+    tc::tc_fence_before();
+    tc::cluster_sync();                              // both CTAs' barriers and TMEM are there
+    tc::tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), empty0 = tc::smem_u32(ctl.empty);
+    if (warp == 0 || warp == 6) {
+        const bool is_b = warp == 0;
+        const uint32_t bar0 = tc::map_rank(full0, 0);
+        int i = 0, s = 0;                            // stages asked for
+        uint32_t parity = 1;                         // of the stage's last release; the first round has none
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            const int3 at = tile_at(a, tile);
+            const int row = at.y * 256 + rank * 128;
+            const int col = MODE == kGated ? at.z * 128 : at.z * 256 + rank * 128;
+            for (int kb = 0; kb < kblocks; ++kb, ++i) {
+                if (i >= kStages) {
+                    ok = tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status);
+                    if (!ok) break;
+                }
+                const int part = MODE == kInput && kb >= a.kblocks ? 1 : 0, k = (kb - part * a.kblocks) * 64;
+                const uint32_t st = ring0 + s * kStage, bar = bar0 + 8 * s;
+                if (is_b) {                          // and arms the pair's barrier for all that both CTAs get
+                    tc::expect_bytes(full0 + 8 * s, 2u * kStage, rank == 0);
+                    const int b = MODE == kGated ? rank : MODE == kInput ? part : at.x;
+                    tc::load_tile<B_MN, true>(st + 16384, &maps.b[b], col, k, bar);
+                } else {
+                    tc::load_tile<A_MN, true>(st, &maps.a[MODE == kInput ? part : at.x], row, k, bar);
+                }
+                if (++s == kStages) s = 0, parity ^= 1;
+            }
+        }
+        if (is_b && lane == 0) ctl.issued = i;
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int t = 0, s = 0;
+            uint32_t parity = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
+                if (t >= 2) {
+                    ok = tc::mbar_spin(tc::smem_u32(&ctl.acc_free[t & 1]), ((t >> 1) - 1) & 1, a.spin_limit, a.status);
+                    if (!ok) break;
+                }
+                tc::tc_fence_after();
+                const uint32_t acc = tmem + (t & 1) * 256;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    ok = tc::mbar_spin(full0 + 8 * s, parity, a.spin_limit, a.status);
+                    if (!ok) break;
+                    const uint32_t st = ring0 + s * kStage;
+                    tc::mma_bf16_stage<A_MN, B_MN, true>(acc, tc::desc_tile<A_MN>(st), tc::desc_tile<B_MN>(st + 16384),
+                                                         tc::idesc_bf16(256, 256, A_MN, B_MN), kb > 0, &ctl.empty[s]);
+                    if (++s == kStages) s = 0, parity ^= 1;
+                }
+                if (ok) tc::mma_commit_pair(&ctl.acc_full[t & 1]);
+            }
+            tc::mma_commit_pair(&ctl.done);
+        }
+    } else {
+        // epilogue: each warp takes its 32 rows, 64 columns at a time
+        const int quarter = warp & 3;
+        Stager out{stage_out + quarter * 2 * kBlock, 0};
+        const uint32_t free0 = tc::map_rank(tc::smem_u32(&ctl.acc_free[0]), 0);
+        int t = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++t) {
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_full[t & 1], (t >> 1) & 1, a.spin_limit, a.status))) break;
+            tc::tc_fence_after();
+            const int3 at = tile_at(a, tile);
+            const int row = at.y * 256 + rank * 128 + 32 * quarter, rows = a.c_rows[at.x], cols = a.cols[at.x];
+            const uint32_t acc = tmem + (t & 1) * 256;
+            if constexpr (MODE == kGated) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    const int col = at.z * 128 + c;
+                    const bool in = row < rows && col < cols;
+                    float g[64], u[64];
+                    tc::tmem_ld32x2(tc::tmem_addr(acc, quarter, c), tc::tmem_addr(acc, quarter, c + 32), g, g + 32);
+                    tc::tmem_ld32x2(tc::tmem_addr(acc, quarter, 128 + c), tc::tmem_addr(acc, quarter, 160 + c), u, u + 32);
+                    if (a.save) {
+                        uint8_t *block = out.next(lane);
+                        tc::st_row64(block, lane, g);
+                        out.send(&maps.c[1], block, col, row, in, lane);
+                        block = out.next(lane);
+                        tc::st_row64(block, lane, u);
+                        out.send(&maps.c[2], block, col, row, in, lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) u[i] *= a.gelu ? activation<true>(g[i]) : activation<false>(g[i]);
+                    uint8_t *block = out.next(lane);
+                    tc::st_row64(block, lane, u);
+                    out.send(&maps.c[0], block, col, row, in, lane);
+                }
+            } else if constexpr (MODE == kSlopes) {
+                const long long base = (long long)(row + lane) * cols;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 64) {
+                    const int col = at.z * 256 + c;
+                    const bool in = row < rows && col < cols;
+                    // the three results, a block each: dg, du, then h from gate and up once more
+#pragma unroll 1
+                    for (int what = 0; what < 3; ++what) {
+                        uint8_t *block = out.next(lane);
+#pragma unroll
+                        for (int b = 0; b < 64; b += 32) {
+                            float v[32];
+                            tc::tmem_ld32(tc::tmem_addr(acc, quarter, c + b), v);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                uint4 gr = make_uint4(0, 0, 0, 0), ur = gr;
+                                if (row + lane < rows && col + b + i < cols) {
+                                    gr = __ldg(reinterpret_cast<const uint4 *>(a.gate + base + col + b + i));
+                                    ur = __ldg(reinterpret_cast<const uint4 *>(a.up + base + col + b + i));
+                                }
+                                const __nv_bfloat16 *gs = reinterpret_cast<const __nv_bfloat16 *>(&gr);
+                                const __nv_bfloat16 *us = reinterpret_cast<const __nv_bfloat16 *>(&ur);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float g = to_f(gs[j]), u = to_f(us[j]);
+                                    float slope;
+                                    const float f = a.gelu ? activation<true>(g, slope) : activation<false>(g, slope);
+                                    v[i + j] = what == 0 ? v[i + j] * u * slope : what == 1 ? v[i + j] * f : f * u;
+                                }
+                            }
+                            tc::st_row32(block, lane, b, v);
+                        }
+                        out.send(&maps.c[what], block, col, row, in, lane);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 64) {
+                    const int col = at.z * 256 + c;
+                    float v[64];
+                    tc::tmem_ld32x2(tc::tmem_addr(acc, quarter, c), tc::tmem_addr(acc, quarter, c + 32), v, v + 32);
+                    uint8_t *block = out.next(lane);
+                    tc::st_row64(block, lane, v);
+                    out.send(&maps.c[at.x], block, col, row, row < rows && col < cols, lane);
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(free0 + 8 * (t & 1));
+        }
+        if (lane == 0) tc::bulk_wait_read();
+        __syncwarp();
+    }
+    // every MMA done and every copy landed before TMEM is given back and a CTA goes
+    tc::mbar_drain(&ctl.done, 0);
+    tc::tc_fence_before();
+    tc::cluster_sync();
+    if (threadIdx.x == 0 && rank == 0)
+        for (int i = max(0, ctl.issued - kStages); i < ctl.issued; ++i)
+            tc::mbar_drain(&ctl.full[i % kStages], (i / kStages) & 1);
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+constexpr size_t kPairSmem = kStages * kStage + 8 * kBlock + sizeof(Control);
+static_assert(kPairSmem <= 227 * 1024, "");
+// as much shared memory for its TMEM columns as clusters take (the MX products' rule)
+static_assert(kPairSmem >= 512 * 432 - 1024, "");
+
+// A matrix [rows, cols] as an operand (64-element boxes: 128 rows of it, or 64 of the contraction) or
+// as a result (32 rows).
+cudaError_t operand(CUtensorMap *m, const void *base, long long rows, long long cols, bool mn) {
+    return tc::make_map_rows(m, base, rows, cols, 2, 64, mn ? 64 : 128, true);
+}
+cudaError_t result(CUtensorMap *m, void *base, long long rows, long long cols) {
+    return tc::make_map_rows(m, base, rows, cols, 2, 64, 32, true);
+}
+
+// One launch of up to three products.
+struct Product {
+    const void *a, *b, *b2;      // b2: kGated w_up; kInput: a2 and b2 are the second part
+    const void *a2;
+    void *c[kProducts];          // kGated and kSlopes have three results, the others one
+    long long m, n, k;           // C [m, n], contraction k
+};
+template <int MODE>
+gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, const LayerDevice &dev, cudaStream_t q) {
+    Maps maps = {};
+    cudaError_t e = tc::encoder();
+    g.kblocks = (int)((p->k + 63) / 64);
+    g.parts = MODE == kInput ? 2 : 1;
+    long long tiles = 0;
+    for (int i = 0; i < kProducts; ++i) {
+        g.first[i] = (int)tiles;
+        if (i >= count) continue;
+        const bool amn = a_mn(MODE), bmn = b_mn(MODE);
+        const auto op_a = [&](CUtensorMap *m, const void *base) {
+            if (e == cudaSuccess) e = operand(m, base, amn ? p[i].k : p[i].m, amn ? p[i].m : p[i].k, amn);
+        };
+        const auto op_b = [&](CUtensorMap *m, const void *base) {
+            if (e == cudaSuccess) e = operand(m, base, bmn ? p[i].k : p[i].n, bmn ? p[i].n : p[i].k, bmn);
+        };
+        op_a(&maps.a[i], p[i].a);
+        op_b(&maps.b[i], p[i].b);
+        if (MODE == kInput) op_a(&maps.a[1], p[i].a2);
+        if (MODE == kInput || MODE == kGated) op_b(&maps.b[1], p[i].b2);
+        for (int j = 0; j < (MODE == kGated || MODE == kSlopes ? kProducts : 1); ++j)
+            if (p[i].c[j] && e == cudaSuccess) e = result(&maps.c[i + j], p[i].c[j], p[i].m, p[i].n);
+        g.m_tiles[i] = (int)((p[i].m + 255) / 256);
+        g.n_tiles[i] = (int)((p[i].n + (MODE == kGated ? 127 : 255)) / (MODE == kGated ? 128 : 256));
+        g.c_rows[i] = (int)p[i].m;
+        g.cols[i] = (int)p[i].n;
+        tiles += (long long)g.m_tiles[i] * g.n_tiles[i];
+        if (tiles >= (1ll << 30)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "tensor map of a product");
+    g.first[kProducts] = (int)tiles;
+    for (int i = count; i < kProducts; ++i) g.first[i] = (int)tiles;
+    g.status = dev.status;
+    g.spin_limit = dev.spin_limit;
+    auto k = pair_kernel<MODE>;
+    if ((e = allow_smem((const void *)k, kPairSmem)) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
+    const int pairs = (int)std::min<long long>(tiles, dev.sms / 2);
+    prof_before(name, q);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, 2, q, maps, g);
+    prof_after(q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward product launch");
+}
+
+gdn_status check(int M, int K, int F, int dtype, int activation) {
+    if (M < 0 || K < 1 || F < 1) return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d K=%d F=%d", M, K, F);
+    if (std::max({M, K, F}) > kMaxExtent) return fail(GDN_ERR_INVALID_ARG, "problem too large: M=%d K=%d F=%d", M, K, F);
+    if (K % 8 != 0 || F % 8 != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "K = %d, F = %d: rows start on 16 bytes, multiples of 8", K, F);
+    if (dtype != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d is not GDN_BF16", dtype);
+    if (activation != GDN_ACT_SILU && activation != GDN_ACT_GELU)
+        return fail(GDN_ERR_UNSUPPORTED, "activation %d is not GDN_ACT_SILU or GDN_ACT_GELU", activation);
+    return GDN_OK;
+}
+// Bytes of `count` [M, F] tensors, each from a 256-byte boundary on.
+size_t hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace ffn
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_ffn_fwd_workspace_size(const gdn_ffn_fwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (ffn::check(a->M, a->K, a->F, a->dtype, a->activation) != GDN_OK) return 0;
+    return a->M == 0 ? 256 : std::max<size_t>(512, ffn::hidden_bytes(a->M, a->F));
+}
+
+gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = ffn::check(a->M, a->K, a->F, a->dtype, a->activation);
+    if (st != GDN_OK || a->M == 0) return st;
+    if (!a->x || !a->w_gate || !a->w_up || !a->w_down || !a->y || !a->gate != !a->up)
+        return fail(GDN_ERR_INVALID_ARG, "x, w_gate, w_up, w_down and y are required, gate and up together or not at all");
+    if (misaligned(a->x) || misaligned(a->w_gate) || misaligned(a->w_up) || misaligned(a->w_down) ||
+        misaligned(a->y) || misaligned(a->gate) || misaligned(a->up))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    const size_t need = gdn_ffn_fwd_workspace_size(a);
+    if (!ws || misaligned(ws) || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    cudaStream_t q = (cudaStream_t)stream;
+    ffn::PairArgs g{};
+    g.save = a->gate != nullptr;
+    g.gelu = a->activation == GDN_ACT_GELU;
+    const ffn::Product up{a->x, a->w_gate, a->w_up, nullptr, {ws, a->gate, a->up}, a->M, a->F, a->K};
+    const ffn::Product down{ws, a->w_down, nullptr, nullptr, {a->y}, a->M, a->K, a->F};
+    st = ffn::run_pair<ffn::kGated>("ffn_gated", &up, 1, g, dev, q);
+    return st == GDN_OK ? ffn::run_pair<ffn::kDown>("ffn_down", &down, 1, g, dev, q) : st;
+}
+
+size_t gdn_ffn_bwd_workspace_size(const gdn_ffn_bwd_args *a) {
+    if (!a) {
+        fail(GDN_ERR_INVALID_ARG, "null args");
+        return 0;
+    }
+    if (ffn::check(a->M, a->K, a->F, a->dtype, a->activation) != GDN_OK) return 0;
+    return a->M == 0 ? 256 : std::max<size_t>(512, 3 * ffn::hidden_bytes(a->M, a->F));
+}
+
+gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (!a) return fail(GDN_ERR_INVALID_ARG, "null args");
+    gdn_status st = ffn::check(a->M, a->K, a->F, a->dtype, a->activation);
+    if (st != GDN_OK) return st;
+    if (!a->dw_gate || !a->dw_up || !a->dw_down ||
+        (a->M > 0 && (!a->d_y || !a->x || !a->w_gate || !a->w_up || !a->w_down || !a->gate || !a->up || !a->dx)))
+        return fail(GDN_ERR_INVALID_ARG, "d_y, x, the weights, gate, up, dx and the weights' gradients are required");
+    if (misaligned(a->d_y) || misaligned(a->x) || misaligned(a->w_gate) || misaligned(a->w_up) ||
+        misaligned(a->w_down) || misaligned(a->gate) || misaligned(a->up) || misaligned(a->dx) ||
+        misaligned(a->dw_gate) || misaligned(a->dw_up) || misaligned(a->dw_down))
+        return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    const size_t need = gdn_ffn_bwd_workspace_size(a);
+    if (need > 256 && (!ws || misaligned(ws) || ws_bytes < need))
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    LayerDevice dev;
+    if ((st = layer_device(&dev)) != GDN_OK) return st;
+    cudaStream_t q = (cudaStream_t)stream;
+    if (a->M == 0) {                                 // gradients of no tokens
+        const size_t bytes = (size_t)a->F * a->K * 2;
+        cudaError_t e = cudaMemsetAsync(a->dw_gate, 0, bytes, q);
+        if (e == cudaSuccess) e = cudaMemsetAsync(a->dw_up, 0, bytes, q);
+        if (e == cudaSuccess) e = cudaMemsetAsync(a->dw_down, 0, bytes, q);
+        return e == cudaSuccess ? GDN_OK : cuda_fail(e, "clearing the weights' gradients");
+    }
+    uint8_t *dg = (uint8_t *)ws, *du = dg + ffn::hidden_bytes(a->M, a->F), *h = du + ffn::hidden_bytes(a->M, a->F);
+    ffn::PairArgs g{};
+    g.gelu = a->activation == GDN_ACT_GELU;
+    g.gate = (const __nv_bfloat16 *)a->gate;
+    g.up = (const __nv_bfloat16 *)a->up;
+    const ffn::Product dh{a->d_y, a->w_down, nullptr, nullptr, {dg, du, h}, a->M, a->F, a->K};
+    const ffn::Product dx{dg, a->w_gate, a->w_up, du, {a->dx}, a->M, a->K, a->F};
+    const ffn::Product dw[3] = {{dg, a->x, nullptr, nullptr, {a->dw_gate}, a->F, a->K, a->M},
+                                {du, a->x, nullptr, nullptr, {a->dw_up}, a->F, a->K, a->M},
+                                {a->d_y, h, nullptr, nullptr, {a->dw_down}, a->K, a->F, a->M}};
+    st = ffn::run_pair<ffn::kSlopes>("ffn_slopes", &dh, 1, g, dev, q);
+    if (st == GDN_OK) st = ffn::run_pair<ffn::kInput>("ffn_input", &dx, 1, g, dev, q);
+    if (st == GDN_OK) st = ffn::run_pair<ffn::kWeights>("ffn_weights", dw, 3, g, dev, q);
+    return st;
+}
+
+}  // extern "C"

@@ -2,7 +2,8 @@
  * gdn_layer.h -- C ABI of libgdn.so for the operators a recurrent layer needs
  * around the gated delta rule of gdn.h: the residual addition with the RMS
  * norm, microscaled (MX) quantisation and products, a per-channel gated linear
- * recurrence, the short causal convolution, and the selective state space scan.
+ * recurrence, the short causal convolution, the selective state space scan, and the gated
+ * feed-forward block.
  *
  * The conventions are those of gdn.h: device pointers on the current device,
  * contiguous row-major tensors whose bases are 16-byte aligned, every call
@@ -328,6 +329,46 @@ size_t gdn_ssm_bwd_workspace_size(const gdn_ssm_bwd_args *args);
 gdn_status gdn_ssm_bwd(const gdn_ssm_bwd_args *args, void *workspace, size_t workspace_bytes,
                        void *stream);
 gdn_status gdn_ssm_step(const gdn_ssm_step_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated feed-forward block of M tokens of width K, F features wide inside:
+ *
+ *     g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T
+ *
+ * act is silu, or gelu in its tanh form.  bf16 tensors, fp32 sums; h is rounded to bf16 between the
+ * products.  K and F are multiples of 8. */
+typedef struct gdn_ffn_fwd_args {
+    const void *x;              /* [M, K], dtype                                     */
+    const void *w_gate, *w_up;  /* [F, K], dtype                                     */
+    const void *w_down;         /* [K, F], dtype                                     */
+    int32_t M, K, F;
+    int32_t dtype;              /* GDN_BF16                                          */
+    int32_t activation;         /* GDN_ACT_SILU or GDN_ACT_GELU                      */
+    void *y;                    /* [M, K], dtype                                     */
+    void *gate, *up;            /* [M, F], dtype: g and u for the backward pass; NULL
+                                   (both) = not written                              */
+} gdn_ffn_fwd_args;
+
+/* Backward, dh = dy w_down:  dg = dh u act'(g), du = dh act(g);  dx = dg w_gate + du w_up;
+ * dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h (h from gate and up once more).  dg, du and h
+ * are rounded to bf16 between the products. */
+typedef struct gdn_ffn_bwd_args {
+    const void *d_y;            /* [M, K], dtype                                     */
+    const void *x, *w_gate, *w_up, *w_down;                        /* the forward's  */
+    const void *gate, *up;      /* [M, F], dtype: what the forward wrote             */
+    int32_t M, K, F;
+    int32_t dtype, activation;
+    void *dx;                   /* [M, K], dtype                                     */
+    void *dw_gate, *dw_up;      /* [F, K], dtype                                     */
+    void *dw_down;              /* [K, F], dtype                                     */
+} gdn_ffn_bwd_args;
+
+size_t gdn_ffn_fwd_workspace_size(const gdn_ffn_fwd_args *args);
+gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *args, void *workspace, size_t workspace_bytes,
+                       void *stream);
+size_t gdn_ffn_bwd_workspace_size(const gdn_ffn_bwd_args *args);
+gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *args, void *workspace, size_t workspace_bytes,
+                       void *stream);
 
 #ifdef __cplusplus
 }

@@ -12,6 +12,9 @@ OK = dict(
     gdn_ssm_bwd=dict(d_y=4096, x=4096, dt=4096, a=4096, b=4096, c=4096, dx=4096, ddt=4096, da=4096, db=4096, dc=4096,
                      B=2, T=5, D=64, S=16),
     gdn_ssm_step=dict(x=4096, dt=4096, a=4096, b=4096, c=4096, state=4096, y=4096, out_state=4096, N=2, D=64, S=16),
+    gdn_ffn_fwd=dict(x=4096, w_gate=4096, w_up=4096, w_down=4096, y=4096, M=3, K=64, F=128, dtype=1, activation=1),
+    gdn_ffn_bwd=dict(d_y=4096, x=4096, w_gate=4096, w_up=4096, w_down=4096, gate=4096, up=4096, dx=4096, dw_gate=4096,
+                     dw_up=4096, dw_down=4096, M=3, K=64, F=128, dtype=1, activation=1),
 )
 
 
@@ -71,6 +74,20 @@ def call(abi, name, **kw):
     ("gdn_ssm_step", dict(out_state=None), 1, "required"),
     ("gdn_ssm_step", dict(state=4104), 1, "aligned"),
     ("gdn_ssm_step", dict(N=TOP), 1, "too large"),
+    ("gdn_ffn_fwd", dict(M=-1), 1, "bad sizes"),
+    ("gdn_ffn_fwd", dict(K=0), 1, "bad sizes"),
+    ("gdn_ffn_fwd", dict(K=60), 2, "multiples of 8"),
+    ("gdn_ffn_fwd", dict(F=100), 2, "multiples of 8"),
+    ("gdn_ffn_fwd", dict(F=TOP), 1, "too large"),
+    ("gdn_ffn_fwd", dict(dtype=0), 2, "dtype"),
+    ("gdn_ffn_fwd", dict(activation=0), 2, "activation"),
+    ("gdn_ffn_fwd", dict(gate=4096), 1, "together"),
+    ("gdn_ffn_fwd", dict(w_down=None), 1, "required"),
+    ("gdn_ffn_fwd", dict(y=4104), 1, "aligned"),
+    ("gdn_ffn_bwd", dict(dw_up=None), 1, "required"),
+    ("gdn_ffn_bwd", dict(up=None), 1, "required"),
+    ("gdn_ffn_bwd", dict(dx=4100), 1, "aligned"),
+    ("gdn_ffn_bwd", dict(activation=7), 2, "activation"),
 ])
 def test_bad_arguments_are_rejected_on_the_host(abi, name, bad, rc, msg):
     assert call(abi, name, **bad) == rc
@@ -94,6 +111,7 @@ def test_null_arguments_and_small_workspaces(abi):
 def test_empty_problems_are_host_side_no_ops(abi):
     assert call(abi, "gdn_conv_step", N=0) == 0
     assert call(abi, "gdn_ssm_step", N=0) == 0
+    assert call(abi, "gdn_ffn_fwd", M=0) == 0
     assert abi.ENTRIES["gdn_conv_bwd"].workspace_size(raw(abi, "gdn_conv_bwd", T=0)) == 256
 
 
