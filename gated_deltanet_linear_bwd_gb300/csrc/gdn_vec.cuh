@@ -44,21 +44,26 @@ struct Vec {
     }
 };
 
-// The logistic function.  fp32 tensors take the accurate functions; of bf16 ones, whose results
-// are rounded to 2^-9 of themselves, the hardware's exponential and reciprocal (2^-21).
-template <typename T>
-__device__ __forceinline__ float logistic(float x) {
-    if (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
-    return __fdividef(1.f, 1.f + __expf(-x));
-}
-// d(x logistic(x)) / dx, s = logistic(x).
-__device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f + x * (1.f - s)); }
-
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The logistic function.  fp32 tensors take the accurate functions; of bf16 ones, whose results
+// are rounded to 2^-8 of themselves, the hardware's exponential and reciprocal (2^-21).
+template <typename T>
+__device__ __forceinline__ float logistic(float x) {
+    if (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
+    return rcp(1.f + ex2(x * -1.4426950408889634f));
+}
+// d(x logistic(x)) / dx, s = logistic(x).
+__device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f + x * (1.f - s)); }
 
 // log(1 + e^x).  Of bf16 tensors with the hardware's exponential and logarithm, but for e = e^-|x| <
 // 1/8, where the logarithm of the rounded 1 + e would lose what a small step is made of: there e p(e),
