@@ -27,6 +27,11 @@ __device__ __forceinline__ void pdl_enter() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The same for kernels whose few long-lived CTAs have to be spread evenly over the SMs: the dependents
+// start only when this kernel's CTAs leave.  Let in earlier, they would be placed on whatever slots
+// these CTAs leave free, several to some SMs and none to others, and stay there.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Everything a kernel needs to locate a sequence, chunk or segment and to
 // read the inputs.  Passed by value.
 struct Geo {

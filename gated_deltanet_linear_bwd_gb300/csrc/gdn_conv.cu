@@ -48,14 +48,6 @@ __device__ __forceinline__ void clear(float2 (&v)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = make_float2(0.f, 0.f);
 }
-template <typename T>
-__device__ __forceinline__ float2 logistic2(float2 x) {
-    if (sizeof(T) == 4) return make_float2(logistic<T>(x.x), logistic<T>(x.y));
-    const float2 y = __fmul2_rn(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    const float2 e = __fadd2_rn(make_float2(ex2(y.x), ex2(y.y)), make_float2(1.f, 1.f));
-    return make_float2(rcp(e.x), rcp(e.y));
-}
-
 // A thread's own loads, GROUPS groups of kAhead tokens of N tensors in flight, by cp.async to shared
 // memory: in registers there is no room for enough of them (16 x (512 .. 8192) x 4096 bf16 forward 200
 // us from registers, 176 so; backward of 4 x 4096 x 4096 110, 97).  Only the thread that asked reads them, so that no barrier is needed.

@@ -4,9 +4,10 @@
 //
 //     h_t = exp(delta_t a) h_{t-1} + delta_t x_t b_t,   y_t = (<c_t, h_t> + skip x_t) silu(z_t)
 //
-// A channel's states are shared out to LP lanes, four to each, which stay in registers while the
-// lanes walk the tokens; x, dt, b and c come through shared memory a tile at a time, the step's
-// softplus taken once for all lanes.  <c, h> of LP tokens is added up over the lanes together.
+// A channel's states are shared out to LP lanes, eight to each (four in the backward pass), which stay
+// in registers while the lanes walk the tokens; x, dt, z, b and c come through shared memory a tile at a
+// time, the step's softplus and the gate taken once for all lanes.  <c, h> of a few tokens is added up
+// over the lanes together.
 //
 // Where sequences and channels are too few for the GPU, sequences are cut into parts that are
 // walked twice: first for a part's end state from zero and the sum of its steps (whose exponential
@@ -25,7 +26,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 256;
 constexpr int kMaxStates = 64;
-constexpr int kItems = 8 * kThreads;               // (token, channel) pairs of a tile: eight to a thread
 constexpr int kSegment = 64;                       // tokens of the backward pass's segments
 constexpr int kSub = 8;                            // tokens whose decays it holds in registers
 
@@ -37,12 +37,12 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // (a step of 0 still gives exactly 1).  fp32 tensors take for |y| < 1/32 the polynomial 1 + y q(y), q
 // through (2^y - 1) / y at the three Chebyshev points of -1/32 .. 1/32 (1.1e-7 of y).
 template <typename T>
-__device__ __forceinline__ float2 decay(float step, float2 a2) {
+__device__ __forceinline__ float2 decay(float2 step, float2 a2) {
     if (sizeof(T) == 2) {
-        const float2 y = __ffma2_rn(both(step), a2, both(1.73e-8f));
+        const float2 y = __ffma2_rn(step, a2, both(1.73e-8f));
         return make_float2(ex2(y.x), ex2(y.y));
     }
-    const float2 y = __fmul2_rn(both(step), a2);
+    const float2 y = __fmul2_rn(step, a2);
     float2 p = __ffma2_rn(y, both(5.5505085252e-2f), both(2.4023355157e-1f));
     p = __ffma2_rn(p, y, both(0.6931471805599453f));
     p = __ffma2_rn(p, y, both(1.f));
@@ -152,25 +152,40 @@ __device__ __forceinline__ void params8(const float *p, int ch, int D, float (&v
     for (int i = 0; i < 8; ++i) v[i] = p && ch + i < D ? p[ch + i] : 0.f;
 }
 
-// A lane's four states of a [.., D, S] tensor.
-__device__ __forceinline__ void load_states(const float *base, long long row, int S, int s0, bool in, float2 (&v)[2]) {
-    float f[4];
+// A lane's 2 P neighbouring states, from s0 on, of a row of a [.., D, S] tensor.
+template <int P>
+__device__ __forceinline__ void load_states(const float *base, long long row, int S, int s0, bool in, float2 (&v)[P]) {
+    const float *p = base + row * S + s0;
+    const bool there = base && in;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = base && in && s0 + i < S ? base[row * S + s0 + i] : 0.f;
-    v[0] = make_float2(f[0], f[1]);
-    v[1] = make_float2(f[2], f[3]);
+    for (int i = 0; i < P; i += 2) {
+        if ((S & 3) == 0) {
+            const float4 f = there && s0 + 2 * i < S ? *reinterpret_cast<const float4 *>(p + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = make_float2(f.x, f.y);
+            v[i + 1] = make_float2(f.z, f.w);
+        } else {
+#pragma unroll
+            for (int j = i; j < i + 2; ++j)
+                v[j] = make_float2(there && s0 + 2 * j < S ? p[2 * j] : 0.f, there && s0 + 2 * j + 1 < S ? p[2 * j + 1] : 0.f);
+        }
+    }
 }
-__device__ __forceinline__ void store_states(float *base, long long row, int S, int s0, bool in, const float2 (&v)[2]) {
+template <int P>
+__device__ __forceinline__ void store_states(float *base, long long row, int S, int s0, bool in, const float2 (&v)[P]) {
     if (!in) return;
     float *p = base + row * S + s0;
-    if ((S & 3) == 0) {
-        if (s0 < S) *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        return;
-    }
-    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (s0 + i < S) p[i] = f[i];
+    for (int i = 0; i < P; i += 2) {
+        if ((S & 3) == 0) {
+            if (s0 + 2 * i < S) *reinterpret_cast<float4 *>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+        } else {
+#pragma unroll
+            for (int j = i; j < i + 2; ++j) {
+                if (s0 + 2 * j < S) p[2 * j] = v[j].x;
+                if (s0 + 2 * j + 1 < S) p[2 * j + 1] = v[j].y;
+            }
+        }
+    }
 }
 
 // Adds up NV values over NL lanes that are STRIDE apart, `lane` being this one's place among them.
@@ -221,17 +236,37 @@ struct FwdArgs {
 // that its tokens leave to the state before it.
 enum Mode { kOutputs, kPairs, kBothPairs };
 
-// Shared memory of a tile: TT = 8 LP tokens of CH = 256 / LP channels.
-template <int LP>
-struct Tile {
-    static constexpr int CH = kThreads / LP, TT = 8 * LP;
-    static constexpr int YS = CH + (LP == 16 ? 4 : 32 / LP);    // the row of a lane's token in other banks
-    float2 du[kItems];                             // step, step x
-    float y[TT * YS];                              // <c, h>, or the gradient before the gate
-    float4 b[TT * LP], c[TT * LP];
+// A lane has eight states of two channels, LP lanes share a pair of channels.  What bounds the walk
+// beside its arithmetic is what the lanes read of shared memory: b and c, which every channel needs.
+// Two channels to a lane, and states by pairs through the arithmetic on two numbers at once, take 80
+// bytes for 16 states; four states of one channel 40 bytes for four, and pairs of channels, with b and
+// c there twice, 144 for 16 (4.9 ps a token and channel of 16 states, the rate of shared memory).
+//
+// The lanes take U tokens at a time, each lane U / LP of them as its own: it loads their x, dt and z
+// kAhead groups ahead, by cp.async to shared memory (of loads to registers a warp can only await all
+// that are in flight), makes their steps and gates, leaves the steps to the others in shared memory,
+// and stores their y when the lanes have added up <c, h>.  So a warp waits for the CTA's others only
+// for b and c, of TB tokens at a time (whole pairs of groups).
+constexpr int kFwdThreads = 128;
+constexpr int kStates = 8;                         // of a lane and channel
+constexpr int kAhead = 4;
+template <typename T, int LP>
+struct Lanes {
+    static constexpr int CH = 2 * kFwdThreads / LP, SP = kStates * LP;
+    static constexpr int U = LP <= 4 ? 4 : LP, OWN = U / LP, TB = LP <= 4 ? 64 / LP : 2 * U;
+    struct Two {
+        T e[2];
+    };
+    struct Shared {
+        float4 b[2][TB * SP / 4], c[2][TB * SP / 4];
+        float4 du[2][U][kFwdThreads / LP];         // steps and steps x, two groups in turn
+        float2 ds[2][U][kFwdThreads / LP];         // and gradients before the gate
+        alignas(16) Two raw[kAhead + 1][OWN][4][kFwdThreads];    // a lane's x, dt, z, dy
+    };
 };
 
-// The j-th longest of up to 256 sequences: long ones are not left for the end.
+// The j-th longest of up to kMaxOrdered sequences: long ones are not left for the end.
+constexpr int kMaxOrdered = kFwdThreads;
 __device__ __forceinline__ int longest(const Seqs &s, int j, int *scratch) {
     const int t = threadIdx.x;
     if (t < s.N) scratch[t] = s.cu[t + 1] - s.cu[t];
@@ -240,130 +275,268 @@ __device__ __forceinline__ int longest(const Seqs &s, int j, int *scratch) {
         const int mine = scratch[t];
         int rank = 0;
         for (int u = 0; u < s.N; ++u) rank += scratch[u] > mine || (scratch[u] == mine && u < t);
-        if (rank == j) scratch[kThreads] = t;
+        if (rank == j) scratch[kMaxOrdered] = t;
     }
     __syncthreads();
-    const int n = scratch[kThreads];
+    const int n = scratch[kMaxOrdered];
     __syncthreads();
     return n;
 }
 
-template <typename T, int LP>
-__device__ __forceinline__ void load_bc(float4 *to, const void *from, long long token, int tokens, int live, int S) {
-    // [tokens][S] as [tokens][4 LP], zeros behind
-    for (int k = threadIdx.x; k < tokens * 4 * LP; k += blockDim.x) {
-        const int t = k / (4 * LP), s = k % (4 * LP);
-        reinterpret_cast<float *>(to)[k] = t < live && s < S ? to_f(((const T *)from)[(token + t) * S + s]) : 0.f;
+// b or c of a tile, [tokens][S] as [tokens][SP] with zeros behind, a few to a thread.
+template <typename T, int TT, int SP, int THREADS>
+struct Coefficients {
+    static constexpr int N = (TT * SP + THREADS - 1) / THREADS;
+    T v[N];                                        // converted only when they are put down: that waits for them
+    // Tokens from `token` on, `live` of them (FULL: all of the tile's).
+    template <bool FULL>
+    __device__ __forceinline__ void fetch(const void *from, long long token, int live, int S) {
+        const T *p = (const T *)from + token * S;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = threadIdx.x + i * THREADS, t = k / SP, s = k % SP;
+            v[i] = (FULL ? N * THREADS == TT * SP || t < TT : t < live) && s < S ? p[t * S + s] : T(0.f);
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void put(F put_one) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (N * THREADS == TT * SP || threadIdx.x + i * THREADS < TT * SP) put_one(threadIdx.x + i * THREADS, to_f(v[i]));
+    }
+};
+
+// Two neighbouring elements of T, of which the second may not exist; PAIRS: rows of even width, which
+// cp.async can copy them from.
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void copy2(T *to, const T *from, bool both_in) {
+    if (PAIRS) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                     "n"(2 * (int)sizeof(T))
+                     : "memory");
+    } else {
+        to[0] = from[0];
+        if (both_in) to[1] = from[1];
+    }
+}
+template <typename T>
+__device__ __forceinline__ float2 get2(const T *e) {
+    float f[2];
+    Vec<T, 2>::load(e, f);
+    return make_float2(f[0], f[1]);
+}
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void store2(T *p, bool both_in, float2 v) {
+    if (PAIRS) {
+        const float f[2] = {v.x, v.y};
+        Vec<T, 2>::store(p, f);
+    } else {
+        from_f(p, v.x);
+        if (both_in) from_f(p + 1, v.y);
     }
 }
 
-template <typename T, int LP, bool VECT, int MODE>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(FwdArgs a) {
-    using L = Tile<LP>;
+// A lane's states of two channels, [channel][pairs of states]: of each channel 4 (i LP + s) to + 3, i = 0
+// and 1, so that the lanes' b and c lie side by side.
+using LaneStates = float2[2][kStates / 2];
+template <int LP>
+__device__ __forceinline__ void load_lane(const float *base, long long row, int S, int s, bool in0, bool in1, LaneStates &v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 p[2];
+        load_states(base, row + (i & 1), S, 4 * (i / 2 * LP + s), i & 1 ? in1 : in0, p);
+        v[i & 1][i / 2 * 2] = p[0];
+        v[i & 1][i / 2 * 2 + 1] = p[1];
+    }
+}
+template <int LP>
+__device__ __forceinline__ void store_lane(float *base, long long row, int S, int s, bool in0, bool in1, const LaneStates &v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p[2] = {v[i & 1][i / 2 * 2], v[i & 1][i / 2 * 2 + 1]};
+        store_states(base, row + (i & 1), S, 4 * (i / 2 * LP + s), i & 1 ? in1 : in0, p);
+    }
+}
+
+template <typename T, int LP, bool PAIRS, int MODE>
+__global__ void __launch_bounds__(kFwdThreads, MODE == kBothPairs ? 3 : 4) fwd_kernel(FwdArgs a) {
+    using L = Lanes<T, LP>;
+    constexpr int U = L::U, OWN = L::OWN;
     extern __shared__ __align__(16) uint8_t shared[];
-    L &tile = *reinterpret_cast<L *>(shared);
-    pdl_enter();
+    typename L::Shared &m = *reinterpret_cast<typename L::Shared *>(shared);
+    pdl_wait();
 
     const int group = blockIdx.x % a.in.groups;
     int slot = blockIdx.x / a.in.groups;
     if (a.longest_first) slot = longest(a.cut.s, slot, reinterpret_cast<int *>(shared));
     Part part;
     if (!part_of(a.cut, slot, part)) return;
-    const int D = a.in.D, S = a.in.S;
-    // as one of the lanes: a channel and four states of it
-    const int s = threadIdx.x % LP, c = threadIdx.x / LP, ch = group * L::CH + c;
-    const bool in = ch < D;
-    // as one that loads and stores: eight channels of a token
-    const int mt = threadIdx.x * 8 / L::CH, mc = threadIdx.x * 8 % L::CH, mch = group * L::CH + mc;
-    float bias[8], skip[8];
-    params8(a.in.dt_bias, mch, D, bias);
-    params8(a.in.skip, mch, D, skip);
+    const int D = a.in.D, S = a.in.S, len = part.len, blocks = (len + L::TB - 1) / L::TB;
+    const int pair = threadIdx.x / LP, s = threadIdx.x % LP;
+    const int ch = group * L::CH + 2 * pair;
+    const bool in0 = ch < D, in1 = ch + 1 < D;
 
-    float2 a2[2], h[2], P[2] = {both(1.f), both(1.f)}, acc[2] = {both(0.f), both(0.f)};
-    load_states(a.in.a, ch, S, 4 * s, in, a2);
-    a2[0] = __fmul2_rn(a2[0], both(kLog2e));
-    a2[1] = __fmul2_rn(a2[1], both(kLog2e));
-    h[0] = h[1] = both(0.f);
-    if (MODE == kOutputs) {
-        if (a.start) load_states(a.start, (long long)slot * D + ch, S, 4 * s, in, h);
-        else load_states(a.h0, (long long)part.n * D + ch, S, 4 * s, in, h);
-    }
-    float steps = 0.f;
-
-    Eight<T> x, dt, z, dy;
-    const auto fetch = [&](int at) {
-        const bool live = at + mt < part.len;
-        x = load8<T, VECT>(a.in.x, part.first + at + mt, mch, D, live);
-        dt = load8<T, VECT>(a.in.dt, part.first + at + mt, mch, D, live);
-        if (MODE != kPairs) z = load8<T, VECT>(a.in.z, part.first + at + mt, mch, D, live);
-        if (MODE == kBothPairs) dy = load8<T, VECT>(a.in.dy, part.first + at + mt, mch, D, live);
-    };
-    fetch(0);
-    for (int at = 0; at < part.len; at += L::TT) {
-        const int tokens = min(L::TT, part.len - at);
-        const bool live = mt < tokens;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float raw = dt.at(i) + bias[i];
-            const float step = !live ? 0.f : a.in.dt_bias ? softplus<T>(raw) : raw;
-            tile.du[mt * L::CH + mc + i] = make_float2(step, step * x.at(i));
-            if (MODE == kBothPairs) {
-                const float zi = z.at(i);
-                tile.y[mt * L::YS + mc + i] = a.in.z ? dy.at(i) * zi * logistic<T>(zi) : dy.at(i);
-            }
+    Coefficients<T, L::TB, L::SP, kFwdThreads> nb, nc;
+    const auto fetch = [&](int k) {
+        const long long token = part.first + k * L::TB;
+        const int left = len - k * L::TB;
+        if (left >= L::TB) {
+            nb.template fetch<true>(a.in.b, token, left, S);
+            if (MODE != kPairs) nc.template fetch<true>(a.in.c, token, left, S);
+        } else if (left > 0) {
+            nb.template fetch<false>(a.in.b, token, left, S);
+            if (MODE != kPairs) nc.template fetch<false>(a.in.c, token, left, S);
         }
-        load_bc<T, LP>(tile.b, a.in.b, part.first + at, L::TT, tokens, S);
-        if (MODE != kPairs) load_bc<T, LP>(tile.c, a.in.c, part.first + at, L::TT, tokens, S);
-        const Eight<T> cx = x, cz = z;
-        fetch(at + L::TT);
-        __syncthreads();
-        for (int t = 0; t < tokens; t += LP) {
-            float v[LP];
+    };
+    const auto put = [&](int k) {
+        nb.put([&](int i, float v) { reinterpret_cast<float *>(m.b[k & 1])[i] = v; });
+        if (MODE != kPairs) nc.put([&](int i, float v) { reinterpret_cast<float *>(m.c[k & 1])[i] = v; });
+    };
+    // this lane's tokens of a group, OWN from t on; what lies past the end keeps what was there
+    const long long base = part.first * D + ch;
+    int asked = 0, taken = 0;
+    const auto ask = [&](int t) {
 #pragma unroll
-            for (int k = 0; k < LP; ++k) {
-                const float2 du = tile.du[(t + k) * L::CH + c];
-                const float4 b = tile.b[(t + k) * LP + s];
-                const float2 e0 = decay<T>(du.x, a2[0]), e1 = decay<T>(du.x, a2[1]);
-                h[0] = __ffma2_rn(e0, h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
-                h[1] = __ffma2_rn(e1, h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
-                if (MODE != kOutputs) steps += du.x;
-                if (MODE != kPairs) {
-                    const float4 cc = tile.c[(t + k) * LP + s];
-                    if (MODE == kOutputs) {
-                        float2 d = __fmul2_rn(make_float2(cc.x, cc.y), h[0]);
-                        d = __ffma2_rn(make_float2(cc.z, cc.w), h[1], d);
-                        v[k] = d.x + d.y;
-                    } else {
-                        const float ds = tile.y[(t + k) * L::YS + c];
-                        P[0] = __fmul2_rn(P[0], e0);
-                        P[1] = __fmul2_rn(P[1], e1);
-                        acc[0] = __ffma2_rn(P[0], __fmul2_rn(both(ds), make_float2(cc.x, cc.y)), acc[0]);
-                        acc[1] = __ffma2_rn(P[1], __fmul2_rn(both(ds), make_float2(cc.z, cc.w)), acc[1]);
+        for (int j = 0; j < OWN; ++j) {
+            if (t + j >= len || !in0) continue;
+            const long long at = base + (long long)(t + j) * D;
+            const auto copy = [&](int what, const void *from) {
+                copy2<T, PAIRS>(m.raw[asked][j][what][threadIdx.x].e, (const T *)from + at, in1);
+            };
+            copy(0, a.in.x);
+            copy(1, a.in.dt);
+            if (MODE != kPairs && a.in.z) copy(2, a.in.z);
+            if (MODE == kBothPairs) copy(3, a.in.dy);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++asked == kAhead + 1) asked = 0;
+    };
+    const auto param = [&](const float *p) { return make_float2(p && in0 ? p[ch] : 0.f, p && in1 ? p[ch + 1] : 0.f); };
+    const float2 bias = param(a.in.dt_bias), skip = param(a.in.skip);
+
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) ask(g * U + s * OWN);
+    fetch(0);
+    LaneStates a2, h, prod, acc;
+    float2 steps = both(0.f);
+    load_lane<LP>(a.in.a, ch, S, s, in0, in1, a2);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < kStates / 2; ++i) {
+            a2[c][i] = __fmul2_rn(a2[c][i], both(kLog2e));
+            h[c][i] = acc[c][i] = both(0.f);
+            prod[c][i] = both(1.f);
+        }
+    if (MODE == kOutputs)
+        load_lane<LP>(a.start ? a.start : a.h0, (long long)(a.start ? slot : part.n) * D + ch, S, s, in0, in1, h);
+    put(0);
+    fetch(1);
+    __syncthreads();
+
+    // Of the group from token t on: this lane's tokens' steps, and what their outputs will take.
+    struct Gates {
+        float2 sx[OWN], gate[OWN];
+    };
+    const auto own_tokens = [&](int which, int t, Gates &g) {
+        const int own = t + s * OWN;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const auto mine = [&](int j, int what) { return get2(m.raw[taken][j][what][threadIdx.x].e); };
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            const float2 xi = mine(j, 0);
+            float2 st = mine(j, 1);
+            if (a.in.dt_bias) st = softplus2<T>(__fadd2_rn(st, bias));
+            const bool live = own + j < len;
+            float2 u = __fmul2_rn(st, xi);
+            if (!live) st = u = both(0.f);
+            m.du[which][s * OWN + j][pair] = make_float4(st.x, st.y, u.x, u.y);
+            if (MODE == kPairs) continue;
+            g.gate[j] = both(1.f);
+            if (a.in.z) {
+                g.gate[j] = mine(j, 2);
+                g.gate[j] = __fmul2_rn(g.gate[j], logistic2<T>(g.gate[j]));
+            }
+            if (MODE == kOutputs) g.sx[j] = __fmul2_rn(skip, xi);
+            else m.ds[which][s * OWN + j][pair] = live ? __fmul2_rn(g.gate[j], mine(j, 3)) : both(0.f);
+        }
+        if (++taken == kAhead + 1) taken = 0;
+        ask(own + kAhead * U);
+    };
+    const auto walk = [&](int which, int t, const Gates &g, const float4 *bt, const float4 *ct) {
+        float v[2 * U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const float4 du = m.du[which][j][pair];
+            const float2 ds = MODE == kBothPairs ? m.ds[which][j][pair] : both(0.f);
+            float2 dot[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {          // four states
+                const float4 b4 = bt[(j * 2 + q) * LP], c4 = MODE != kPairs ? ct[(j * 2 + q) * LP] : b4;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {      // two of them
+                    const int i = 2 * q + o;
+                    const float2 b = o ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+                    const float2 cc = o ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float2 e = decay<T>(both(c ? du.y : du.x), a2[c][i]);
+                        h[c][i] = __ffma2_rn(e, h[c][i], __fmul2_rn(both(c ? du.w : du.z), b));
+                        if (MODE == kOutputs) dot[c] = i ? __ffma2_rn(cc, h[c][i], dot[c]) : __fmul2_rn(cc, h[c][i]);
+                        if (MODE == kBothPairs) {
+                            prod[c][i] = __fmul2_rn(prod[c][i], e);
+                            acc[c][i] = __ffma2_rn(prod[c][i], __fmul2_rn(both(c ? ds.y : ds.x), cc), acc[c][i]);
+                        }
                     }
                 }
             }
             if (MODE == kOutputs) {
-                share_sum<LP, LP, 1>(v, s);        // token t + s is this lane's
-                tile.y[(t + s) * L::YS + c] = v[0];
+                v[2 * j] = dot[0].x + dot[0].y;
+                v[2 * j + 1] = dot[1].x + dot[1].y;
+            } else {
+                steps = __fadd2_rn(steps, make_float2(du.x, du.y));
             }
+        }
+        if (MODE != kOutputs) return;
+        share_sum<2 * U, LP, 1>(v, s);             // those of this lane's tokens
+        const int own = t + s * OWN;
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            if (own + j >= len || !in0) continue;
+            const float2 y = __fmul2_rn(__fadd2_rn(make_float2(v[2 * j], v[2 * j + 1]), g.sx[j]), g.gate[j]);
+            store2<T, PAIRS>((T *)a.y + base + (long long)(own + j) * D, in1, y);
+        }
+    };
+    // the next group's steps under this one's walk; a group's are read behind a __syncwarp
+    Gates g0, g1;
+    own_tokens(0, 0, g0);
+    __syncwarp();
+    for (int k = 0; k < blocks; ++k) {
+        const float4 *bt = m.b[k & 1] + s, *ct = m.c[k & 1] + s;
+        const int t0 = k * L::TB, t1 = min(t0 + L::TB, len);
+#pragma unroll 1
+        for (int t = t0; t < t1; t += 2 * U, bt += U * L::SP / 2, ct += U * L::SP / 2) {
+            own_tokens(1, t + U, g1);
+            walk(0, t, g0, bt, ct);
+            __syncwarp();
+            own_tokens(0, t + 2 * U, g0);
+            walk(1, t + U, g1, bt + U * L::SP / 4, ct + U * L::SP / 4);
+            __syncwarp();
+        }
+        if (k + 1 < blocks) {
+            put(k + 1);
+            fetch(k + 2);
         }
         __syncthreads();
-        if (MODE == kOutputs && live) {
-            float out[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                out[i] = fmaf(skip[i], cx.at(i), tile.y[mt * L::YS + mc + i]);
-                if (a.in.z) out[i] *= cz.at(i) * logistic<T>(cz.at(i));
-            }
-            store8<T, VECT>(a.y, part.first + at + mt, mch, D, out);
-        }
     }
     if (MODE == kOutputs) {
-        if (part.ends && a.ht) store_states(a.ht, (long long)part.n * D + ch, S, 4 * s, in, h);
+        if (part.ends && a.ht) store_lane<LP>(a.ht, (long long)part.n * D + ch, S, s, in0, in1, h);
     } else {
-        store_states(a.end, (long long)slot * D + ch, S, 4 * s, in, h);
-        if (MODE == kBothPairs) store_states(a.back, (long long)slot * D + ch, S, 4 * s, in, acc);
-        if (in && s == 0) a.steps[(long long)slot * D + ch] = steps;
+        const long long row = (long long)slot * D + ch;
+        store_lane<LP>(a.end, row, S, s, in0, in1, h);
+        if (MODE == kBothPairs) store_lane<LP>(a.back, row, S, s, in0, in1, acc);
+        if (s == 0 && in0) a.steps[row] = steps.x;
+        if (s == 0 && in1) a.steps[row + 1] = steps.y;
     }
 }
 
@@ -376,7 +549,7 @@ struct JoinArgs {
     Cut cut;
 };
 __global__ void __launch_bounds__(256) join_kernel(JoinArgs a) {
-    pdl_enter();
+    pdl_wait();
     const long long states = (long long)a.D * a.S, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int n = blockIdx.y;
     if (i >= states) return;
@@ -454,7 +627,7 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
     using G = Segment<LP>;
     extern __shared__ __align__(16) uint8_t shared[];
     G &m = *reinterpret_cast<G *>(shared);
-    pdl_enter();
+    pdl_wait();
 
     const int slot = blockIdx.x / a.lanes, lane_no = blockIdx.x - slot * a.lanes;
     const int D = a.in.D, S = a.in.S, tid = threadIdx.x;
@@ -475,8 +648,13 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
         return;
     }
     const int len = part.len, subs = (len + kSub - 1) / kSub;
-    load_bc<T, LP>(m.b, a.in.b, part.first, kSegment, len, S);
-    load_bc<T, LP>(m.c, a.in.c, part.first, kSegment, len, S);
+    {
+        Coefficients<T, kSegment, G::SP, G::NT> co;
+        co.template fetch<false>(a.in.b, part.first, len, S);
+        co.put([&](int i, float v) { reinterpret_cast<float *>(m.b)[i] = v; });
+        co.template fetch<false>(a.in.c, part.first, len, S);
+        co.put([&](int i, float v) { reinterpret_cast<float *>(m.c)[i] = v; });
+    }
     for (int k = tid; k < kSegment * G::V; k += G::NT) m.acc[k] = 0.f;
 
     for (int g = g0; g < g1; ++g) {
@@ -518,8 +696,8 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
                     const int t = q * kSub + k;
                     const float2 du = m.du[t * G::CH + c];
                     const float4 b = m.b[t * LP + s];
-                    h[0] = __ffma2_rn(decay<T>(du.x, a2[0]), h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
-                    h[1] = __ffma2_rn(decay<T>(du.x, a2[1]), h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
+                    h[0] = __ffma2_rn(decay<T>(both(du.x), a2[0]), h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
+                    h[1] = __ffma2_rn(decay<T>(both(du.x), a2[1]), h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
                 }
                 m.saved[q * G::NT + tid] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
             }
@@ -538,7 +716,7 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
                 const float4 b = m.b[t * LP + s];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    e[k][i] = decay<T>(du.x, a2[i]);
+                    e[k][i] = decay<T>(both(du.x), a2[i]);
                     p[k][i] = __fmul2_rn(e[k][i], h[i]);
                     h[i] = __ffma2_rn(both(du.y), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y), p[k][i]);
                 }
@@ -724,7 +902,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 e = decay<T>(step, __fmul2_rn(an[i], both(kLog2e)));
+            const float2 e = decay<T>(both(step), __fmul2_rn(an[i], both(kLog2e)));
             h[i] = __ffma2_rn(e, h[i], __fmul2_rn(both(step * x), make_float2(b[2 * i], b[2 * i + 1])));
             y += h[i].x * cc[2 * i] + h[i].y * cc[2 * i + 1];
         }
@@ -743,33 +921,30 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
 }
 
 // ------------------------------------------------------------------ host
-// Lanes of a channel: four states to each.
-int lanes_of(int S) {
+// Lanes of a channel, with so many states to each.
+int lanes_of(int S, int states) {
     int lp = 1;
-    while (4 * lp < S) lp *= 2;
+    while (states * lp < S) lp *= 2;
     return lp;
 }
-template <typename F>
+template <int MOST, typename F>
 auto by_lanes(int lp, F f) {
-    switch (lp) {
-        case 1: return f(std::integral_constant<int, 1>());
-        case 2: return f(std::integral_constant<int, 2>());
-        case 4: return f(std::integral_constant<int, 4>());
-        case 8: return f(std::integral_constant<int, 8>());
-        default: return f(std::integral_constant<int, 16>());
-    }
+    if (lp == 1) return f(std::integral_constant<int, 1>());
+    if (lp == 2) return f(std::integral_constant<int, 2>());
+    if (lp == 4) return f(std::integral_constant<int, 4>());
+    if (lp == 8 || MOST == 8) return f(std::integral_constant<int, 8>());
+    return f(std::integral_constant<int, MOST>());
 }
 template <typename F>
 auto by_type(int dtype, F f) {
     return dtype == GDN_BF16 ? f((__nv_bfloat16 *)nullptr) : f((float *)nullptr);
 }
 template <typename F>
-auto by_alignment(int D, F f) {
-    return D % 8 == 0 ? f(std::true_type()) : f(std::false_type());
+auto by_alignment(bool whole, F f) {
+    return whole ? f(std::true_type()) : f(std::false_type());
 }
 
 constexpr int kSms = 152;          // of the GPU that the choices below are made for
-constexpr int kMaxOrdered = kThreads;
 
 gdn_status check(int B, int T, int D, int S, int N, int dtype, bool packed) {
     if (B < 1 || T < 0 || D < 1 || S < 1)
@@ -797,12 +972,13 @@ Cut cut_of(const int32_t *cu, int B, int T, int N, int part) {
     return c;
 }
 
-// Tokens of a part of the forward pass, T + 1 for sequences left whole.
+// Tokens of a part of the forward pass, T + 1 for sequences left whole.  Parts (of 128 tokens at least)
+// pay, with their second walk, where whole sequences leave a third of the SMs without a CTA.
 int fwd_part(int B, int T, int D, int S, int N, bool packed) {
-    const int lp = lanes_of(S), ch = kThreads / lp;
+    const int lp = lanes_of(S, kStates), ch = 2 * kFwdThreads / lp;
     const long long n = packed ? N : B, ctas = n * ((D + ch - 1) / ch), mean = packed ? T / n : T;
-    const long long parts = std::min<long long>(4 * kSms / std::max(1ll, ctas), mean / 128);
-    if (parts < 3) return T + 1;
+    const long long fill = 4 * kSms / std::max(1ll, ctas), parts = std::min(fill, mean / 128);
+    if (fill < 6 || parts < 3) return T + 1;
     return (int)((mean + parts - 1) / parts + 7) / 8 * 8;
 }
 
@@ -831,7 +1007,7 @@ struct BwdPlan {
 BwdPlan plan_of(const gdn_ssm_bwd_args *a) {
     BwdPlan p{};
     p.cut = cut_of(a->cu_seqlens, a->B, a->T, a->N, kSegment);
-    const int lp = lanes_of(a->S), ch = lp <= 4 ? 64 : 256 / lp, groups = (a->D + ch - 1) / ch;
+    const int lp = lanes_of(a->S, 4), ch = lp <= 4 ? 64 : 256 / lp, groups = (a->D + ch - 1) / ch;
     // CTAs for about four waves, so that the last one is short
     const long long want = (8ll * kSms + p.cut.slots - 1) / p.cut.slots;
     p.lanes = (int)std::max(1ll, std::min<long long>(groups, want));
@@ -849,16 +1025,16 @@ template <int MODE>
 cudaError_t launch_fwd(const char *name, FwdArgs f, int dtype, cudaStream_t q) {
     return by_type(dtype, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        return by_lanes(lanes_of(f.in.S), [&](auto lp) {
-            return by_alignment(f.in.D, [&](auto vect) {
+        return by_lanes<8>(lanes_of(f.in.S, kStates), [&](auto lp) {
+            return by_alignment(f.in.D % 2 == 0, [&](auto vect) {
                 constexpr int LP = decltype(lp)::value;
                 auto k = fwd_kernel<T, LP, decltype(vect)::value, MODE>;
-                cudaError_t e = allow_smem((const void *)k, sizeof(Tile<LP>));
+                cudaError_t e = allow_smem((const void *)k, sizeof(typename Lanes<T, LP>::Shared));
                 if (e != cudaSuccess) return e;
-                f.in.groups = (f.in.D + Tile<LP>::CH - 1) / Tile<LP>::CH;
+                f.in.groups = (f.in.D + Lanes<T, LP>::CH - 1) / Lanes<T, LP>::CH;
                 prof_before(name, q);
-                e = launch_pdl(k, dim3((unsigned)((long long)f.in.groups * f.cut.slots)), dim3(kThreads),
-                               sizeof(Tile<LP>), q, f);
+                e = launch_pdl(k, dim3((unsigned)((long long)f.in.groups * f.cut.slots)),
+                               dim3(kFwdThreads), sizeof(typename Lanes<T, LP>::Shared), q, f);
                 prof_after(q);
                 return e;
             });
@@ -876,8 +1052,8 @@ cudaError_t launch_join(const JoinArgs &j, cudaStream_t q) {
 
 template <typename T>
 cudaError_t launch_bwd(BwdArgs b, cudaStream_t q) {
-    cudaError_t e = by_lanes(lanes_of(b.in.S), [&](auto lp) {
-        return by_alignment(b.in.D, [&](auto vect) {
+    cudaError_t e = by_lanes<16>(lanes_of(b.in.S, 4), [&](auto lp) {
+        return by_alignment(b.in.D % 8 == 0, [&](auto vect) {
             constexpr int LP = decltype(lp)::value;
             using G = Segment<LP>;
             auto k = bwd_kernel<T, LP, decltype(vect)::value>;
@@ -1037,7 +1213,7 @@ gdn_status gdn_ssm_step(const gdn_ssm_step_args *a, void *stream) {
     prof_before("ssm_step", q);
     const cudaError_t e = ssm::by_type(a->dtype, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        return ssm::by_lanes(ssm::lanes_of(a->S), [&](auto lp) {
+        return ssm::by_lanes<16>(ssm::lanes_of(a->S, 4), [&](auto lp) {
             constexpr int LP = decltype(lp)::value, rows = ssm::kThreads / LP;
             const long long ctas = ((long long)a->N * a->D + rows - 1) / rows;
             return launch_pdl(ssm::step_kernel<T, LP>, dim3((unsigned)std::min<long long>(ctas, 16ll * dev.sms)),

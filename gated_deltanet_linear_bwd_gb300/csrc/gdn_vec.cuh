@@ -62,6 +62,13 @@ __device__ __forceinline__ float logistic(float x) {
     if (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
     return rcp(1.f + ex2(x * -1.4426950408889634f));
 }
+template <typename T>
+__device__ __forceinline__ float2 logistic2(float2 x) {
+    if (sizeof(T) == 4) return make_float2(logistic<T>(x.x), logistic<T>(x.y));
+    const float2 y = __fmul2_rn(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 e = __fadd2_rn(make_float2(ex2(y.x), ex2(y.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp(e.x), rcp(e.y));
+}
 // d(x logistic(x)) / dx, s = logistic(x).
 __device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f + x * (1.f - s)); }
 
@@ -69,13 +76,22 @@ __device__ __forceinline__ float silu_slope(float x, float s) { return s * (1.f 
 // 1/8, where the logarithm of the rounded 1 + e would lose what a small step is made of: there e p(e),
 // p the polynomial through log2(1 + e) / e at the four Chebyshev points of 0 .. 1/8 (3.1e-7 of itself).
 template <typename T>
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    if (sizeof(T) == 4)
+        return make_float2(fmaxf(x.x, 0.f) + log1pf(expf(-fabsf(x.x))), fmaxf(x.y, 0.f) + log1pf(expf(-fabsf(x.y))));
+    const auto both = [](float v) { return make_float2(v, v); };
+    const float2 y = __fmul2_rn(make_float2(fabsf(x.x), fabsf(x.y)), both(-1.4426950408889634f));
+    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+    float2 p = __ffma2_rn(e, both(-2.9770274392e-1f), both(4.7618794121e-1f));
+    p = __ffma2_rn(p, e, both(-7.2123178461e-1f));
+    p = __fmul2_rn(__ffma2_rn(p, e, both(1.4426945903f)), e);
+    const float2 u = __fadd2_rn(e, both(1.f));
+    return __ffma2_rn(make_float2(e.x < 0.125f ? p.x : __log2f(u.x), e.y < 0.125f ? p.y : __log2f(u.y)),
+                      both(0.6931471805599453f), make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+template <typename T>
 __device__ __forceinline__ float softplus(float x) {
-    if (sizeof(T) == 4) return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-    const float e = ex2(-fabsf(x) * 1.4426950408889634f);
-    float p = fmaf(e, -2.9770274392e-1f, 4.7618794121e-1f);
-    p = fmaf(p, e, -7.2123178461e-1f);
-    p = fmaf(p, e, 1.4426945903f) * e;
-    return fmaf(e < 0.125f ? p : __log2f(1.f + e), 0.6931471805599453f, fmaxf(x, 0.f));
+    return softplus2<T>(make_float2(x, x)).x;
 }
 
 // Sequences: rows of T tokens, or (cu) a packed batch of T tokens in all.
