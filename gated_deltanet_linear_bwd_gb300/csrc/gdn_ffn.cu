@@ -371,6 +371,254 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward product launch");
 }
 
+// ------------------------------------------------------------------ few tokens
+// One CTA makes 128 rows of a weight (or 64 rows of w_gate and 64 of w_up) x `nt` tokens: the weight is
+// the MMA's 128-row operand, so that few tokens cost a narrow MMA and not idle rows.  Where tiles are
+// too few for the GPU the CTAs of a cluster share the contraction: each leaves its fp32 tile in its
+// shared memory, and each adds up its share of the tokens, in rank order.  Bound by the weights' bytes.
+constexpr int kFewThreads = 192;                     // loads, MMA, four epilogue warps
+constexpr int kFewStages = 10, kMaxSplits = 8;
+constexpr int kTmemBarrier = 1;                      // named: TMEM is there, and waits with a limit may begin
+
+struct FewArgs {
+    __nv_bfloat16 *c, *gate, *up;                    // gate, up: kGated, null = not stored
+    int tokens, cols;                                // of C (kGated: features)
+    int nt, token_tiles, kblocks, stages, stage_bytes, tmem_cols;
+    int early_w;                                     // the kernel ahead began when all before it had ended, the weight's
+                                                     // writers among them
+    int gelu;
+    int *status;
+    long long spin_limit;
+};
+struct FewControl {
+    uint64_t full[kFewStages], empty[kFewStages], done;
+    uint32_t tmem;
+    int failed, issued;
+};
+struct FewMaps {
+    CUtensorMap x, w[2];
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+    extern __shared__ uint8_t raw[];
+    __shared__ FewControl ctl;
+    uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    constexpr int kRows = GATED ? 64 : 128;          // columns of C of a tile
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_rank(), splits = (int)tc::cluster_size();
+    const int tile = blockIdx.x / splits;
+    const int f0 = tile / a.token_tiles * kRows, t0 = tile % a.token_tiles * a.nt;
+    const int kb0 = (int)((long long)a.kblocks * rank / splits);
+    const int kb1 = (int)((long long)a.kblocks * (rank + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            tc::mbar_init(&ctl.full[s], 1);
+            tc::mbar_init(&ctl.empty[s], 1);
+        }
+        tc::mbar_init(&ctl.done, 1);
+        ctl.failed = 0;
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
+
+    if (warp == 0) {
+        const int n = kb1 - kb0;
+        const uint32_t ring0 = tc::smem_u32(ring), full0 = tc::smem_u32(ctl.full), empty0 = tc::smem_u32(ctl.empty);
+        auto load_w = [&](int kb, uint32_t st, uint32_t bar) {       // arms the stage for all it gets
+            tc::expect_bytes(bar, (uint32_t)a.stage_bytes, true);
+            if (GATED) {
+                tc::load_box<false>(st, &maps.w[0], kb * 64, f0, bar);
+                tc::load_box<false>(st + 8192, &maps.w[1], kb * 64, f0, bar);
+            } else {
+                tc::load_box<false>(st, &maps.w[0], kb * 64, f0, bar);
+            }
+        };
+        // a ring's worth of weights may come before the kernel ahead has written the tokens
+        const int ahead = a.early_w ? min(n, a.stages) : 0;
+        for (int i = 0; i < ahead; ++i) load_w(kb0 + i, ring0 + i * a.stage_bytes, full0 + 8 * i);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // all before this kernel has ended
+        int i = 0, s = 0;
+        uint32_t parity = 1;                         // of the stage's last release; the first round has none
+        auto fill = [&] {
+            const uint32_t st = ring0 + s * a.stage_bytes, bar = full0 + 8 * s;
+            if (i >= ahead) load_w(kb0 + i, st, bar);
+            tc::load_box<false>(st + 16384, &maps.x, (kb0 + i) * 64, t0, bar);
+            if (++s == a.stages) s = 0, parity ^= 1;
+        };
+        for (; i < min(n, a.stages); ++i) fill();
+        tc::named_sync(kTmemBarrier, kFewThreads);
+        for (; i < n; ++i) {
+            if (!tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status)) {
+                ctl.failed = 1;
+                break;
+            }
+            fill();
+        }
+        if (lane == 0) ctl.issued = i;
+    } else if (warp == 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");           // the kernel ahead may hold TMEM
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        tc::tmem_alloc(&ctl.tmem, (uint32_t)a.tmem_cols);
+        tc::tmem_relinquish();
+        tc::tc_fence_before();
+        tc::named_sync(kTmemBarrier, kFewThreads);
+        tc::tc_fence_after();
+        const uint32_t tmem = ctl.tmem, idesc = tc::idesc_bf16(128, a.nt, false, false);
+        int s = 0;
+        uint32_t parity = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!tc::mbar_spin(tc::smem_u32(&ctl.full[s]), parity, a.spin_limit, a.status)) {
+                ctl.failed = 1;
+                break;
+            }
+            const uint32_t st = tc::smem_u32(ring + s * a.stage_bytes);
+            tc::mma_bf16_stage<false, false, false>(tmem, tc::desc_tile<false>(st), tc::desc_tile<false>(st + 16384), idesc,
+                                                    kb > kb0, &ctl.empty[s]);
+            if (++s == a.stages) s = 0, parity ^= 1;
+        }
+        tc::mma_commit(&ctl.done);
+    }
+    if (warp > 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");              // C may be written
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        tc::named_sync(kTmemBarrier, kFewThreads);
+    }
+    __syncwarp();
+    // every MMA done: the ring is free and the tile is whole
+    if (!tc::mbar_wait(&ctl.done, 0, a.spin_limit, a.status)) {
+        ctl.failed = 1;
+        tc::mbar_drain(&ctl.done, 0);
+    }
+    tc::tc_fence_after();
+    __syncthreads();
+    const uint32_t tmem = ctl.tmem;
+    const bool ok = ctl.failed == 0;
+    if (!ok && threadIdx.x == 0)   // a wait gave up: nothing may land after the CTA has gone
+        for (int j = max(0, ctl.issued - a.stages); j < ctl.issued; ++j)
+            tc::mbar_drain(&ctl.full[j % a.stages], (j / a.stages) & 1);
+    float *out = reinterpret_cast<float *>(ring);    // [nt][128]
+    if (ok && warp >= 2) {
+        float *to = out + 32 * (warp & 3) + lane;
+        for (int c = 0; c < a.nt; c += 16) {
+            float v[16];
+            tc::tmem_ld8x2(tc::tmem_addr(tmem, warp, c), tc::tmem_addr(tmem, warp, c + 8), v, v + 8);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) to[(c + j) * 128] = v[j];
+        }
+    }
+    tc::tc_fence_before();
+    if (splits > 1) tc::cluster_sync();
+    else __syncthreads();
+    tc::tc_fence_after();
+    if (ok) {
+        const uint32_t base = tc::smem_u32(out);
+        const int step = splits * (kFewThreads / 32), rows = min(a.nt, a.tokens - t0);
+        for (int j = rank * (kFewThreads / 32) + warp; j < rows; j += step) {
+            const int at = j * 128 + 4 * lane;
+            float4 v;
+            if (splits == 1) {
+                v = *reinterpret_cast<const float4 *>(out + at);
+            } else {
+                float4 p[kMaxSplits];
+#pragma unroll
+                for (int r = 0; r < kMaxSplits; ++r)
+                    if (r < splits) p[r] = tc::ld_cluster4(tc::map_rank(base + 4u * (uint32_t)at, r));
+                v = p[0];
+#pragma unroll
+                for (int r = 1; r < kMaxSplits; ++r)
+                    if (r < splits) v.x += p[r].x, v.y += p[r].y, v.z += p[r].z, v.w += p[r].w;
+            }
+            float x[4] = {v.x, v.y, v.z, v.w};
+            const long long row = (long long)(t0 + j) * a.cols;
+            if (!GATED) {
+                if (f0 + 4 * lane < a.cols) tc::st4(a.c + row + f0 + 4 * lane, x);
+                continue;
+            }
+            // lanes 0 - 15 have the gate of 64 features, 16 - 31 their up
+            const int f = f0 + 4 * (lane & 15);
+            const bool in = f < a.cols;
+            __nv_bfloat16 *kept = lane < 16 ? a.gate : a.up;
+            if (kept && in) tc::st4(kept + row + f, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = __shfl_down_sync(0xffffffffu, x[i], 16);
+                x[i] = u * (a.gelu ? activation<true>(x[i]) : activation<false>(x[i]));
+            }
+            if (lane < 16 && in) tc::st4(a.c + row + f, x);
+        }
+    }
+    if (splits > 1) tc::cluster_sync();              // the others have read this CTA's tile
+    if (warp == 1) tc::tmem_dealloc(tmem, (uint32_t)a.tmem_cols);
+}
+
+// Tokens of a tile: 16, or as many as there are up to 128.
+int token_tile(int tokens) {
+    int nt = 16;
+    while (nt < 128 && nt < tokens) nt *= 2;
+    return nt;
+}
+
+// Single CTAs for up to 128 tokens, and while their tiles are no more than a wave.
+bool few_fits(const Product &p, int sms) {
+    const int nt = token_tile((int)std::min<long long>(p.m, 128));
+    return p.m <= 128 || (p.n + 127) / 128 * ((p.m + nt - 1) / nt) <= sms;
+}
+
+template <bool GATED>
+gdn_status run_few(const char *name, const Product &p, int gelu, bool early_w, const LayerDevice &dev, cudaStream_t q) {
+    FewMaps maps = {};
+    FewArgs g{};
+    g.c = (__nv_bfloat16 *)p.c[0];
+    if (GATED) g.gate = (__nv_bfloat16 *)p.c[1], g.up = (__nv_bfloat16 *)p.c[2];
+    g.tokens = (int)p.m;
+    g.cols = (int)p.n;
+    g.nt = token_tile((int)std::min<long long>(p.m, 128));
+    g.token_tiles = (int)((p.m + g.nt - 1) / g.nt);
+    g.kblocks = (int)((p.k + 63) / 64);
+    g.stage_bytes = 16384 + g.nt * 128;
+    g.early_w = early_w;
+    g.gelu = gelu;
+    g.status = dev.status;
+    g.spin_limit = dev.spin_limit;
+    // The CTAs of a cluster share the contraction, by powers of two, while slots of the GPU are empty:
+    // two CTAs to an SM and up to 8 to a cluster for few tokens; one and up to 4 for many, whose tiles
+    // take long to add up.  Clusters of c leave about c SMs without one.
+    const int rows = GATED ? 64 : 128;
+    const long long tiles = (p.n + rows - 1) / rows * g.token_tiles;
+    const bool few = g.nt <= 32;
+    int splits = 1;
+    while (splits < (few ? kMaxSplits : 4) && 2 * splits <= g.kblocks &&
+           2 * splits * tiles <= (few ? 2 : 1) * (dev.sms - 2 * splits))
+        splits *= 2;
+    const int per = (g.kblocks + splits - 1) / splits;
+    g.stages = std::max(1, std::min({kFewStages, per, (tiles * splits <= dev.sms - splits ? 200 : 100) * 1024 / g.stage_bytes}));
+    g.tmem_cols = 32;
+    while (g.tmem_cols < g.nt) g.tmem_cols *= 2;
+    cudaError_t e = tc::encoder();
+    const auto map = [&](CUtensorMap *m, const void *base, long long r, int box) {
+        if (e == cudaSuccess) e = tc::make_map_rows(m, base, r, p.k, 2, 64, box, true);
+    };
+    map(&maps.x, p.a, p.m, g.nt);
+    map(&maps.w[0], p.b, p.n, rows);
+    if (GATED) map(&maps.w[1], p.b2, p.n, rows);
+    if (e != cudaSuccess) return cuda_fail(e, "tensor map of a product");
+    size_t smem = std::max(g.stages * g.stage_bytes, g.nt * 128 * 4) + 1024;
+    // a cluster's CTAs hold their TMEM until all have theirs: shared memory in proportion, as the MX products
+    if (splits > 1) smem = std::max(smem, (size_t)g.tmem_cols * 432 - 1024);
+    auto k = few_kernel<GATED>;
+    if ((e = allow_smem((const void *)k, smem)) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
+    const long long ctas = tiles * splits;
+    if (ctas >= (1ll << 31)) return fail(GDN_ERR_INVALID_ARG, "problem too large");
+    prof_before(name, q);
+    e = launch_pdl_cluster(k, dim3((unsigned)ctas), dim3(kFewThreads), smem, splits, q, maps, g);
+    prof_after(q);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward product launch");
+}
+
 gdn_status check(int M, int K, int F, int dtype, int activation) {
     if (M < 0 || K < 1 || F < 1) return fail(GDN_ERR_INVALID_ARG, "bad sizes M=%d K=%d F=%d", M, K, F);
     if (std::max({M, K, F}) > kMaxExtent) return fail(GDN_ERR_INVALID_ARG, "problem too large: M=%d K=%d F=%d", M, K, F);
@@ -421,8 +669,12 @@ gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *a, void *ws, size_t ws_bytes, voi
     g.gelu = a->activation == GDN_ACT_GELU;
     const ffn::Product up{a->x, a->w_gate, a->w_up, nullptr, {ws, a->gate, a->up}, a->M, a->F, a->K};
     const ffn::Product down{ws, a->w_down, nullptr, nullptr, {a->y}, a->M, a->K, a->F};
-    st = ffn::run_pair<ffn::kGated>("ffn_gated", &up, 1, g, dev, q);
-    return st == GDN_OK ? ffn::run_pair<ffn::kDown>("ffn_down", &down, 1, g, dev, q) : st;
+    const bool few = ffn::few_fits(up, dev.sms);
+    st = few ? ffn::run_few<true>("ffn_gated_few", up, g.gelu, false, dev, q)
+             : ffn::run_pair<ffn::kGated>("ffn_gated", &up, 1, g, dev, q);
+    if (st != GDN_OK) return st;
+    return ffn::few_fits(down, dev.sms) ? ffn::run_few<false>("ffn_down_few", down, 0, few, dev, q)
+                                        : ffn::run_pair<ffn::kDown>("ffn_down", &down, 1, g, dev, q);
 }
 
 size_t gdn_ffn_bwd_workspace_size(const gdn_ffn_bwd_args *a) {

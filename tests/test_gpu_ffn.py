@@ -84,7 +84,9 @@ def check_backward(p, name, out):
 
 CASES = [(1, 8, 8, "silu"), (3, 64, 128, "gelu"), (7, 72, 136, "silu"), (16, 512, 264, "silu"), (33, 200, 520, "gelu"),
          (128, 128, 256, "silu"), (129, 264, 64, "gelu"), (257, 72, 392, "silu"), (300, 520, 1000, "silu"),
-         (700, 256, 2048, "gelu"), (1, 1024, 4096, "silu"), (2500, 64, 72, "silu")]
+         (700, 256, 2048, "gelu"), (1, 1024, 4096, "silu"), (2500, 64, 72, "silu"),
+         # wide enough for pairs of CTAs, into the block and out of it
+         (2600, 72, 2000, "gelu"), (1300, 1928, 72, "silu")]
 
 
 @pytest.mark.parametrize("M,K,F,name", CASES)
