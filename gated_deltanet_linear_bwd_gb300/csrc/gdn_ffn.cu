@@ -54,26 +54,29 @@ constexpr bool a_mn(int mode) { return mode == kWeights; }
 constexpr bool b_mn(int mode) { return mode >= kSlopes; }
 
 constexpr int kPairThreads = 224;                    // B, MMA, four epilogue warps, A
-constexpr int kStages = 6, kStage = 32768;
+constexpr int kStage = 32768;
 constexpr int kBlock = 4096;                         // a warp's staged 32 rows x 128 bytes
+constexpr int kMaxStages = 6;
+constexpr int stages(int mode) { return mode == kSlopes ? 5 : 6; }
+constexpr int blocks(int mode) { return mode == kSlopes ? 3 : 2; }    // of a warp
 constexpr int kProducts = 3;
 
 struct Maps {
-    CUtensorMap a[kProducts], b[kProducts], c[kProducts];
+    CUtensorMap a[kProducts], b[kProducts], c[kProducts];    // kSlopes: a[1] gate, a[2] up
 };
 struct PairArgs {
     int rows, m_tiles[kProducts], n_tiles[kProducts], first[kProducts + 1];   // tiles of the products
     int cols[kProducts];                             // of C (kGated: features)
     int kblocks, parts;                              // blocks of 64 of a part of the contraction; kInput has two
     int c_rows[kProducts];
-    const __nv_bfloat16 *gate, *up;                  // kSlopes
     int save;                                        // kGated: gate and up are stored too
     int gelu;
     int *status;
     long long spin_limit;
 };
 struct Control {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_free[2], done;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_free[2], done;
+    uint64_t in[4];                                  // kSlopes: a warp's blocks of gate and up are there
     uint32_t tmem;
     int issued;
 };
@@ -116,9 +119,10 @@ template <int MODE>
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ Maps maps,
                                                             const __grid_constant__ PairArgs a) {
     constexpr bool A_MN = a_mn(MODE), B_MN = b_mn(MODE);
+    constexpr int kStages = stages(MODE);
     extern __shared__ __align__(1024) uint8_t ring[];
     uint8_t *stage_out = ring + kStages * kStage;
-    Control &ctl = *reinterpret_cast<Control *>(stage_out + 8 * kBlock);
+    Control &ctl = *reinterpret_cast<Control *>(stage_out + 4 * blocks(MODE) * kBlock);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank();
@@ -138,6 +142,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
             tc::mbar_init(&ctl.acc_full[i], 1);
             tc::mbar_init(&ctl.acc_free[i], 8);      // the epilogue warps of both CTAs
         }
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&ctl.in[i], 1);
         tc::mbar_init(&ctl.done, 1);
         ctl.issued = 0;
         tc::fence_barrier_init();
@@ -209,8 +214,23 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     } else {
         // epilogue: each warp takes its 32 rows, 64 columns at a time
         const int quarter = warp & 3;
-        Stager out{stage_out + quarter * 2 * kBlock, 0};
+        Stager out{stage_out + quarter * blocks(MODE) * kBlock, 0};
         const uint32_t free0 = tc::map_rank(tc::smem_u32(&ctl.acc_free[0]), 0);
+        // kSlopes: the next block's gate and up, by TMA, under the products and the stores before it;
+        // dg and du take their places, h a third block
+        uint8_t *const gate = out.base, *const up = gate + kBlock, *const hidden = up + kBlock;
+        int asked = 0, had = 0;
+        const auto ask = [&](int tile, int c) {
+            const int3 at = tile_at(a, tile);
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&ctl.in[quarter], 2 * kBlock);
+                const int row = at.y * 256 + rank * 128 + 32 * quarter, col = at.z * 256 + c;
+                tc::tma_load_2d(gate, &maps.a[1], &ctl.in[quarter], col, row);
+                tc::tma_load_2d(up, &maps.a[2], &ctl.in[quarter], col, row);
+            }
+            ++asked;
+        };
+        if (MODE == kSlopes && pair < tiles) ask(pair, 0);
         int t = 0;
         for (int tile = pair; tile < tiles; tile += pairs, ++t) {
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&ctl.acc_full[t & 1], (t >> 1) & 1, a.spin_limit, a.status))) break;
@@ -241,41 +261,62 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                     out.send(&maps.c[0], block, col, row, in, lane);
                 }
             } else if constexpr (MODE == kSlopes) {
-                const long long base = (long long)(row + lane) * cols;
+                bool there = true;
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 64) {
                     const int col = at.z * 256 + c;
                     const bool in = row < rows && col < cols;
-                    // the three results, a block each: dg, du, then h from gate and up once more
-#pragma unroll 1
-                    for (int what = 0; what < 3; ++what) {
-                        uint8_t *block = out.next(lane);
+                    there = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.in[quarter], had & 1, a.spin_limit, a.status));
+                    if (!there) break;
+                    ++had;
 #pragma unroll
-                        for (int b = 0; b < 64; b += 32) {
-                            float v[32];
-                            tc::tmem_ld32(tc::tmem_addr(acc, quarter, c + b), v);
+                    for (int b = 0; b < 64; b += 32) {
+                        float v[32];
+                        tc::tmem_ld32(tc::tmem_addr(acc, quarter, c + b), v);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                uint4 gr = make_uint4(0, 0, 0, 0), ur = gr;
-                                if (row + lane < rows && col + b + i < cols) {
-                                    gr = __ldg(reinterpret_cast<const uint4 *>(a.gate + base + col + b + i));
-                                    ur = __ldg(reinterpret_cast<const uint4 *>(a.up + base + col + b + i));
-                                }
-                                const __nv_bfloat16 *gs = reinterpret_cast<const __nv_bfloat16 *>(&gr);
-                                const __nv_bfloat16 *us = reinterpret_cast<const __nv_bfloat16 *>(&ur);
+                        for (int i = 0; i < 32; i += 8) {
+                            const uint32_t off = tc::sw128_off(lane, b + i);
+                            uint4 *pg = reinterpret_cast<uint4 *>(gate + off), *pu = reinterpret_cast<uint4 *>(up + off);
+                            const uint4 gr = *pg, ur = *pu;
+                            const __nv_bfloat16 *gs = reinterpret_cast<const __nv_bfloat16 *>(&gr);
+                            const __nv_bfloat16 *us = reinterpret_cast<const __nv_bfloat16 *>(&ur);
+                            float dg[8], du[8], h[8];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const float g = to_f(gs[j]), u = to_f(us[j]);
-                                    float slope;
-                                    const float f = a.gelu ? activation<true>(g, slope) : activation<false>(g, slope);
-                                    v[i + j] = what == 0 ? v[i + j] * u * slope : what == 1 ? v[i + j] * f : f * u;
-                                }
+                            for (int j = 0; j < 8; ++j) {
+                                const float g = to_f(gs[j]), u = to_f(us[j]);
+                                float slope;
+                                const float f = a.gelu ? activation<true>(g, slope) : activation<false>(g, slope);
+                                dg[j] = v[i + j] * u * slope;
+                                du[j] = v[i + j] * f;
+                                h[j] = f * u;
                             }
-                            tc::st_row32(block, lane, b, v);
+                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pg), dg);
+                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pu), du);
+                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(hidden + off), h);
                         }
-                        out.send(&maps.c[what], block, col, row, in, lane);
                     }
+                    if (c == 192) {                  // the accumulator is free
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cluster(free0 + 8 * (t & 1));
+                    }
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (in) {
+                            tc::tma_store_2d(&maps.c[0], gate, col, row);
+                            tc::tma_store_2d(&maps.c[1], up, col, row);
+                            tc::tma_store_2d(&maps.c[2], hidden, col, row);
+                        }
+                        tc::bulk_commit();
+                        tc::bulk_wait_read();
+                    }
+                    __syncwarp();
+                    if (c < 192) ask(tile, c + 64);
+                    else if (tile + pairs < tiles) ask(tile + pairs, 0);
                 }
+                if (!there) break;
+                continue;
             } else {
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 64) {
@@ -292,6 +333,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
             if (lane == 0) tc::mbar_arrive_cluster(free0 + 8 * (t & 1));
         }
         if (lane == 0) tc::bulk_wait_read();
+        if (had < asked) tc::mbar_drain(&ctl.in[quarter], had & 1);
         __syncwarp();
     }
     // every MMA done and every copy landed before TMEM is given back and a CTA goes
@@ -306,23 +348,25 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
-constexpr size_t kPairSmem = kStages * kStage + 8 * kBlock + sizeof(Control);
-static_assert(kPairSmem <= 227 * 1024, "");
-// as much shared memory for its TMEM columns as clusters take (the MX products' rule)
-static_assert(kPairSmem >= 512 * 432 - 1024, "");
+// As much shared memory for its TMEM columns as clusters take (the MX products' rule), and no more than
+// there is.
+constexpr size_t pair_smem(int mode) {
+    return std::max<size_t>(stages(mode) * kStage + 4 * blocks(mode) * kBlock + sizeof(Control), 512 * 432 - 1024);
+}
+static_assert(pair_smem(kGated) <= 227 * 1024 && pair_smem(kSlopes) <= 227 * 1024, "");
 
 // A matrix [rows, cols] as an operand (64-element boxes: 128 rows of it, or 64 of the contraction) or
 // as a result (32 rows).
 cudaError_t operand(CUtensorMap *m, const void *base, long long rows, long long cols, bool mn) {
     return tc::make_map_rows(m, base, rows, cols, 2, 64, mn ? 64 : 128, true);
 }
-cudaError_t result(CUtensorMap *m, void *base, long long rows, long long cols) {
+cudaError_t result(CUtensorMap *m, const void *base, long long rows, long long cols) {
     return tc::make_map_rows(m, base, rows, cols, 2, 64, 32, true);
 }
 
 // One launch of up to three products.
 struct Product {
-    const void *a, *b, *b2;      // b2: kGated w_up; kInput: a2 and b2 are the second part
+    const void *a, *b, *b2;      // b2: kGated w_up; kInput: a2 and b2 are the second part; kSlopes: gate and up
     const void *a2;
     void *c[kProducts];          // kGated and kSlopes have three results, the others one
     long long m, n, k;           // C [m, n], contraction k
@@ -347,6 +391,8 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
         op_a(&maps.a[i], p[i].a);
         op_b(&maps.b[i], p[i].b);
         if (MODE == kInput) op_a(&maps.a[1], p[i].a2);
+        if (MODE == kSlopes && e == cudaSuccess) e = result(&maps.a[1], p[i].a2, p[i].m, p[i].n);
+        if (MODE == kSlopes && e == cudaSuccess) e = result(&maps.a[2], p[i].b2, p[i].m, p[i].n);
         if (MODE == kInput || MODE == kGated) op_b(&maps.b[1], p[i].b2);
         for (int j = 0; j < (MODE == kGated || MODE == kSlopes ? kProducts : 1); ++j)
             if (p[i].c[j] && e == cudaSuccess) e = result(&maps.c[i + j], p[i].c[j], p[i].m, p[i].n);
@@ -363,10 +409,10 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
     g.status = dev.status;
     g.spin_limit = dev.spin_limit;
     auto k = pair_kernel<MODE>;
-    if ((e = allow_smem((const void *)k, kPairSmem)) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
+    if ((e = allow_smem((const void *)k, pair_smem(MODE))) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
     const int pairs = (int)std::min<long long>(tiles, dev.sms / 2);
     prof_before(name, q);
-    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, 2, q, maps, g);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), pair_smem(MODE), 2, q, maps, g);
     prof_after(q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward product launch");
 }
@@ -713,9 +759,7 @@ gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *a, void *ws, size_t ws_bytes, voi
     uint8_t *dg = (uint8_t *)ws, *du = dg + ffn::hidden_bytes(a->M, a->F), *h = du + ffn::hidden_bytes(a->M, a->F);
     ffn::PairArgs g{};
     g.gelu = a->activation == GDN_ACT_GELU;
-    g.gate = (const __nv_bfloat16 *)a->gate;
-    g.up = (const __nv_bfloat16 *)a->up;
-    const ffn::Product dh{a->d_y, a->w_down, nullptr, nullptr, {dg, du, h}, a->M, a->F, a->K};
+    const ffn::Product dh{a->d_y, a->w_down, a->up, a->gate, {dg, du, h}, a->M, a->F, a->K};
     const ffn::Product dx{dg, a->w_gate, a->w_up, du, {a->dx}, a->M, a->K, a->F};
     const ffn::Product dw[3] = {{dg, a->x, nullptr, nullptr, {a->dw_gate}, a->F, a->K, a->M},
                                 {du, a->x, nullptr, nullptr, {a->dw_up}, a->F, a->K, a->M},
