@@ -42,7 +42,9 @@ __device__ __forceinline__ float activation(float g, float &slope) {
 // ------------------------------------------------------------------ CTA pairs
 // Tiles of 256 x 256 by two CTAs (cta_group::2), persistent over the tiles of up to three products;
 // each CTA holds 128 rows of A and half the columns' rows of B.  Two accumulators of 256 columns fill
-// TMEM, so that a tile's epilogue runs under the next tile's MMAs.
+// TMEM, so that a tile's epilogue runs under the next tile's MMAs.  A stage's MMAs take 512 cycles at the
+// least, and its 32 KB into either SM as long.  8192 x 4096 x 12288: into the block 843 us (1.96 PFLOP/s, 104% of
+// the measured burst rate), out of it 432, backward dh 534, dx 874, the weights' gradients 1300.
 enum Mode {
     kGated,      // A x, B gate's rows in the one CTA and up's in the other: a tile is 256 tokens x 128 features
     kDown,       // A h, B w_down
@@ -54,10 +56,10 @@ constexpr bool a_mn(int mode) { return mode == kWeights; }
 constexpr bool b_mn(int mode) { return mode >= kSlopes; }
 
 constexpr int kPairThreads = 224;                    // B, MMA, four epilogue warps, A
-constexpr int kStage = 32768;
 constexpr int kBlock = 4096;                         // a warp's staged 32 rows x 128 bytes
-constexpr int kMaxStages = 6;
-constexpr int stages(int mode) { return mode == kSlopes ? 5 : 6; }
+constexpr int kMaxStages = 8;
+constexpr int stages(int mode, int tn) { return mode == kSlopes ? 5 : tn == 128 ? 8 : 6; }
+constexpr int stage_bytes(int tn) { return 16384 + tn / 2 * 128; }
 constexpr int blocks(int mode) { return mode == kSlopes ? 3 : 2; }    // of a warp
 constexpr int kProducts = 3;
 
@@ -115,11 +117,11 @@ struct Stager {
     }
 };
 
-template <int MODE>
+template <int MODE, int TN>
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ Maps maps,
                                                             const __grid_constant__ PairArgs a) {
     constexpr bool A_MN = a_mn(MODE), B_MN = b_mn(MODE);
-    constexpr int kStages = stages(MODE);
+    constexpr int kStages = stages(MODE, TN), kStage = stage_bytes(TN);
     extern __shared__ __align__(1024) uint8_t ring[];
     uint8_t *stage_out = ring + kStages * kStage;
     Control &ctl = *reinterpret_cast<Control *>(stage_out + 4 * blocks(MODE) * kBlock);
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
         for (int tile = pair; tile < tiles && ok; tile += pairs) {
             const int3 at = tile_at(a, tile);
             const int row = at.y * 256 + rank * 128;
-            const int col = MODE == kGated ? at.z * 128 : at.z * 256 + rank * 128;
+            const int col = MODE == kGated ? at.z * 128 : at.z * TN + rank * (TN / 2);
             for (int kb = 0; kb < kblocks; ++kb, ++i) {
                 if (i >= kStages) {
                     ok = tc::mbar_spin(empty0 + 8 * s, parity, a.spin_limit, a.status);
@@ -179,9 +181,9 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                 if (is_b) {                          // and arms the pair's barrier for all that both CTAs get
                     tc::expect_bytes(full0 + 8 * s, 2u * kStage, rank == 0);
                     const int b = MODE == kGated ? rank : MODE == kInput ? part : at.x;
-                    tc::load_tile<B_MN, true>(st + 16384, &maps.b[b], col, k, bar);
+                    tc::load_tile<B_MN, true, TN / 2>(st + 16384, &maps.b[b], col, k, bar);
                 } else {
-                    tc::load_tile<A_MN, true>(st, &maps.a[MODE == kInput ? part : at.x], row, k, bar);
+                    tc::load_tile<A_MN, true, 128>(st, &maps.a[MODE == kInput ? part : at.x], row, k, bar);
                 }
                 if (++s == kStages) s = 0, parity ^= 1;
             }
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                     if (!ok) break;
                     const uint32_t st = ring0 + s * kStage;
                     tc::mma_bf16_stage<A_MN, B_MN, true>(acc, tc::desc_tile<A_MN>(st), tc::desc_tile<B_MN>(st + 16384),
-                                                         tc::idesc_bf16(256, 256, A_MN, B_MN), kb > 0, &ctl.empty[s]);
+                                                         tc::idesc_bf16(256, TN, A_MN, B_MN), kb > 0, &ctl.empty[s]);
                     if (++s == kStages) s = 0, parity ^= 1;
                 }
                 if (ok) tc::mma_commit_pair(&ctl.acc_full[t & 1]);
@@ -319,8 +321,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                 continue;
             } else {
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 64) {
-                    const int col = at.z * 256 + c;
+                for (int c = 0; c < TN; c += 64) {
+                    const int col = at.z * TN + c;
                     float v[64];
                     tc::tmem_ld32x2(tc::tmem_addr(acc, quarter, c), tc::tmem_addr(acc, quarter, c + 32), v, v + 32);
                     uint8_t *block = out.next(lane);
@@ -350,15 +352,15 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
 
 // As much shared memory for its TMEM columns as clusters take (the MX products' rule), and no more than
 // there is.
-constexpr size_t pair_smem(int mode) {
-    return std::max<size_t>(stages(mode) * kStage + 4 * blocks(mode) * kBlock + sizeof(Control), 512 * 432 - 1024);
+constexpr size_t pair_smem(int mode, int tn) {
+    return std::max<size_t>(stages(mode, tn) * stage_bytes(tn) + 4 * blocks(mode) * kBlock + sizeof(Control), 512 * 432 - 1024);
 }
-static_assert(pair_smem(kGated) <= 227 * 1024 && pair_smem(kSlopes) <= 227 * 1024, "");
+static_assert(pair_smem(kGated, 256) <= 227 * 1024 && pair_smem(kSlopes, 256) <= 227 * 1024 && pair_smem(kDown, 128) <= 227 * 1024, "");
 
-// A matrix [rows, cols] as an operand (64-element boxes: 128 rows of it, or 64 of the contraction) or
+// A matrix [rows, cols] as an operand (64-element boxes: `box` rows of it, or 64 of the contraction) or
 // as a result (32 rows).
-cudaError_t operand(CUtensorMap *m, const void *base, long long rows, long long cols, bool mn) {
-    return tc::make_map_rows(m, base, rows, cols, 2, 64, mn ? 64 : 128, true);
+cudaError_t operand(CUtensorMap *m, const void *base, long long rows, long long cols, bool mn, int box) {
+    return tc::make_map_rows(m, base, rows, cols, 2, 64, mn ? 64 : box, true);
 }
 cudaError_t result(CUtensorMap *m, const void *base, long long rows, long long cols) {
     return tc::make_map_rows(m, base, rows, cols, 2, 64, 32, true);
@@ -371,7 +373,7 @@ struct Product {
     void *c[kProducts];          // kGated and kSlopes have three results, the others one
     long long m, n, k;           // C [m, n], contraction k
 };
-template <int MODE>
+template <int MODE, int TN = 256>
 gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, const LayerDevice &dev, cudaStream_t q) {
     Maps maps = {};
     cudaError_t e = tc::encoder();
@@ -383,10 +385,10 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
         if (i >= count) continue;
         const bool amn = a_mn(MODE), bmn = b_mn(MODE);
         const auto op_a = [&](CUtensorMap *m, const void *base) {
-            if (e == cudaSuccess) e = operand(m, base, amn ? p[i].k : p[i].m, amn ? p[i].m : p[i].k, amn);
+            if (e == cudaSuccess) e = operand(m, base, amn ? p[i].k : p[i].m, amn ? p[i].m : p[i].k, amn, 128);
         };
         const auto op_b = [&](CUtensorMap *m, const void *base) {
-            if (e == cudaSuccess) e = operand(m, base, bmn ? p[i].k : p[i].n, bmn ? p[i].n : p[i].k, bmn);
+            if (e == cudaSuccess) e = operand(m, base, bmn ? p[i].k : p[i].n, bmn ? p[i].n : p[i].k, bmn, TN / 2);
         };
         op_a(&maps.a[i], p[i].a);
         op_b(&maps.b[i], p[i].b);
@@ -397,7 +399,7 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
         for (int j = 0; j < (MODE == kGated || MODE == kSlopes ? kProducts : 1); ++j)
             if (p[i].c[j] && e == cudaSuccess) e = result(&maps.c[i + j], p[i].c[j], p[i].m, p[i].n);
         g.m_tiles[i] = (int)((p[i].m + 255) / 256);
-        g.n_tiles[i] = (int)((p[i].n + (MODE == kGated ? 127 : 255)) / (MODE == kGated ? 128 : 256));
+        g.n_tiles[i] = (int)((p[i].n + (MODE == kGated ? 127 : TN - 1)) / (MODE == kGated ? 128 : TN));
         g.c_rows[i] = (int)p[i].m;
         g.cols[i] = (int)p[i].n;
         tiles += (long long)g.m_tiles[i] * g.n_tiles[i];
@@ -408,13 +410,23 @@ gdn_status run_pair(const char *name, const Product *p, int count, PairArgs g, c
     for (int i = count; i < kProducts; ++i) g.first[i] = (int)tiles;
     g.status = dev.status;
     g.spin_limit = dev.spin_limit;
-    auto k = pair_kernel<MODE>;
-    if ((e = allow_smem((const void *)k, pair_smem(MODE))) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
+    auto k = pair_kernel<MODE, TN>;
+    if ((e = allow_smem((const void *)k, pair_smem(MODE, TN))) != cudaSuccess) return cuda_fail(e, "shared memory of the product");
     const int pairs = (int)std::min<long long>(tiles, dev.sms / 2);
     prof_before(name, q);
-    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), pair_smem(MODE), 2, q, maps, g);
+    e = launch_pdl_cluster(k, dim3(2 * pairs), dim3(kPairThreads), pair_smem(MODE, TN), 2, q, maps, g);
     prof_after(q);
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward product launch");
+}
+
+// Tiles of 256 x 128 where those of 256 x 256 would leave half of the pairs without one: 1000 x 5464 x
+// 2048 41 us in 32 wide tiles, 33 in 64 narrow ones (not half, as a stage of either is bound by what
+// comes into an SM).
+bool narrow_fits(const Product &p, int sms) { return (p.m + 255) / 256 * ((p.n + 255) / 256) * 2 <= sms / 2; }
+
+template <int MODE>
+gdn_status run_pair_any(const char *name, const Product &p, const PairArgs &g, const LayerDevice &dev, cudaStream_t q) {
+    return narrow_fits(p, dev.sms) ? run_pair<MODE, 128>(name, &p, 1, g, dev, q) : run_pair<MODE>(name, &p, 1, g, dev, q);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -608,10 +620,14 @@ int token_tile(int tokens) {
     return nt;
 }
 
-// Single CTAs for up to 128 tokens, and while their tiles are no more than a wave.
-bool few_fits(const Product &p, int sms) {
-    const int nt = token_tile((int)std::min<long long>(p.m, 128));
-    return p.m <= 128 || (p.n + 127) / 128 * ((p.m + nt - 1) / nt) <= sms;
+// Single CTAs for up to 128 tokens; of the product out of the block also while their tiles are three
+// fifths of a wave at most.  Above, a stage of theirs takes 0.5 us, as long as its 32 KB to every SM, and
+// CTA pairs, which take half as much for a product, are ahead.  Us of single CTAs | pairs, into the
+// block: 128 x 4096 x 12288 47 | 55, 192 x 2048 x 5464 25 | 22, 256 x 4096 x 12288 68 | 56; out of it 256
+// x 12288 x 4096 35 | 49, 512 x 5464 x 2048 27 | 33, 768 x 5464 x 2048 40 | 33, 1000 x 5464 x 2048 40 | 33.
+bool few_fits(const Product &p, bool gated, int sms) {
+    if (p.m <= 128) return true;
+    return !gated && (p.n + 127) / 128 * ((p.m + 127) / 128) * 5 <= sms * 3;
 }
 
 template <bool GATED>
@@ -715,12 +731,12 @@ gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *a, void *ws, size_t ws_bytes, voi
     g.gelu = a->activation == GDN_ACT_GELU;
     const ffn::Product up{a->x, a->w_gate, a->w_up, nullptr, {ws, a->gate, a->up}, a->M, a->F, a->K};
     const ffn::Product down{ws, a->w_down, nullptr, nullptr, {a->y}, a->M, a->K, a->F};
-    const bool few = ffn::few_fits(up, dev.sms);
+    const bool few = ffn::few_fits(up, true, dev.sms);
     st = few ? ffn::run_few<true>("ffn_gated_few", up, g.gelu, false, dev, q)
              : ffn::run_pair<ffn::kGated>("ffn_gated", &up, 1, g, dev, q);
     if (st != GDN_OK) return st;
-    return ffn::few_fits(down, dev.sms) ? ffn::run_few<false>("ffn_down_few", down, 0, few, dev, q)
-                                        : ffn::run_pair<ffn::kDown>("ffn_down", &down, 1, g, dev, q);
+    return ffn::few_fits(down, false, dev.sms) ? ffn::run_few<false>("ffn_down_few", down, 0, few, dev, q)
+                                        : ffn::run_pair_any<ffn::kDown>("ffn_down", down, g, dev, q);
 }
 
 size_t gdn_ffn_bwd_workspace_size(const gdn_ffn_bwd_args *a) {
@@ -765,7 +781,7 @@ gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *a, void *ws, size_t ws_bytes, voi
                                 {du, a->x, nullptr, nullptr, {a->dw_up}, a->F, a->K, a->M},
                                 {a->d_y, h, nullptr, nullptr, {a->dw_down}, a->K, a->F, a->M}};
     st = ffn::run_pair<ffn::kSlopes>("ffn_slopes", &dh, 1, g, dev, q);
-    if (st == GDN_OK) st = ffn::run_pair<ffn::kInput>("ffn_input", &dx, 1, g, dev, q);
+    if (st == GDN_OK) st = ffn::run_pair_any<ffn::kInput>("ffn_input", dx, g, dev, q);
     if (st == GDN_OK) st = ffn::run_pair<ffn::kWeights>("ffn_weights", dw, 3, g, dev, q);
     return st;
 }

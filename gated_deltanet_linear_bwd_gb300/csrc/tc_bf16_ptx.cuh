@@ -86,12 +86,12 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
 }
-// Rows row .. row + 127 of an operand, contraction k .. k + 63.
-template <bool MN, bool PAIR>
+// ROWS (64 or 128) of an operand from `row` on, contraction k .. k + 63.
+template <bool MN, bool PAIR, int ROWS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int row, int k, uint32_t bar) {
     if (MN) {
         load_box<PAIR>(dst, map, row, k, bar);
-        load_box<PAIR>(dst + 8192, map, row + 64, k, bar);
+        if (ROWS == 128) load_box<PAIR>(dst + 8192, map, row + 64, k, bar);
     } else {
         load_box<PAIR>(dst, map, k, row, bar);
     }
