@@ -104,54 +104,6 @@ __device__ __forceinline__ int parts_of(const Cut &c, int n, int &count) {
     return c.s.cu ? (int)(bos / c.part) + n : n * c.per;
 }
 
-// Eight neighbouring channels of a token; VECT: rows that start on 16 bytes.
-template <typename T>
-struct Eight {
-    uint4 r[sizeof(T) / 2];
-    __device__ __forceinline__ float at(int i) const { return to_f(reinterpret_cast<const T *>(r)[i]); }
-};
-template <typename T, bool VECT>
-__device__ __forceinline__ Eight<T> load8(const void *base, long long token, int ch, int D, bool live) {
-    Eight<T> e;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.r[i] = make_uint4(0, 0, 0, 0);
-    if (!base || !live) return e;
-    const T *p = (const T *)base + token * D + ch;
-    if (VECT) {
-        if (ch < D) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.r[i] = reinterpret_cast<const uint4 *>(p)[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (ch + i < D) reinterpret_cast<T *>(e.r)[i] = p[i];
-    }
-    return e;
-}
-template <typename T, bool VECT>
-__device__ __forceinline__ void store8(void *base, long long token, int ch, int D, const float *v) {
-    T *p = (T *)base + token * D + ch;
-    if (VECT) {
-        if (ch < D) {
-            uint4 r[sizeof(T) / 2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) from_f(reinterpret_cast<T *>(r) + i, v[i]);
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (ch + i < D) from_f(p + i, v[i]);
-    }
-}
-// Eight neighbouring parameters; zeros past the end and without any.
-__device__ __forceinline__ void params8(const float *p, int ch, int D, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p && ch + i < D ? p[ch + i] : 0.f;
-}
-
 // A lane's 2 P neighbouring states, from s0 on, of a row of a [.., D, S] tensor.
 template <int P>
 __device__ __forceinline__ void load_states(const float *base, long long row, int S, int s0, bool in, float2 (&v)[P]) {
@@ -314,6 +266,15 @@ __device__ __forceinline__ void copy2(T *to, const T *from, bool both_in) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
                      "n"(2 * (int)sizeof(T))
                      : "memory");
+    } else {
+        to[0] = from[0];
+        if (both_in) to[1] = from[1];
+    }
+}
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void load2(T *to, const T *from, bool both_in) {
+    if (PAIRS) {
+        *reinterpret_cast<typename Vec<T, 2>::Raw *>(to) = Vec<T, 2>::raw(from);
     } else {
         to[0] = from[0];
         if (both_in) to[1] = from[1];
@@ -557,41 +518,29 @@ __global__ void __launch_bounds__(256) join_kernel(JoinArgs a) {
     int count;
     const int first = parts_of(a.cut, n, count);
     const float a2 = a.a[i] * kLog2e;
-    constexpr int kAhead = 8;
-    float v = a.h0 ? a.h0[n * states + i] : 0.f;
+    constexpr int kAhead = 16;                     // parts whose loads are in flight
+    // one direction to a thread: parts in order for the states, from the last for the gradients
+    const bool back = blockIdx.z == 1;
+    float *const pairs = back ? a.back : a.end;
+    const float *const from = back ? a.dht : a.h0;
+    const auto at = [&](int j) { return (long long)(first + (back ? count - 1 - j : j)); };
+    float v = from ? from[n * states + i] : 0.f;
     for (int j = 0; j < count; j += kAhead) {
         float e[kAhead], st[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (j + k < count) {
-                e[k] = a.end[(first + j + k) * states + i];
-                st[k] = a.steps[(long long)(first + j + k) * a.D + d];
+                e[k] = pairs[at(j + k) * states + i];
+                st[k] = a.steps[at(j + k) * a.D + d];
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (j + k < count) {
-                a.end[(first + j + k) * states + i] = v;
+                pairs[at(j + k) * states + i] = v;
                 v = fmaf(ex2(st[k] * a2), v, e[k]);
             }
     }
-    if (!a.back) return;
-    v = a.dht ? a.dht[n * states + i] : 0.f;
-    for (int j = count; j > 0; j -= kAhead) {
-        float e[kAhead], st[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (j - 1 - k >= 0) {
-                e[k] = a.back[(first + j - 1 - k) * states + i];
-                st[k] = a.steps[(long long)(first + j - 1 - k) * a.D + d];
-            }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (j - 1 - k >= 0) {
-                a.back[(first + j - 1 - k) * states + i] = v;
-                v = fmaf(ex2(st[k] * a2), v, e[k]);
-            }
-    }
-    if (a.dh0 && count > 0) a.dh0[n * states + i] = v;
+    if (back && a.dh0 && count > 0) a.dh0[n * states + i] = v;
 }
 
 // ------------------------------------------------------------------ backward
@@ -608,22 +557,23 @@ struct BwdArgs {
     Cut cut;
 };
 
+// A lane has four states of two channels here, LP lanes a pair of channels: the decays and decayed
+// states of a sub-segment's tokens are 128 registers.
 template <int LP>
 struct Segment {
-    static constexpr int CH = LP <= 4 ? 64 : 256 / LP, NT = CH * LP, WARPS = NT / 32;
+    static constexpr int CP = LP <= 4 ? 32 : 128 / LP, CH = 2 * CP, NT = CP * LP, WARPS = NT / 32;
     static constexpr int SP = 4 * LP, V = 2 * SP;  // states, and gradients of b and c of a token
-    static constexpr int BUFS = LP <= 4 ? 2 : 1;
-    static constexpr int YS = CH + (LP == 16 ? 4 : 32 / LP);
-    float2 du[kSegment * CH];                      // step, step x; then <e, b>, <e a, p>
-    float ds[kSegment * YS];                       // gradient before the gate; then <c, h>
+    float4 du[kSegment][CP];                       // steps, steps x; then <e, b>, <e a, p>
+    float2 ds[kSegment][CP];                       // gradients before the gate; then <c, h>
     float4 b[kSegment * LP], c[kSegment * LP];
-    float4 saved[(kSegment / kSub - 1) * NT];      // states before the sub-segments; then sums of dskip, dbias
-    float red[BUFS][WARPS][kSub][V];
+    float4 saved[kSegment / kSub - 1][2][NT];      // states before the sub-segments; then sums of dskip, dbias
+    float red[2][WARPS][kSub][V];
     float acc[kSegment * V];
 };
+using SubStates = float2[2][2];                    // [channel][pair of states]
 
-template <typename T, int LP, bool VECT>
-__global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::NT : 1) bwd_kernel(BwdArgs a) {
+template <typename T, int LP, bool PAIRS>
+__global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 256 / Segment<LP>::NT : 1) bwd_kernel(BwdArgs a) {
     using G = Segment<LP>;
     extern __shared__ __align__(16) uint8_t shared[];
     G &m = *reinterpret_cast<G *>(shared);
@@ -632,19 +582,21 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
     const int slot = blockIdx.x / a.lanes, lane_no = blockIdx.x - slot * a.lanes;
     const int D = a.in.D, S = a.in.S, tid = threadIdx.x;
     const int g0 = (int)((long long)a.in.groups * lane_no / a.lanes), g1 = (int)((long long)a.in.groups * (lane_no + 1) / a.lanes);
-    const int s = tid % LP, c = tid / LP, warp = tid / 32;
+    const int s = tid % LP, pair = tid / LP, warp = tid / 32;
     Part part;
     const bool there = part_of(a.cut, slot, part) && part.len > 0;
     if (!there) {                                  // its parts of the sums
-        for (int g = g0; g < g1; ++g) {
-            const int ch = g * G::CH + c;
-            const float2 none[2] = {both(0.f), both(0.f)};
-            store_states(a.start, (long long)slot * D + ch, S, 4 * s, ch < D, none);
-            if (ch < D && s == 0) {
-                if (a.dskip) a.dskip[(long long)slot * D + ch] = 0.f;
-                if (a.dbias) a.dbias[(long long)slot * D + ch] = 0.f;
+        for (int g = g0; g < g1; ++g)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int ch = g * G::CH + 2 * pair + c;
+                const float2 none[2] = {both(0.f), both(0.f)};
+                store_states(a.start, (long long)slot * D + ch, S, 4 * s, ch < D, none);
+                if (ch < D && s == 0) {
+                    if (a.dskip) a.dskip[(long long)slot * D + ch] = 0.f;
+                    if (a.dbias) a.dbias[(long long)slot * D + ch] = 0.f;
+                }
             }
-        }
         return;
     }
     const int len = part.len, subs = (len + kSub - 1) / kSub;
@@ -657,100 +609,136 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
     }
     for (int k = tid; k < kSegment * G::V; k += G::NT) m.acc[k] = 0.f;
 
+    // as one that loads and stores: a pair of channels, every LP-th token
+    const int mp = tid % G::CP, mt = tid / G::CP;
+    struct alignas(16) Raw {
+        T x[2], dt[2], z[2], dy[2];
+    };
     for (int g = g0; g < g1; ++g) {
-        const int ch = g * G::CH + c;
-        const bool in = ch < D;
-        float bias[8];
-        const int mc = tid * 8 % G::CH, mch = g * G::CH + mc;
-        params8(a.in.dt_bias, mch, D, bias);
-        for (int k = tid * 8; k < kSegment * G::CH; k += 8 * G::NT) {
-            const int t = k / G::CH;
-            const bool live = t < len;
-            const Eight<T> x = load8<T, VECT>(a.in.x, part.first + t, mch, D, live);
-            const Eight<T> dt = load8<T, VECT>(a.in.dt, part.first + t, mch, D, live);
-            const Eight<T> z = load8<T, VECT>(a.in.z, part.first + t, mch, D, live);
-            const Eight<T> dy = load8<T, VECT>(a.in.dy, part.first + t, mch, D, live);
+        const int mch = g * G::CH + 2 * mp;
+        const bool m0 = mch < D, m1 = mch + 1 < D;
+        const auto param = [&](const float *p) { return make_float2(p && m0 ? p[mch] : 0.f, p && m1 ? p[mch + 1] : 0.f); };
+        const float2 bias = param(a.in.dt_bias), skip = param(a.in.skip);
+        const long long base = part.first * D + mch;
+        const auto fetch = [&](int t, Raw &r) {
+            r = {};
+            if (t >= len || !m0) return;
+            const long long at = base + (long long)t * D;
+            load2<T, PAIRS>(r.x, (const T *)a.in.x + at, m1);
+            load2<T, PAIRS>(r.dt, (const T *)a.in.dt + at, m1);
+            if (a.in.z) load2<T, PAIRS>(r.z, (const T *)a.in.z + at, m1);
+            load2<T, PAIRS>(r.dy, (const T *)a.in.dy + at, m1);
+        };
+        constexpr int kBatch = 8 < kSegment / LP ? 8 : kSegment / LP;    // tokens whose loads are in flight
+        for (int t0 = mt; t0 < kSegment; t0 += kBatch * LP) {
+            Raw r[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float raw = dt.at(i) + bias[i], zi = z.at(i);
-                const float step = !live ? 0.f : a.in.dt_bias ? softplus<T>(raw) : raw;
-                m.du[t * G::CH + mc + i] = make_float2(step, step * x.at(i));
-                m.ds[t * G::YS + mc + i] = a.in.z ? dy.at(i) * zi * logistic<T>(zi) : dy.at(i);
+            for (int j = 0; j < kBatch; ++j) fetch(t0 + j * LP, r[j]);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int t = t0 + j * LP;
+                float2 step = get2(r[j].dt), ds = get2(r[j].dy);
+                if (a.in.dt_bias) step = softplus2<T>(__fadd2_rn(step, bias));
+                if (t >= len) step = both(0.f);
+                if (a.in.z) {
+                    const float2 z = get2(r[j].z);
+                    ds = __fmul2_rn(ds, __fmul2_rn(z, logistic2<T>(z)));
+                }
+                const float2 u = __fmul2_rn(step, get2(r[j].x));
+                m.du[t][mp] = make_float4(step.x, step.y, u.x, u.y);
+                m.ds[t][mp] = ds;
             }
         }
-        float2 an[2], a2[2], hs[2], carry[2], da[2] = {both(0.f), both(0.f)};
+        SubStates an, a2, hs, carry, da;
+        const int ch = g * G::CH + 2 * pair;
         const long long row = (long long)slot * D + ch;
-        load_states(a.in.a, ch, S, 4 * s, in, an);
-        load_states(a.start, row, S, 4 * s, in, hs);
-        load_states(a.behind, row, S, 4 * s, in, carry);
-        a2[0] = __fmul2_rn(an[0], both(kLog2e));
-        a2[1] = __fmul2_rn(an[1], both(kLog2e));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            load_states(a.in.a, ch + c, S, 4 * s, ch + c < D, an[c]);
+            load_states(a.start, row + c, S, 4 * s, ch + c < D, hs[c]);
+            load_states(a.behind, row + c, S, 4 * s, ch + c < D, carry[c]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a2[c][i] = __fmul2_rn(an[c][i], both(kLog2e));
+                da[c][i] = both(0.f);
+            }
+        }
         __syncthreads();
 
         // the states before every sub-segment
         {
-            float2 h[2] = {hs[0], hs[1]};
+            SubStates h = {{hs[0][0], hs[0][1]}, {hs[1][0], hs[1][1]}};
             for (int q = 0; q + 1 < subs; ++q) {
 #pragma unroll
                 for (int k = 0; k < kSub; ++k) {
                     const int t = q * kSub + k;
-                    const float2 du = m.du[t * G::CH + c];
-                    const float4 b = m.b[t * LP + s];
-                    h[0] = __ffma2_rn(decay<T>(both(du.x), a2[0]), h[0], __fmul2_rn(both(du.y), make_float2(b.x, b.y)));
-                    h[1] = __ffma2_rn(decay<T>(both(du.x), a2[1]), h[1], __fmul2_rn(both(du.y), make_float2(b.z, b.w)));
+                    const float4 du = m.du[t][pair], b = m.b[t * LP + s];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            h[c][i] = __ffma2_rn(decay<T>(both(c ? du.y : du.x), a2[c][i]), h[c][i],
+                                                 __fmul2_rn(both(c ? du.w : du.z), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y)));
                 }
-                m.saved[q * G::NT + tid] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) m.saved[q][c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
             }
         }
         for (int q = subs - 1; q >= 0; --q) {
-            float2 h[2] = {hs[0], hs[1]}, e[kSub][2], p[kSub][2];
-            if (q > 0) {
-                const float4 v = m.saved[(q - 1) * G::NT + tid];
-                h[0] = make_float2(v.x, v.y);
-                h[1] = make_float2(v.z, v.w);
-            }
+            SubStates h = {{hs[0][0], hs[0][1]}, {hs[1][0], hs[1][1]}}, e[kSub], p[kSub];
+            if (q > 0)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float4 v = m.saved[q - 1][c][tid];
+                    h[c][0] = make_float2(v.x, v.y);
+                    h[c][1] = make_float2(v.z, v.w);
+                }
 #pragma unroll
             for (int k = 0; k < kSub; ++k) {
                 const int t = q * kSub + k;
-                const float2 du = m.du[t * G::CH + c];
-                const float4 b = m.b[t * LP + s];
+                const float4 du = m.du[t][pair], b = m.b[t * LP + s];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    e[k][i] = decay<T>(both(du.x), a2[i]);
-                    p[k][i] = __fmul2_rn(e[k][i], h[i]);
-                    h[i] = __ffma2_rn(both(du.y), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y), p[k][i]);
-                }
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        e[k][c][i] = decay<T>(both(c ? du.y : du.x), a2[c][i]);
+                        p[k][c][i] = __fmul2_rn(e[k][c][i], h[c][i]);
+                        h[c][i] = __ffma2_rn(both(c ? du.w : du.z), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y), p[k][c][i]);
+                    }
             }
-            float hc[kSub], eb[kSub], ep[kSub];    // <c, h>, <e, b>, <e a, p> of this lane's states
-            float *red = &m.red[G::BUFS == 2 ? q & 1 : 0][warp][0][0];
-            if (G::BUFS == 1) __syncthreads();     // the sub-segment before has been added up
+            // <c, h>, <e, b> and <e a, p> of this lane's states, [token][channel]
+            float hc[2 * kSub], eb[2 * kSub], ep[2 * kSub];
+            float *red = &m.red[q & 1][warp][0][0];
 #pragma unroll
             for (int k = kSub - 1; k >= 0; --k) {
                 const int t = q * kSub + k;
-                const float2 du = m.du[t * G::CH + c];
-                const float ds = m.ds[t * G::YS + c];
-                const float4 b4 = m.b[t * LP + s], c4 = m.c[t * LP + s];
-                float2 vh = both(0.f), vb = both(0.f), vp = both(0.f);
-                float2 gbc[4];                     // gradients of b and c
+                const float4 du = m.du[t][pair], b4 = m.b[t * LP + s], c4 = m.c[t * LP + s];
+                const float2 ds2 = m.ds[t][pair];
+                float2 gb[2], gc[2];               // gradients of b and c, of both channels
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 b = i ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
-                    const float2 cc = i ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
-                    const float2 hh = __ffma2_rn(both(du.y), b, p[k][i]);
-                    gbc[2 + i] = __fmul2_rn(both(ds), hh);
-                    vh = __ffma2_rn(cc, hh, vh);
-                    const float2 grad = __ffma2_rn(cc, both(ds), carry[i]);
-                    gbc[i] = __fmul2_rn(grad, both(du.y));
-                    vb = __ffma2_rn(grad, b, vb);
-                    const float2 lost = __fmul2_rn(grad, p[k][i]);
-                    da[i] = __ffma2_rn(lost, both(du.x), da[i]);
-                    vp = __ffma2_rn(lost, an[i], vp);
-                    carry[i] = __fmul2_rn(e[k][i], grad);
+                for (int c = 0; c < 2; ++c) {
+                    const float2 step = both(c ? du.y : du.x), u = both(c ? du.w : du.z), ds = both(c ? ds2.y : ds2.x);
+                    float2 vh, vb, vp;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 b = i ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+                        const float2 cc = i ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+                        const float2 hh = __ffma2_rn(u, b, p[k][c][i]);
+                        const float2 grad = __ffma2_rn(cc, ds, carry[c][i]);
+                        const float2 lost = __fmul2_rn(grad, p[k][c][i]);
+                        gc[i] = c ? __ffma2_rn(ds, hh, gc[i]) : __fmul2_rn(ds, hh);
+                        gb[i] = c ? __ffma2_rn(grad, u, gb[i]) : __fmul2_rn(grad, u);
+                        vh = i ? __ffma2_rn(cc, hh, vh) : __fmul2_rn(cc, hh);
+                        vb = i ? __ffma2_rn(grad, b, vb) : __fmul2_rn(grad, b);
+                        vp = i ? __ffma2_rn(lost, an[c][i], vp) : __fmul2_rn(lost, an[c][i]);
+                        da[c][i] = __ffma2_rn(lost, step, da[c][i]);
+                        carry[c][i] = __fmul2_rn(e[k][c][i], grad);
+                    }
+                    hc[2 * k + c] = vh.x + vh.y;
+                    eb[2 * k + c] = vb.x + vb.y;
+                    ep[2 * k + c] = vp.x + vp.y;
                 }
-                hc[k] = vh.x + vh.y;
-                eb[k] = vb.x + vb.y;
-                ep[k] = vp.x + vp.y;
-                float v[8] = {gbc[0].x, gbc[0].y, gbc[1].x, gbc[1].y, gbc[2].x, gbc[2].y, gbc[3].x, gbc[3].y};
+                float v[8] = {gb[0].x, gb[0].y, gb[1].x, gb[1].y, gc[0].x, gc[0].y, gc[1].x, gc[1].y};
                 constexpr int NL = 32 / LP, LEFT = NL >= 8 ? 1 : 8 / NL;
                 const int lane = (tid & 31) / LP, from = share_sum<8, NL, LP>(v, lane);
                 if (NL <= 8 || (lane & (NL / 8 - 1)) == 0) {
@@ -761,80 +749,88 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 512 / Segment<LP>::
                     }
                 }
             }
-            // over the channel's lanes; every lane has read its tokens' steps and gradients
+            // over the channels' lanes; every lane has read its tokens' steps and gradients
             {
-                constexpr int LEFT = LP >= 8 ? 1 : 8 / LP;
-                int from = share_sum<8, LP, 1>(hc, s);
-                share_sum<8, LP, 1>(eb, s);
-                share_sum<8, LP, 1>(ep, s);
+                constexpr int LEFT = 2 * kSub / LP;
+                const int from = share_sum<2 * kSub, LP, 1>(hc, s);
+                share_sum<2 * kSub, LP, 1>(eb, s);
+                share_sum<2 * kSub, LP, 1>(ep, s);
                 __syncwarp();
-                if (LP <= 8 || (s & (LP / 8 - 1)) == 0) {
+                const int t = q * kSub + from / 2;
+                if constexpr (LEFT >= 2) {
 #pragma unroll
-                    for (int i = 0; i < LEFT; ++i) {
-                        const int t = q * kSub + from + i;
-                        m.du[t * G::CH + c] = make_float2(eb[i], ep[i]);
-                        m.ds[t * G::YS + c] = hc[i];
+                    for (int i = 0; i < LEFT; i += 2) {
+                        m.du[t + i / 2][pair] = make_float4(eb[i], eb[i + 1], ep[i], ep[i + 1]);
+                        m.ds[t + i / 2][pair] = make_float2(hc[i], hc[i + 1]);
                     }
+                } else {                           // one channel's
+                    const int c = from & 1;
+                    float *sums = reinterpret_cast<float *>(&m.du[t][pair]);
+                    sums[c] = eb[0];
+                    sums[2 + c] = ep[0];
+                    reinterpret_cast<float *>(&m.ds[t][pair])[c] = hc[0];
                 }
             }
             __syncthreads();
             for (int k = tid; k < kSub * G::V; k += G::NT) {
                 float v = m.acc[q * kSub * G::V + k];
 #pragma unroll
-                for (int w = 0; w < G::WARPS; ++w) v += (&m.red[G::BUFS == 2 ? q & 1 : 0][w][0][0])[k];
+                for (int w = 0; w < G::WARPS; ++w) v += (&m.red[q & 1][w][0][0])[k];
                 m.acc[q * kSub * G::V + k] = v;
             }
         }
-        store_states(a.start, row, S, 4 * s, in, da);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) store_states(a.start, row + c, S, 4 * s, ch + c < D, da[c]);
         __syncthreads();                           // every channel's sums are there
 
-        float skip[8], gs[8], gb[8];
-        params8(a.in.skip, mch, D, skip);
+        float2 gs = both(0.f), gbias = both(0.f);
+        for (int t0 = mt; t0 < len; t0 += kBatch * LP) {
+            Raw r[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gs[i] = gb[i] = 0.f;
-        for (int k = tid * 8; k < len * G::CH; k += 8 * G::NT) {
-            const int t = k / G::CH;
-            const Eight<T> x = load8<T, VECT>(a.in.x, part.first + t, mch, D, true);
-            const Eight<T> dt = load8<T, VECT>(a.in.dt, part.first + t, mch, D, true);
-            const Eight<T> z = load8<T, VECT>(a.in.z, part.first + t, mch, D, true);
-            const Eight<T> dy = load8<T, VECT>(a.in.dy, part.first + t, mch, D, true);
-            float dx[8], ddt[8], dz[8];
+            for (int j = 0; j < kBatch; ++j) fetch(t0 + j * LP, r[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float raw = dt.at(i) + bias[i], zi = z.at(i), xi = x.at(i);
-                const float step = a.in.dt_bias ? softplus<T>(raw) : raw;
-                const float2 sums = m.du[t * G::CH + mc + i];
-                float ds = dy.at(i);
-                if (a.in.z) {
-                    const float sg = logistic<T>(zi);
-                    dz[i] = ds * fmaf(skip[i], xi, m.ds[t * G::YS + mc + i]) * silu_slope(zi, sg);
-                    ds *= zi * sg;
+            for (int j = 0; j < kBatch; ++j) {
+                const int t = t0 + j * LP;
+                if (t >= len || !m0) continue;
+                const float4 sums = m.du[t][mp];
+                const float2 x = get2(r[j].x), dy = get2(r[j].dy), hc = m.ds[t][mp];
+                float2 step = get2(r[j].dt), slope = both(1.f), ds = dy;
+                if (a.in.dt_bias) {
+                    const float2 raw = __fadd2_rn(step, bias);
+                    step = softplus2<T>(raw);
+                    slope = logistic2<T>(raw);
                 }
-                dx[i] = fmaf(skip[i], ds, step * sums.x);
-                ddt[i] = fmaf(xi, sums.x, sums.y);
-                if (a.in.dt_bias) ddt[i] *= logistic<T>(raw);
-                gs[i] = fmaf(ds, xi, gs[i]);
-                gb[i] += ddt[i];
+                const long long at = base + (long long)t * D;
+                if (a.in.z) {
+                    const float2 z = get2(r[j].z), sg = logistic2<T>(z), y = __ffma2_rn(skip, x, hc);
+                    store2<T, PAIRS>((T *)a.dz + at, m1,
+                                     __fmul2_rn(__fmul2_rn(dy, y), make_float2(silu_slope(z.x, sg.x), silu_slope(z.y, sg.y))));
+                    ds = __fmul2_rn(dy, __fmul2_rn(z, sg));
+                }
+                const float2 eb = make_float2(sums.x, sums.y);
+                const float2 ddt = __fmul2_rn(slope, __ffma2_rn(x, eb, make_float2(sums.z, sums.w)));
+                store2<T, PAIRS>((T *)a.dx + at, m1, __ffma2_rn(skip, ds, __fmul2_rn(step, eb)));
+                store2<T, PAIRS>((T *)a.ddt + at, m1, ddt);
+                gs = __ffma2_rn(ds, x, gs);
+                gbias = __fadd2_rn(gbias, ddt);
             }
-            store8<T, VECT>(a.dx, part.first + t, mch, D, dx);
-            store8<T, VECT>(a.ddt, part.first + t, mch, D, ddt);
-            if (a.in.z) store8<T, VECT>(a.dz, part.first + t, mch, D, dz);
         }
         // over the threads that took the same channels
-        float *sums = reinterpret_cast<float *>(m.saved);
-        constexpr int ROWS = 8 * G::NT / G::CH;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sums[(tid * 8 / G::CH) * G::CH + mc + i] = gs[i];
-            sums[(ROWS + tid * 8 / G::CH) * G::CH + mc + i] = gb[i];
-        }
+        float4 *sums = &m.saved[0][0][0];
+        sums[mt * G::CP + mp] = make_float4(gs.x, gs.y, gbias.x, gbias.y);
         __syncthreads();
-        for (int k = tid; k < 2 * G::CH; k += G::NT) {
-            const int what = k / G::CH, at = k % G::CH;
-            float v = 0.f;
-            for (int r = 0; r < ROWS; ++r) v += sums[(what * ROWS + r) * G::CH + at];
-            float *out = what ? a.dbias : a.dskip;
-            if (out && g * G::CH + at < D) out[(long long)slot * D + g * G::CH + at] = v;
+        if (tid < G::CP) {
+            float4 v = sums[tid];
+#pragma unroll
+            for (int r = 1; r < LP; ++r) {
+                const float4 w = sums[r * G::CP + tid];
+                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+            }
+            const long long at = (long long)slot * D + mch;
+            if (a.dskip && m0) a.dskip[at] = v.x;
+            if (a.dskip && m1) a.dskip[at + 1] = v.y;
+            if (a.dbias && m0) a.dbias[at] = v.z;
+            if (a.dbias && m1) a.dbias[at + 1] = v.w;
         }
         __syncthreads();                           // before the next channels' tile
     }
@@ -1045,7 +1041,8 @@ cudaError_t launch_fwd(const char *name, FwdArgs f, int dtype, cudaStream_t q) {
 cudaError_t launch_join(const JoinArgs &j, cudaStream_t q) {
     const long long states = (long long)j.D * j.S;
     prof_before("ssm_join", q);
-    const cudaError_t e = launch_pdl(join_kernel, dim3((unsigned)((states + 255) / 256), j.cut.s.N), dim3(256), 0, q, j);
+    const cudaError_t e = launch_pdl(join_kernel, dim3((unsigned)((states + 255) / 256), j.cut.s.N, j.back ? 2 : 1),
+                                     dim3(256), 0, q, j);
     prof_after(q);
     return e;
 }
@@ -1053,7 +1050,7 @@ cudaError_t launch_join(const JoinArgs &j, cudaStream_t q) {
 template <typename T>
 cudaError_t launch_bwd(BwdArgs b, cudaStream_t q) {
     cudaError_t e = by_lanes<16>(lanes_of(b.in.S, 4), [&](auto lp) {
-        return by_alignment(b.in.D % 8 == 0, [&](auto vect) {
+        return by_alignment(b.in.D % 2 == 0, [&](auto vect) {
             constexpr int LP = decltype(lp)::value;
             using G = Segment<LP>;
             auto k = bwd_kernel<T, LP, decltype(vect)::value>;
