@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 3) fwd_kernel(FwdArgs a) {
 struct BwdArgs {
     const void *dy, *x, *w, *bias, *h0, *dht;
     void *dx, *dh0;
-    float *partial;                // [runs][D][W], then [runs][D]: each run's dweight and dbias
+    float *partial;                // [runs][D][W + 1]: each run's dweight and dbias
     Seqs s;
     int tokens, D, run, runs;
     int *status;
@@ -396,13 +396,32 @@ __global__ void __launch_bounds__(kThreads, 2) bwd_kernel(BwdArgs a) {
             }
         }
     }
-    float *pw = a.partial + ((long long)item * a.D + ch) * W, *pb = a.partial + (long long)a.runs * a.D * W + (long long)item * a.D + ch;
+    float *p = a.partial + ((long long)item * a.D + ch) * (W + 1);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) pw[i * W + k] = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
-        pb[i] = i & 1 ? db[i / 2].y : db[i / 2].x;
+        for (int k = 0; k < W; ++k) p[i * (W + 1) + k] = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
+        p[i * (W + 1) + W] = i & 1 ? db[i / 2].y : db[i / 2].x;
     }
+}
+
+// dweight and dbias from the runs' sums, [runs][D][W + 1], in a fixed order.
+__global__ void __launch_bounds__(256) sums_kernel(const float *partial, int runs, int D, int W, float *dweight, float *dbias) {
+    __shared__ float strip[8][32];
+    pdl_enter();
+    const int lane = threadIdx.x & 31, strip_no = threadIdx.x >> 5, columns = D * (W + 1);
+    const int i = blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (i < columns)
+        for (int r = strip_no; r < runs; r += 8) t += partial[(long long)r * columns + i];
+    strip[strip_no][lane] = t;
+    __syncthreads();
+    if (strip_no > 0 || i >= columns) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t += strip[k][lane];
+    const int d = i / (W + 1), k = i - d * (W + 1);
+    if (k < W) dweight[d * W + k] = t;
+    else if (dbias) dbias[d] = t;
 }
 
 template <typename T, int VEC, int W, bool SILU>
@@ -518,9 +537,11 @@ cudaError_t run_bwd(BwdArgs g, int W, int activation, float *dweight, float *dbi
         prof_after(q);
         return r;
     });
-    if (e == cudaSuccess) e = column_sum(g.partial, g.runs, g.D * W, dweight, q);
-    if (e == cudaSuccess && dbias)
-        e = column_sum(g.partial + (long long)g.runs * g.D * W, g.runs, g.D, dbias, q);
+    if (e != cudaSuccess) return e;
+    prof_before("conv_sums", q);
+    e = launch_pdl(sums_kernel, dim3((unsigned)(((long long)g.D * (W + 1) + 31) / 32)), dim3(256), 0, q, (const float *)g.partial,
+                   g.runs, g.D, W, dweight, dbias);
+    prof_after(q);
     return e;
 }
 

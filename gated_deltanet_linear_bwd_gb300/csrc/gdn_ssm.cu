@@ -570,10 +570,11 @@ struct Segment {
     float red[2][WARPS][kSub][V];
     float acc[kSegment * V];
 };
+constexpr int kBwdThreads = 256;                   // on an SM at once
 using SubStates = float2[2][2];                    // [channel][pair of states]
 
 template <typename T, int LP, bool PAIRS>
-__global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 256 / Segment<LP>::NT : 1) bwd_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT) bwd_kernel(BwdArgs a) {
     using G = Segment<LP>;
     extern __shared__ __align__(16) uint8_t shared[];
     G &m = *reinterpret_cast<G *>(shared);
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 256 / Segment<LP>::
             }
             // over the channels' lanes; every lane has read its tokens' steps and gradients
             {
-                constexpr int LEFT = 2 * kSub / LP;
+                constexpr int LEFT = LP < 2 * kSub ? 2 * kSub / LP : 1;
                 const int from = share_sum<2 * kSub, LP, 1>(hc, s);
                 share_sum<2 * kSub, LP, 1>(eb, s);
                 share_sum<2 * kSub, LP, 1>(ep, s);
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(Segment<LP>::NT, LP <= 8 ? 256 / Segment<LP>::
                         m.du[t + i / 2][pair] = make_float4(eb[i], eb[i + 1], ep[i], ep[i + 1]);
                         m.ds[t + i / 2][pair] = make_float2(hc[i], hc[i + 1]);
                     }
-                } else {                           // one channel's
+                } else if (LP <= 2 * kSub || (s & (LP / (2 * kSub) - 1)) == 0) {    // one channel's
                     const int c = from & 1;
                     float *sums = reinterpret_cast<float *>(&m.du[t][pair]);
                     sums[c] = eb[0];
@@ -869,50 +870,54 @@ struct StepArgs {
     float *out;
     int N;
 };
+// A thread takes four states of a channel, of every gridDim.y-th sequence.
 template <typename T, int LP>
 __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
     pdl_enter();
-    const int D = a.in.D, S = a.in.S, s = threadIdx.x % LP;
-    const long long rows = (long long)a.N * D;
-    for (long long r0 = (long long)blockIdx.x * (kThreads / LP); r0 < rows; r0 += (long long)gridDim.x * (kThreads / LP)) {
-        const long long row = r0 + threadIdx.x / LP;
-        const bool in = row < rows;
-        const long long n = in ? row / D : 0;
-        const int ch = in ? (int)(row - n * D) : 0;
-        float2 h[2], an[2];
+    const int D = a.in.D, S = a.in.S, s = threadIdx.x % LP, ch = blockIdx.x * (kThreads / LP) + threadIdx.x / LP;
+    const bool in = ch < D;
+    float2 a2[2];
+    load_states(a.in.a, ch, S, 4 * s, in, a2);
+    a2[0] = __fmul2_rn(a2[0], both(kLog2e));
+    a2[1] = __fmul2_rn(a2[1], both(kLog2e));
+    const float bias = a.in.dt_bias && in ? a.in.dt_bias[ch] : 0.f, skip = a.in.skip && in ? a.in.skip[ch] : 0.f;
+    const auto coefficients = [&](const void *base, long long n, float (&v)[4]) {
+        const T *p = (const T *)base + n * S + 4 * s;
+        if ((S & 3) == 0 && 4 * s < S) {
+            Vec<T, 4>::load(p, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = 4 * s + i < S ? to_f(p[i]) : 0.f;
+        }
+    };
+    for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
+        const long long row = (long long)n * D + ch;
+        float2 h[2];
         load_states(a.state, row, S, 4 * s, in, h);
-        load_states(a.in.a, ch, S, 4 * s, in, an);
-        float step = 0.f, x = 0.f;
+        float b[4], cc[4], step = 0.f, x = 0.f, z = 0.f;
+        coefficients(a.in.b, n, b);
+        coefficients(a.in.c, n, cc);
         if (in) {
             x = to_f(((const T *)a.in.x)[row]);
             step = to_f(((const T *)a.in.dt)[row]);
-            if (a.in.dt_bias) step = softplus<T>(step + a.in.dt_bias[ch]);
+            if (a.in.z) z = to_f(((const T *)a.in.z)[row]);
         }
-        float b[4], cc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool has = in && 4 * s + i < S;
-            b[i] = has ? to_f(((const T *)a.in.b)[n * S + 4 * s + i]) : 0.f;
-            cc[i] = has ? to_f(((const T *)a.in.c)[n * S + 4 * s + i]) : 0.f;
-        }
-        float y = 0.f;
+        if (a.in.dt_bias) step = softplus<T>(step + bias);
+        float2 dot = both(0.f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 e = decay<T>(both(step), __fmul2_rn(an[i], both(kLog2e)));
-            h[i] = __ffma2_rn(e, h[i], __fmul2_rn(both(step * x), make_float2(b[2 * i], b[2 * i + 1])));
-            y += h[i].x * cc[2 * i] + h[i].y * cc[2 * i + 1];
+            h[i] = __ffma2_rn(decay<T>(both(step), a2[i]), h[i],
+                              __fmul2_rn(both(step * x), make_float2(b[2 * i], b[2 * i + 1])));
+            dot = __ffma2_rn(make_float2(cc[2 * i], cc[2 * i + 1]), h[i], dot);
         }
         store_states(a.out, row, S, 4 * s, in, h);
+        float y = dot.x + dot.y;
 #pragma unroll
         for (int o = LP / 2; o > 0; o /= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (in && s == 0) {
-            if (a.in.skip) y = fmaf(a.in.skip[ch], x, y);
-            if (a.in.z) {
-                const float z = to_f(((const T *)a.in.z)[row]);
-                y *= z * logistic<T>(z);
-            }
-            from_f((T *)a.y + row, y);
-        }
+        if (!in || s != 0) continue;
+        y = fmaf(skip, x, y);
+        if (a.in.z) y *= z * logistic<T>(z);
+        from_f((T *)a.y + row, y);
     }
 }
 
@@ -923,9 +928,13 @@ int lanes_of(int S, int states) {
     while (states * lp < S) lp *= 2;
     return lp;
 }
+// Of the forward pass two at least: alone with eight states or fewer a lane has so much to do for its own
+// tokens that they hold the walk up (8 x 2048 x 4096 x 8 bf16 533 us, with two 453).
+int fwd_lanes(int S) { return std::max(2, lanes_of(S, kStates)); }
 template <int MOST, typename F>
 auto by_lanes(int lp, F f) {
-    if (lp == 1) return f(std::integral_constant<int, 1>());
+    if constexpr (MOST > 8)
+        if (lp == 1) return f(std::integral_constant<int, 1>());
     if (lp == 2) return f(std::integral_constant<int, 2>());
     if (lp == 4) return f(std::integral_constant<int, 4>());
     if (lp == 8 || MOST == 8) return f(std::integral_constant<int, 8>());
@@ -968,13 +977,15 @@ Cut cut_of(const int32_t *cu, int B, int T, int N, int part) {
     return c;
 }
 
-// Tokens of a part of the forward pass, T + 1 for sequences left whole.  Parts (of 128 tokens at least)
-// pay, with their second walk, where whole sequences leave a third of the SMs without a CTA.
+// Tokens of a part of the forward pass, T + 1 for sequences left whole.  Parts, of 32 tokens at least,
+// pay, with their second walk and two launches, from sequences of 192 tokens on where whole ones are no
+// more than a CTA to an SM, which waits for its own arithmetic.  Us whole | in parts, 16 states gated bf16:
+// 8 x 2048 x 2048 360 | 321, 2 x 400 x 4096 72 | 41, 2 x 200 x 4096 37 | 31, 2 x 1000 x 1024 175 | 31.
 int fwd_part(int B, int T, int D, int S, int N, bool packed) {
-    const int lp = lanes_of(S, kStates), ch = 2 * kFwdThreads / lp;
+    const int lp = fwd_lanes(S), ch = 2 * kFwdThreads / lp;
     const long long n = packed ? N : B, ctas = n * ((D + ch - 1) / ch), mean = packed ? T / n : T;
-    const long long fill = 4 * kSms / std::max(1ll, ctas), parts = std::min(fill, mean / 128);
-    if (fill < 6 || parts < 3) return T + 1;
+    const long long fill = 4 * kSms / std::max(1ll, ctas), parts = std::min(fill, mean / 32);
+    if (fill < 4 || mean < 192) return T + 1;
     return (int)((mean + parts - 1) / parts + 7) / 8 * 8;
 }
 
@@ -1021,7 +1032,7 @@ template <int MODE>
 cudaError_t launch_fwd(const char *name, FwdArgs f, int dtype, cudaStream_t q) {
     return by_type(dtype, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        return by_lanes<8>(lanes_of(f.in.S, kStates), [&](auto lp) {
+        return by_lanes<8>(fwd_lanes(f.in.S), [&](auto lp) {
             return by_alignment(f.in.D % 2 == 0, [&](auto vect) {
                 constexpr int LP = decltype(lp)::value;
                 auto k = fwd_kernel<T, LP, decltype(vect)::value, MODE>;
@@ -1212,9 +1223,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_step_args *a, void *stream) {
         using T = std::remove_pointer_t<decltype(t)>;
         return ssm::by_lanes<16>(ssm::lanes_of(a->S, 4), [&](auto lp) {
             constexpr int LP = decltype(lp)::value, rows = ssm::kThreads / LP;
-            const long long ctas = ((long long)a->N * a->D + rows - 1) / rows;
-            return launch_pdl(ssm::step_kernel<T, LP>, dim3((unsigned)std::min<long long>(ctas, 16ll * dev.sms)),
-                              dim3(ssm::kThreads), 0, q, s);
+            const int across = (a->D + rows - 1) / rows, down = std::min(a->N, std::max(1, 16 * dev.sms / across));
+            return launch_pdl(ssm::step_kernel<T, LP>, dim3(across, down), dim3(ssm::kThreads), 0, q, s);
         });
     });
     prof_after(q);
