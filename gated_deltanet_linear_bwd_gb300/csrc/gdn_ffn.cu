@@ -9,35 +9,17 @@
 //
 // Sums are fp32 in TMEM.  h, dg and du pass to the next product as bf16, the tensor cores' operand
 // type: each is rounded once, by 2^-8 of itself at most.  Such roundings are of either sign, so that a
-// sum of products with them is off by about as much as its own rounding to bf16 is.
+// sum of products with them is off by about as much as its own rounding to bf16 is.  Of few tokens,
+// where there are few to average over, they pass whole.
 #include <algorithm>
 
 #include "gdn_layer_internal.h"
-#include "gdn_vec.cuh"
+#include "gdn_ffn.cuh"
 #include "tc_bf16_ptx.cuh"
 
 namespace gdn {
 namespace ffn {
 namespace {
-
-// The activation f(g) and its derivative; gelu is its tanh form, g logistic(2 c (g + 0.044715 g^3))
-// with c = sqrt(2 / pi).
-constexpr float kGelu2c = 1.5957691216057308f, kGeluCube = 0.044715f;
-template <bool GELU>
-__device__ __forceinline__ float activation(float g) {
-    return g * logistic<__nv_bfloat16>(GELU ? kGelu2c * g * fmaf(kGeluCube, g * g, 1.f) : g);
-}
-template <bool GELU>
-__device__ __forceinline__ float activation(float g, float &slope) {
-    if (!GELU) {
-        const float s = logistic<__nv_bfloat16>(g);
-        slope = silu_slope(g, s);
-        return g * s;
-    }
-    const float g2 = g * g, s = logistic<__nv_bfloat16>(kGelu2c * g * fmaf(kGeluCube, g2, 1.f));
-    slope = fmaf(g * s * (1.f - s), kGelu2c * fmaf(3.f * kGeluCube, g2, 1.f), s);
-    return g * s;
-}
 
 // ------------------------------------------------------------------ CTA pairs
 // Tiles of 256 x 256 by two CTAs (cta_group::2), persistent over the tiles of up to three products;
@@ -445,6 +427,8 @@ struct FewArgs {
     int early_w;                                     // the kernel ahead began when all before it had ended, the weight's
                                                      // writers among them
     int gelu;
+    int low;                                         // rows of C between its high parts and its low ones; not GATED: rows of
+                                                     // tokens between those; 0 = no low parts
     int *status;
     long long spin_limit;
 };
@@ -574,11 +558,18 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     tc::tc_fence_after();
     if (ok) {
         const uint32_t base = tc::smem_u32(out);
-        const int step = splits * (kFewThreads / 32), rows = min(a.nt, a.tokens - t0);
+        const int step = splits * (kFewThreads / 32), rows = min(a.nt, GATED || !a.low ? a.tokens - t0 : a.low);
         for (int j = rank * (kFewThreads / 32) + warp; j < rows; j += step) {
             const int at = j * 128 + 4 * lane;
             float4 v;
-            if (splits == 1) {
+            if (!GATED && a.low) {                   // of one tile of tokens: high and low parts
+                v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int r = 0; r < 2 * splits; ++r) {
+                    const uint32_t from = base + 4u * (uint32_t)(at + (r & 1) * a.low * 128);
+                    const float4 p = tc::ld_cluster4(tc::map_rank(from, r / 2));
+                    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+                }
+            } else if (splits == 1) {
                 v = *reinterpret_cast<const float4 *>(out + at);
             } else {
                 float4 p[kMaxSplits];
@@ -606,7 +597,14 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                 const float u = __shfl_down_sync(0xffffffffu, x[i], 16);
                 x[i] = u * (a.gelu ? activation<true>(x[i]) : activation<false>(x[i]));
             }
-            if (lane < 16 && in) tc::st4(a.c + row + f, x);
+            if (lane < 16 && in) {
+                tc::st4(a.c + row + f, x);
+                if (a.low) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] -= __bfloat162float(__float2bfloat16_rn(x[i]));
+                    tc::st4(a.c + row + (long long)a.low * a.cols + f, x);
+                }
+            }
         }
     }
     if (splits > 1) tc::cluster_sync();              // the others have read this CTA's tile
@@ -631,7 +629,7 @@ bool few_fits(const Product &p, bool gated, int sms) {
 }
 
 template <bool GATED>
-gdn_status run_few(const char *name, const Product &p, int gelu, bool early_w, const LayerDevice &dev, cudaStream_t q) {
+gdn_status run_few(const char *name, const Product &p, int gelu, int low, bool early_w, const LayerDevice &dev, cudaStream_t q) {
     FewMaps maps = {};
     FewArgs g{};
     g.c = (__nv_bfloat16 *)p.c[0];
@@ -644,6 +642,7 @@ gdn_status run_few(const char *name, const Product &p, int gelu, bool early_w, c
     g.stage_bytes = 16384 + g.nt * 128;
     g.early_w = early_w;
     g.gelu = gelu;
+    g.low = low;
     g.status = dev.status;
     g.spin_limit = dev.spin_limit;
     // The CTAs of a cluster share the contraction, by powers of two, while slots of the GPU are empty:
@@ -708,7 +707,7 @@ size_t gdn_ffn_fwd_workspace_size(const gdn_ffn_fwd_args *a) {
         return 0;
     }
     if (ffn::check(a->M, a->K, a->F, a->dtype, a->activation) != GDN_OK) return 0;
-    return a->M == 0 ? 256 : std::max<size_t>(512, ffn::hidden_bytes(a->M, a->F));
+    return a->M == 0 ? 256 : std::max<size_t>(512, ffn::hidden_bytes(a->M <= ffn::kLowTokens ? 2 * a->M : a->M, a->F));
 }
 
 gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -730,12 +729,14 @@ gdn_status gdn_ffn_fwd(const gdn_ffn_fwd_args *a, void *ws, size_t ws_bytes, voi
     g.save = a->gate != nullptr;
     g.gelu = a->activation == GDN_ACT_GELU;
     const ffn::Product up{a->x, a->w_gate, a->w_up, nullptr, {ws, a->gate, a->up}, a->M, a->F, a->K};
-    const ffn::Product down{ws, a->w_down, nullptr, nullptr, {a->y}, a->M, a->K, a->F};
+    // of few tokens h is two rows, what bf16 holds of it and of the rest: tokens to the second product
+    const int low = a->M <= ffn::kLowTokens ? a->M : 0;
+    const ffn::Product down{ws, a->w_down, nullptr, nullptr, {a->y}, a->M + low, a->K, a->F};
     const bool few = ffn::few_fits(up, true, dev.sms);
-    st = few ? ffn::run_few<true>("ffn_gated_few", up, g.gelu, false, dev, q)
+    st = few ? ffn::run_few<true>("ffn_gated_few", up, g.gelu, low, false, dev, q)
              : ffn::run_pair<ffn::kGated>("ffn_gated", &up, 1, g, dev, q);
     if (st != GDN_OK) return st;
-    return ffn::few_fits(down, false, dev.sms) ? ffn::run_few<false>("ffn_down_few", down, 0, few, dev, q)
+    return ffn::few_fits(down, false, dev.sms) ? ffn::run_few<false>("ffn_down_few", down, 0, low, few, dev, q)
                                         : ffn::run_pair_any<ffn::kDown>("ffn_down", down, g, dev, q);
 }
 
@@ -745,7 +746,9 @@ size_t gdn_ffn_bwd_workspace_size(const gdn_ffn_bwd_args *a) {
         return 0;
     }
     if (ffn::check(a->M, a->K, a->F, a->dtype, a->activation) != GDN_OK) return 0;
-    return a->M == 0 ? 256 : std::max<size_t>(512, 3 * ffn::hidden_bytes(a->M, a->F));
+    if (a->M == 0) return 256;
+    return std::max<size_t>(512, ffn::few_bwd_fits(a->M, a->K, a->F) ? ffn::few_bwd_bytes(a->M, a->K, a->F)
+                                                                     : 3 * ffn::hidden_bytes(a->M, a->F));
 }
 
 gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *a, void *ws, size_t ws_bytes, void *stream) {
@@ -771,6 +774,10 @@ gdn_status gdn_ffn_bwd(const gdn_ffn_bwd_args *a, void *ws, size_t ws_bytes, voi
         if (e == cudaSuccess) e = cudaMemsetAsync(a->dw_up, 0, bytes, q);
         if (e == cudaSuccess) e = cudaMemsetAsync(a->dw_down, 0, bytes, q);
         return e == cudaSuccess ? GDN_OK : cuda_fail(e, "clearing the weights' gradients");
+    }
+    if (ffn::few_bwd_fits(a->M, a->K, a->F)) {
+        const cudaError_t e = ffn::few_bwd(a, (float *)ws, q);
+        return e == cudaSuccess ? GDN_OK : cuda_fail(e, "feed-forward backward launch");
     }
     uint8_t *dg = (uint8_t *)ws, *du = dg + ffn::hidden_bytes(a->M, a->F), *h = du + ffn::hidden_bytes(a->M, a->F);
     ffn::PairArgs g{};

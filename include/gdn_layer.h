@@ -336,7 +336,7 @@ gdn_status gdn_ssm_step(const gdn_ssm_step_args *args, void *stream);
  *     g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T
  *
  * act is silu, or gelu in its tanh form.  bf16 tensors, fp32 sums; h is rounded to bf16 between the
- * products.  K and F are multiples of 8. */
+ * products (of up to 64 tokens to twice its bits).  K and F are multiples of 8. */
 typedef struct gdn_ffn_fwd_args {
     const void *x;              /* [M, K], dtype                                     */
     const void *w_gate, *w_up;  /* [F, K], dtype                                     */
@@ -351,7 +351,7 @@ typedef struct gdn_ffn_fwd_args {
 
 /* Backward, dh = dy w_down:  dg = dh u act'(g), du = dh act(g);  dx = dg w_gate + du w_up;
  * dw_gate = dg^T x, dw_up = du^T x, dw_down = dy^T h (h from gate and up once more).  dg, du and h
- * are rounded to bf16 between the products. */
+ * are rounded to bf16 between the products (of up to 8 tokens not at all). */
 typedef struct gdn_ffn_bwd_args {
     const void *d_y;            /* [M, K], dtype                                     */
     const void *x, *w_gate, *w_up, *w_down;                        /* the forward's  */

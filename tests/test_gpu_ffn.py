@@ -14,6 +14,11 @@ HALF = HALF_STEP[BF]
 ADD, ARITH = 2.0 ** -22, 2.0 ** -18
 
 
+def between(M, few):
+    """What h, dg and du lose between the products: a rounding to bf16, or of few tokens at most two of them's."""
+    return HALF if M > few else HALF * HALF
+
+
 def make(M, K, F, seed=0, dtype=BF):
     gen = torch.Generator().manual_seed(seed)
     r = lambda *s: torch.randn(*s, generator=gen)
@@ -51,7 +56,7 @@ def check_forward(p, name, y, gate, up):
     h = f * u
     # the activation is off by eg times a slope of 1.13 at most
     eh = 1.13 * eg * (u.abs() + eu) + f.abs() * eu + ARITH * h.abs() + ARITH * 2.0 ** -6
-    eh = eh + HALF * (h.abs() + eh)
+    eh = eh + between(x.shape[0], 64) * (h.abs() + eh)
     want = h @ wd.T
     ey = eh @ wd.abs().T + F * ADD * ((h.abs() + eh) @ wd.abs().T)
     inside("y", y, want, ey + HALF * (want.abs() + ey))
@@ -70,7 +75,7 @@ def check_backward(p, name, out):
     edg = edh * u.abs() * 1.13 + ARITH * (dh.abs() + edh) * u.abs() * (1 + g.abs())
     edu = edh * f.abs() + ARITH * (dh.abs() + edh) * (f.abs() + 2.0 ** -6)
     eh = ARITH * (h.abs() + 2.0 ** -6 * u.abs())
-    edg, edu, eh = (e + HALF * (v.abs() + e) for e, v in ((edg, dg), (edu, du), (eh, h)))
+    edg, edu, eh = (e + between(M, 8) * (v.abs() + e) for e, v in ((edg, dg), (edu, du), (eh, h)))
     a = lambda t: t.abs()
     want = (dg @ wg + du @ wu, dg.T @ x, du.T @ x, dy.T @ h)
     size = (a(dg) @ a(wg) + a(du) @ a(wu), a(dg).T @ a(x), a(du).T @ a(x), a(dy).T @ a(h))
@@ -82,7 +87,7 @@ def check_backward(p, name, out):
             close(k, got, w)
 
 
-CASES = [(1, 8, 8, "silu"), (3, 64, 128, "gelu"), (7, 72, 136, "silu"), (16, 512, 264, "silu"), (33, 200, 520, "gelu"),
+CASES = [(64, 520, 64, "gelu"), (65, 136, 200, "silu"), (8, 1200, 1032, "silu"), (9, 1200, 1032, "gelu"), (5, 2056, 136, "gelu"), (1, 8, 8, "silu"), (3, 64, 128, "gelu"), (7, 72, 136, "silu"), (16, 512, 264, "silu"), (33, 200, 520, "gelu"),
          (128, 128, 256, "silu"), (129, 264, 64, "gelu"), (257, 72, 392, "silu"), (300, 520, 1000, "silu"),
          (700, 256, 2048, "gelu"), (1, 1024, 4096, "silu"), (2500, 64, 72, "silu"),
          # wide enough for pairs of CTAs, into the block and out of it
@@ -235,7 +240,7 @@ def test_captured_and_on_another_stream(M):
     assert all(torch.equal(g, w) for g, w in zip(got, everything()))
 
 
-@pytest.mark.parametrize("M", [5, 600])
+@pytest.mark.parametrize("M", [5, 20, 600])
 def test_waits_that_give_up_are_reported(M):
     """With a limit of no polls every wait gives up at once: the call returns, the status says so, and
     the next calls are whole again."""
@@ -248,7 +253,7 @@ def test_waits_that_give_up_are_reported(M):
         gdn.gated_feed_forward_fwd(*args, save=True)
         assert gdn.gdn_sync_status(0) == 5
         gdn.gated_feed_forward_bwd(*back)
-        assert gdn.gdn_sync_status(0) == 5
+        assert gdn.gdn_sync_status(0) == (5 if M > 8 else 0)      # of so few tokens it has no waits
     finally:
         gdn.gdn_set_spin_limit(-1)
     y, gate, up = gdn.gated_feed_forward_fwd(*args, save=True)
