@@ -473,21 +473,19 @@ __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
             store2<T, PAIRS>((T *)a.y + base + (long long)(own + j) * D, in1, y);
         }
     };
-    // the next group's steps under this one's walk; a group's are read behind a __syncwarp
-    Gates g0, g1;
-    own_tokens(0, 0, g0);
-    __syncwarp();
+    // a group's steps are read behind a __syncwarp, and the next group's are put elsewhere
+    Gates g;
     for (int k = 0; k < blocks; ++k) {
         const float4 *bt = m.b[k & 1] + s, *ct = m.c[k & 1] + s;
         const int t0 = k * L::TB, t1 = min(t0 + L::TB, len);
 #pragma unroll 1
         for (int t = t0; t < t1; t += 2 * U, bt += U * L::SP / 2, ct += U * L::SP / 2) {
-            own_tokens(1, t + U, g1);
-            walk(0, t, g0, bt, ct);
+            own_tokens(0, t, g);
             __syncwarp();
-            own_tokens(0, t + 2 * U, g0);
-            walk(1, t + U, g1, bt + U * L::SP / 4, ct + U * L::SP / 4);
+            walk(0, t, g, bt, ct);
+            own_tokens(1, t + U, g);
             __syncwarp();
+            walk(1, t + U, g, bt + U * L::SP / 4, ct + U * L::SP / 4);
         }
         if (k + 1 < blocks) {
             put(k + 1);
