@@ -85,10 +85,7 @@ __device__ __forceinline__ bool part_of(const Cut &c, int slot, Part &p) {
             else hi = mid - 1;
         }
         p.n = lo;
-        if (!seq_tokens(c.s, lo, bos, len)) {
-            if (threadIdx.x == 0) set_status(c.status, GDN_ERR_BAD_SEQLENS);
-            return false;
-        }
+        if (!seq_tokens(c.s, lo, bos, len)) return false;
         off = (slot - bos / c.part - lo) * c.part;
     }
     if (off < 0 || (off > 0 && off >= len)) return false;
@@ -331,6 +328,11 @@ __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
     extern __shared__ __align__(16) uint8_t shared[];
     typename L::Shared &m = *reinterpret_cast<typename L::Shared *>(shared);
     pdl_wait();
+    if (blockIdx.x == 0 && a.cut.s.cu)             // of impossible ranges some may have no slot
+        for (int n = threadIdx.x; n < a.cut.s.N; n += kFwdThreads) {
+            long long bos, len;
+            if (!seq_tokens(a.cut.s, n, bos, len)) set_status(a.cut.status, GDN_ERR_BAD_SEQLENS);
+        }
 
     const int group = blockIdx.x % a.in.groups;
     int slot = blockIdx.x / a.in.groups;

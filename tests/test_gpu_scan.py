@@ -219,7 +219,7 @@ def test_a_nan_stays_in_its_channel_and_behind_its_token():
     assert torch.isnan(ht[0, 3]).all() and int(torch.isnan(ht).sum()) == 16
 
 
-@pytest.mark.parametrize("cu", [[0, 5, 3, 40], [1, 20, 40], [0, 20, 39], [0, -7, 40], [0, 20, 2 ** 31 - 1]])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 40], [1, 20, 40], [0, 20, 39], [0, -7, 40], [0, 20, 2 ** 31 - 1], [0, 40, 40, 20, 40]])
 def test_impossible_sequences_are_reported(cu):
     gdn = lib()
     m = make(BF, 1, 40, 16, 16)
