@@ -238,8 +238,13 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                         tc::st_row64(block, lane, u);
                         out.send(&maps.c[2], block, col, row, in, lane);
                     }
+                    if (a.gelu) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) u[i] *= a.gelu ? activation<true>(g[i]) : activation<false>(g[i]);
+                        for (int i = 0; i < 64; ++i) u[i] *= activation<true>(g[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) u[i] *= activation<false>(g[i]);
+                    }
                     uint8_t *block = out.next(lane);
                     tc::st_row64(block, lane, u);
                     out.send(&maps.c[0], block, col, row, in, lane);
@@ -253,32 +258,36 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
                     there = __all_sync(0xffffffffu, tc::mbar_wait(&ctl.in[quarter], had & 1, a.spin_limit, a.status));
                     if (!there) break;
                     ++had;
+                    const auto slopes = [&](auto gelu) {
 #pragma unroll
-                    for (int b = 0; b < 64; b += 32) {
-                        float v[32];
-                        tc::tmem_ld32(tc::tmem_addr(acc, quarter, c + b), v);
+                        for (int b = 0; b < 64; b += 32) {
+                            float v[32];
+                            tc::tmem_ld32(tc::tmem_addr(acc, quarter, c + b), v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            const uint32_t off = tc::sw128_off(lane, b + i);
-                            uint4 *pg = reinterpret_cast<uint4 *>(gate + off), *pu = reinterpret_cast<uint4 *>(up + off);
-                            const uint4 gr = *pg, ur = *pu;
-                            const __nv_bfloat16 *gs = reinterpret_cast<const __nv_bfloat16 *>(&gr);
-                            const __nv_bfloat16 *us = reinterpret_cast<const __nv_bfloat16 *>(&ur);
-                            float dg[8], du[8], h[8];
+                            for (int i = 0; i < 32; i += 8) {
+                                const uint32_t off = tc::sw128_off(lane, b + i);
+                                uint4 *pg = reinterpret_cast<uint4 *>(gate + off), *pu = reinterpret_cast<uint4 *>(up + off);
+                                const uint4 gr = *pg, ur = *pu;
+                                const __nv_bfloat16 *gs = reinterpret_cast<const __nv_bfloat16 *>(&gr);
+                                const __nv_bfloat16 *us = reinterpret_cast<const __nv_bfloat16 *>(&ur);
+                                float dg[8], du[8], h[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float g = to_f(gs[j]), u = to_f(us[j]);
-                                float slope;
-                                const float f = a.gelu ? activation<true>(g, slope) : activation<false>(g, slope);
-                                dg[j] = v[i + j] * u * slope;
-                                du[j] = v[i + j] * f;
-                                h[j] = f * u;
+                                for (int j = 0; j < 8; ++j) {
+                                    const float g = to_f(gs[j]), u = to_f(us[j]);
+                                    float slope;
+                                    const float f = activation<decltype(gelu)::value>(g, slope);
+                                    dg[j] = v[i + j] * u * slope;
+                                    du[j] = v[i + j] * f;
+                                    h[j] = f * u;
+                                }
+                                Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pg), dg);
+                                Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pu), du);
+                                Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(hidden + off), h);
                             }
-                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pg), dg);
-                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(pu), du);
-                            Vec<__nv_bfloat16, 8>::store(reinterpret_cast<__nv_bfloat16 *>(hidden + off), h);
                         }
-                    }
+                    };
+                    if (a.gelu) slopes(std::true_type());
+                    else slopes(std::false_type());
                     if (c == 192) {                  // the accumulator is free
                         tc::tc_fence_before();
                         __syncwarp();
