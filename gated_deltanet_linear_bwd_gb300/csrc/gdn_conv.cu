@@ -7,7 +7,7 @@
 // registers, so that each input is read once (and W - 1 more for each run).  The tokens are taken
 // as one long row: where a sequence begins, the registers are filled from its initial state.
 // Bound by memory: 16 x (512 .. 8192) tokens x 4096 bf16 forward 176 us, 97% of the measured copy
-// rate; 4 x 4096 x 4096 backward 97 us, 62%.
+// rate; 4 x 4096 x 4096 backward 94 us, 64%, its issue slots as busy as the memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -50,7 +50,8 @@ __device__ __forceinline__ void clear(float2 (&v)[P]) {
 }
 // A thread's own loads, GROUPS groups of kAhead tokens of N tensors in flight, by cp.async to shared
 // memory: in registers there is no room for enough of them (16 x (512 .. 8192) x 4096 bf16 forward 200
-// us from registers, 176 so; backward of 4 x 4096 x 4096 110, 97).  Only the thread that asked reads them, so that no barrier is needed.
+// us from registers, 176 so; backward of 4 x 4096 x 4096 110, 97).  Only the thread that asked reads
+// them, so that no barrier is needed.
 constexpr int kAhead = 4;
 template <typename T, int VEC, int N, int GROUPS>
 struct Ahead {
@@ -101,7 +102,7 @@ struct FwdArgs {
     const void *x, *w, *bias, *h0;
     void *y, *ht;
     Seqs s;
-    int tokens, D, run, runs;      // tokens of a run, runs; the items behind them write final states
+    int tokens, D, run, runs;      // tokens of a run, runs; the items ahead of them write final states
     int *status;
 };
 

@@ -49,7 +49,7 @@ struct Maps {
     CUtensorMap a[kProducts], b[kProducts], c[kProducts];    // kSlopes: a[1] gate, a[2] up
 };
 struct PairArgs {
-    int rows, m_tiles[kProducts], n_tiles[kProducts], first[kProducts + 1];   // tiles of the products
+    int m_tiles[kProducts], n_tiles[kProducts], first[kProducts + 1];   // tiles of the products
     int cols[kProducts];                             // of C (kGated: features)
     int kblocks, parts;                              // blocks of 64 of a part of the contraction; kInput has two
     int c_rows[kProducts];

@@ -67,7 +67,7 @@ struct Part {
     int n;
     long long first;                               // its first token
     int len;                                       // tokens, 0 only for an empty sequence
-    bool begins, ends;                             // the sequence
+    bool ends;                                     // the sequence
 };
 // False where no part has the slot.
 __device__ __forceinline__ bool part_of(const Cut &c, int slot, Part &p) {
@@ -91,7 +91,6 @@ __device__ __forceinline__ bool part_of(const Cut &c, int slot, Part &p) {
     if (off < 0 || (off > 0 && off >= len)) return false;
     p.first = bos + off;
     p.len = (int)min((long long)c.part, len - off);
-    p.begins = off == 0;
     p.ends = off + p.len == len;
     return true;
 }
