@@ -320,6 +320,16 @@ __device__ __forceinline__ void store_lane(float *base, long long row, int S, in
     }
 }
 
+// Reports impossible ranges, of which some may have no slot.  Not inlined: the walk behind it came out
+// with other registers, a tenth slower.
+__device__ __noinline__ void report_ranges(const int32_t *cu, long long T, int N, int *status) {
+    if (!cu) return;
+    for (int n = threadIdx.x; n < N; n += kFwdThreads) {
+        long long bos, len;
+        if (!seq_tokens({cu, T, N}, n, bos, len)) set_status(status, GDN_ERR_BAD_SEQLENS);
+    }
+}
+
 template <typename T, int LP, bool PAIRS, int MODE>
 __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
     using L = Lanes<T, LP>;
@@ -327,11 +337,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
     extern __shared__ __align__(16) uint8_t shared[];
     typename L::Shared &m = *reinterpret_cast<typename L::Shared *>(shared);
     pdl_wait();
-    if (blockIdx.x == 0 && a.cut.s.cu)             // of impossible ranges some may have no slot
-        for (int n = threadIdx.x; n < a.cut.s.N; n += kFwdThreads) {
-            long long bos, len;
-            if (!seq_tokens(a.cut.s, n, bos, len)) set_status(a.cut.status, GDN_ERR_BAD_SEQLENS);
-        }
+    if (blockIdx.x == 0) report_ranges(a.cut.s.cu, a.cut.s.T, a.cut.s.N, a.cut.status);
 
     const int group = blockIdx.x % a.in.groups;
     int slot = blockIdx.x / a.in.groups;
