@@ -608,9 +608,12 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             }
             if (lane < 16 && in) {
                 tc::st4(a.c + row + f, x);
-                if (a.low) {
+                if (a.low) {                         // nothing of a value that bf16 rounds to infinity
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] -= __bfloat162float(__float2bfloat16_rn(x[i]));
+                    for (int i = 0; i < 4; ++i) {
+                        const float high = __bfloat162float(__float2bfloat16_rn(x[i]));
+                        x[i] = isinf(high) ? 0.f : x[i] - high;
+                    }
                     tc::st4(a.c + row + (long long)a.low * a.cols + f, x);
                 }
             }
