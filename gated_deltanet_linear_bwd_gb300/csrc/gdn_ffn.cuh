@@ -22,7 +22,8 @@ __device__ __forceinline__ float activation(float g, float &slope) {
         slope = silu_slope(g, s);
         return g * s;
     }
-    const float g2 = g * g, s = logistic<__nv_bfloat16>(kGelu2c * g * fmaf(kGeluCube, g2, 1.f));
+    // past 2^60 the slope is 0 or 1 and g^2 might overflow, of which 0 times would be NaN
+    const float g2 = fminf(g * g, 0x1p120f), s = logistic<__nv_bfloat16>(kGelu2c * g * fmaf(kGeluCube, g2, 1.f));
     slope = fmaf(g * s * (1.f - s), kGelu2c * fmaf(3.f * kGeluCube, g2, 1.f), s);
     return g * s;
 }
