@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
                 g.gate[j] = mine(j, 2);
                 g.gate[j] = __fmul2_rn(g.gate[j], logistic2<T>(g.gate[j]));
             }
-            if (MODE == kOutputs) g.sx[j] = __fmul2_rn(skip, xi);
+            // without skip no product with x, which may be infinite
+            if (MODE == kOutputs) g.sx[j] = a.in.skip ? __fmul2_rn(skip, xi) : both(0.f);
             else m.ds[which][s * OWN + j][pair] = live ? __fmul2_rn(g.gate[j], mine(j, 3)) : both(0.f);
         }
         if (++taken == kAhead + 1) taken = 0;
@@ -819,14 +820,16 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
                 }
                 const long long at = base + (long long)t * D;
                 if (a.in.z) {
-                    const float2 z = get2(r[j].z), sg = logistic2<T>(z), y = __ffma2_rn(skip, x, hc);
+                    const float2 z = get2(r[j].z), sg = logistic2<T>(z), y = a.in.skip ? __ffma2_rn(skip, x, hc) : hc;
                     store2<T, PAIRS>((T *)a.dz + at, m1,
                                      __fmul2_rn(__fmul2_rn(dy, y), make_float2(silu_slope(z.x, sg.x), silu_slope(z.y, sg.y))));
                     ds = __fmul2_rn(dy, __fmul2_rn(z, sg));
                 }
                 const float2 eb = make_float2(sums.x, sums.y);
                 const float2 ddt = __fmul2_rn(slope, __ffma2_rn(x, eb, make_float2(sums.z, sums.w)));
-                store2<T, PAIRS>((T *)a.dx + at, m1, __ffma2_rn(skip, ds, __fmul2_rn(step, eb)));
+                float2 dx = __fmul2_rn(step, eb);
+                if (a.in.skip) dx = __ffma2_rn(skip, ds, dx);
+                store2<T, PAIRS>((T *)a.dx + at, m1, dx);
                 store2<T, PAIRS>((T *)a.ddt + at, m1, ddt);
                 gs = __ffma2_rn(ds, x, gs);
                 gbias = __fadd2_rn(gbias, ddt);
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
 #pragma unroll
         for (int o = LP / 2; o > 0; o /= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (!in || s != 0) continue;
-        y = fmaf(skip, x, y);
+        if (a.in.skip) y = fmaf(skip, x, y);
         if (a.in.z) y *= z * logistic<T>(z);
         from_f((T *)a.y + row, y);
     }

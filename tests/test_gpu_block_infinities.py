@@ -3,13 +3,13 @@ further than they reach."""
 import pytest
 import torch
 
-from block_ref import HALF_STEP, inside
+from block_ref import HALF_STEP, inside, scan
 from gpu_helpers import lib
 from test_gpu_ffn import ADD, gpu, make
 
 pytestmark = pytest.mark.gpu
 
-BF = torch.bfloat16
+BF, F = torch.bfloat16, torch.float32
 INF = float("inf")
 
 
@@ -53,3 +53,75 @@ def test_slopes_of_the_largest_projections(M, name):
     want = dg.T @ x
     e = edg.T @ x.abs() + M * ADD * ((dg.abs() + edg).T @ x.abs())
     inside("dw_gate", out[1], want, e + half * (want.abs() + e))
+
+
+# ------------------------------------------------------------------ scan
+def scan_inputs(dtype, T, D, S, skip, seed=0):
+    """Positive coefficients, so that an infinite state is +inf and their sum is too."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)
+    return dict(x=r(1, T, D).to(dtype), dt=(r(1, T, D) - 2).to(dtype), a=-torch.exp(r(D, S) - 2).float(),
+                b=(r(1, T, S).abs() + 0.1).to(dtype), c=(r(1, T, S).abs() + 0.1).to(dtype),
+                skip=(r(D).abs() + 0.1).float() if skip else None, z=r(1, T, D).to(dtype), dt_bias=r(D).float())
+
+
+def on_gpu(p):
+    return {k: None if t is None else t.cuda() for k, t in p.items()}
+
+
+def definition(p, h0, T):
+    flat = {k: None if t is None else t.double().reshape(-1, t.shape[-1]) if t.dim() == 3 else t.double()
+            for k, t in p.items()}
+    return scan(**flat, h0=h0.double(), seqs=[(0, T)])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("S", [16, 64])
+def test_an_infinite_input_without_skip(dtype, S):
+    """With no skip nothing but the states takes x: they and the outputs are infinite from its token on."""
+    gdn = lib()
+    T, D = 40, 6
+    p = scan_inputs(dtype, T, D, S, skip=False)
+    clean, _ = gdn.state_space_scan_fwd(**on_gpu(p))
+    p["x"][0, 7, 3], p["x"][0, 9, 4] = INF, -INF
+    y, ht = gdn.state_space_scan_fwd(**on_gpu(p))
+    want, state = definition(p, torch.zeros(1, D, S), T)
+    assert want[7:, 3].isinf().all() and want[9:, 4].isinf().all()
+    keep = want.isfinite()
+    assert torch.equal(y[0].cpu()[keep], clean[0].cpu()[keep])
+    assert torch.equal(y[0].cpu().double()[~keep], want[~keep])
+    assert torch.equal(ht.cpu().isinf(), state.isinf()) and not torch.isnan(ht).any()
+    # one token
+    h0 = torch.rand(1, D, S)
+    token = {k: t[:, 7].contiguous() if t is not None and t.dim() == 3 else t for k, t in p.items()}
+    h = h0.cuda()
+    y1 = gdn.state_space_step(state=h, **on_gpu(token))
+    one = {k: t[:, 7:8] if t is not None and t.dim() == 3 else t for k, t in p.items()}
+    want, state = definition(one, h0, 1)
+    assert want[0, 3].isinf() and torch.equal(y1.cpu().double().isinf(), want.isinf()) and not torch.isnan(y1).any()
+    assert torch.equal(h.cpu().isinf(), state.isinf()) and not torch.isnan(h).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_infinite_gradients_without_skip(dtype):
+    """Nor does skip come into dz, which is infinite where the states are, and dx, from an infinite dy's
+    token back."""
+    gdn = lib()
+    T, D, S = 40, 6, 16
+    p = scan_inputs(dtype, T, D, S, skip=False)
+    for k in ("b", "c", "z"):
+        p[k] = p[k].abs() + 0.1
+    dy = torch.ones(1, T, D, dtype=dtype)
+    clean = gdn.state_space_scan_bwd(dy.cuda(), **on_gpu(p))
+    p["x"][0, 7, 3] = INF
+    dz = gdn.state_space_scan_bwd(dy.cuda(), **on_gpu(p))[6][0].cpu()
+    bad = torch.zeros(T, D, dtype=torch.bool)
+    bad[7:, 3] = True
+    assert (dz[bad] == INF).all() and torch.equal(dz[~bad], clean[6][0].cpu()[~bad])
+    p["x"][0, 7, 3] = 1
+    clean = gdn.state_space_scan_bwd(dy.cuda(), **on_gpu(p))
+    dy[0, 7, 3] = INF
+    dx = gdn.state_space_scan_bwd(dy.cuda(), **on_gpu(p))[0][0].cpu()
+    bad[:] = False
+    bad[:8, 3] = True
+    assert (dx[bad] == INF).all() and torch.equal(dx[~bad], clean[0][0].cpu()[~bad])
