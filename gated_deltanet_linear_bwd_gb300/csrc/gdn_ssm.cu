@@ -105,21 +105,40 @@ __device__ __forceinline__ int parts_of(const Cut &c, int n, int &count) {
     return c.s.cu ? (int)(bos / c.part) + n : n * c.per;
 }
 
-// A lane's 2 P neighbouring states, from s0 on, of a row of a [.., D, S] tensor.
-template <int P>
+// The lanes of a channel have SP places for its S states.  Those past the last state hold copies of
+// real ones, whose c is shared out among a state's copies (by halves, which is exact): <c, h> stays the
+// same sum, and no place multiplies a zero by what may be infinite (an input, a step).  Fours of places
+// are fours of states where S is a multiple of four.
+struct Place {
+    int state;
+    float share;
+};
+template <int SP>
+__device__ __forceinline__ Place place_of(int i, int S) {
+    const int P = S > 1 ? 1 << (32 - __clz(S - 1)) : 1;      // the power of two from S on
+    const int s = i & (P - 1);
+    const bool copy = s >= S, copied = s < P / 2 && s + P / 2 >= S;
+    return {copy ? s - P / 2 : s, (copy || copied ? 0.5f : 1.f) * (float)P / SP};
+}
+
+// A lane's 2 P neighbouring states, from s0 on, of a row of a [.., D, S] tensor; past the last one copies
+// (COPIES), or zeros.
+template <int SP, bool COPIES, int P>
 __device__ __forceinline__ void load_states(const float *base, long long row, int S, int s0, bool in, float2 (&v)[P]) {
-    const float *p = base + row * S + s0;
+    const float *p = base + row * S;
     const bool there = base && in;
+    const auto at = [&](int i) { return COPIES ? place_of<SP>(s0 + i, S).state : s0 + i; };
+    const auto one = [&](int i) { return there && (COPIES || s0 + i < S) ? p[at(i)] : 0.f; };
 #pragma unroll
     for (int i = 0; i < P; i += 2) {
         if ((S & 3) == 0) {
-            const float4 f = there && s0 + 2 * i < S ? *reinterpret_cast<const float4 *>(p + 2 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 f = there && (COPIES || s0 + 2 * i < S) ? *reinterpret_cast<const float4 *>(p + at(2 * i))
+                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             v[i] = make_float2(f.x, f.y);
             v[i + 1] = make_float2(f.z, f.w);
         } else {
 #pragma unroll
-            for (int j = i; j < i + 2; ++j)
-                v[j] = make_float2(there && s0 + 2 * j < S ? p[2 * j] : 0.f, there && s0 + 2 * j + 1 < S ? p[2 * j + 1] : 0.f);
+            for (int j = i; j < i + 2; ++j) v[j] = make_float2(one(2 * j), one(2 * j + 1));
         }
     }
 }
@@ -236,26 +255,27 @@ __device__ __forceinline__ int longest(const Seqs &s, int j, int *scratch) {
     return n;
 }
 
-// b or c of a tile, [tokens][S] as [tokens][SP] with zeros behind, a few to a thread.
+// b or c of a tile, [tokens][S] as [tokens][SP], a few of a place to a thread.
 template <typename T, int TT, int SP, int THREADS>
 struct Coefficients {
     static constexpr int N = (TT * SP + THREADS - 1) / THREADS;
+    static_assert(THREADS % SP == 0, "a thread's are of one place");
     T v[N];                                        // converted only when they are put down: that waits for them
     // Tokens from `token` on, `live` of them (FULL: all of the tile's).
     template <bool FULL>
     __device__ __forceinline__ void fetch(const void *from, long long token, int live, int S) {
-        const T *p = (const T *)from + token * S;
+        const T *p = (const T *)from + token * S + place_of<SP>(threadIdx.x % SP, S).state;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int k = threadIdx.x + i * THREADS, t = k / SP, s = k % SP;
-            v[i] = (FULL ? N * THREADS == TT * SP || t < TT : t < live) && s < S ? p[t * S + s] : T(0.f);
+            const int t = (threadIdx.x + i * THREADS) / SP;
+            v[i] = (FULL ? N * THREADS == TT * SP || t < TT : t < live) ? p[t * S] : T(0.f);
         }
     }
-    template <typename F>
-    __device__ __forceinline__ void put(F put_one) const {
+    __device__ __forceinline__ void put(float4 *to, float share) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (N * THREADS == TT * SP || threadIdx.x + i * THREADS < TT * SP) put_one(threadIdx.x + i * THREADS, to_f(v[i]));
+            if (N * THREADS == TT * SP || threadIdx.x + i * THREADS < TT * SP)
+                reinterpret_cast<float *>(to)[threadIdx.x + i * THREADS] = to_f(v[i]) * share;
     }
 };
 
@@ -306,7 +326,7 @@ __device__ __forceinline__ void load_lane(const float *base, long long row, int 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float2 p[2];
-        load_states(base, row + (i & 1), S, 4 * (i / 2 * LP + s), i & 1 ? in1 : in0, p);
+        load_states<kStates * LP, true>(base, row + (i & 1), S, 4 * (i / 2 * LP + s), i & 1 ? in1 : in0, p);
         v[i & 1][i / 2 * 2] = p[0];
         v[i & 1][i / 2 * 2 + 1] = p[1];
     }
@@ -362,8 +382,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) fwd_kernel(FwdArgs a) {
         }
     };
     const auto put = [&](int k) {
-        nb.put([&](int i, float v) { reinterpret_cast<float *>(m.b[k & 1])[i] = v; });
-        if (MODE != kPairs) nc.put([&](int i, float v) { reinterpret_cast<float *>(m.c[k & 1])[i] = v; });
+        nb.put(m.b[k & 1], 1.f);
+        if (MODE != kPairs) nc.put(m.c[k & 1], MODE == kOutputs ? place_of<L::SP>(threadIdx.x % L::SP, S).share : 1.f);
     };
     // this lane's tokens of a group, OWN from t on; what lies past the end keeps what was there.
     // Pointers that move a group at a time: 631 -> 600 us against addresses from the token's number.
@@ -621,9 +641,9 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
     {
         Coefficients<T, kSegment, G::SP, G::NT> co;
         co.template fetch<false>(a.in.b, part.first, len, S);
-        co.put([&](int i, float v) { reinterpret_cast<float *>(m.b)[i] = v; });
+        co.put(m.b, 1.f);
         co.template fetch<false>(a.in.c, part.first, len, S);
-        co.put([&](int i, float v) { reinterpret_cast<float *>(m.c)[i] = v; });
+        co.put(m.c, tid % G::SP < S ? 1.f : 0.f);  // copies take no part in the gradients
     }
     for (int k = tid; k < kSegment * G::V; k += G::NT) m.acc[k] = 0.f;
 
@@ -672,9 +692,9 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
         const long long row = (long long)slot * D + ch;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            load_states(a.in.a, ch + c, S, 4 * s, ch + c < D, an[c]);
-            load_states(a.start, row + c, S, 4 * s, ch + c < D, hs[c]);
-            load_states(a.behind, row + c, S, 4 * s, ch + c < D, carry[c]);
+            load_states<G::SP, true>(a.in.a, ch + c, S, 4 * s, ch + c < D, an[c]);
+            load_states<G::SP, false>(a.start, row + c, S, 4 * s, ch + c < D, hs[c]);
+            load_states<G::SP, false>(a.behind, row + c, S, 4 * s, ch + c < D, carry[c]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 a2[c][i] = __fmul2_rn(an[c][i], both(kLog2e));
@@ -895,8 +915,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
     pdl_enter();
     const int D = a.in.D, S = a.in.S, s = threadIdx.x % LP, ch = blockIdx.x * (kThreads / LP) + threadIdx.x / LP;
     const bool in = ch < D;
+    constexpr int SP = 4 * LP;
     float2 a2[2];
-    load_states(a.in.a, ch, S, 4 * s, in, a2);
+    load_states<SP, false>(a.in.a, ch, S, 4 * s, in, a2);
     a2[0] = __fmul2_rn(a2[0], both(kLog2e));
     a2[1] = __fmul2_rn(a2[1], both(kLog2e));
     const float bias = a.in.dt_bias && in ? a.in.dt_bias[ch] : 0.f, skip = a.in.skip && in ? a.in.skip[ch] : 0.f;
@@ -912,7 +933,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
     for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
         const long long row = (long long)n * D + ch;
         float2 h[2];
-        load_states(a.state, row, S, 4 * s, in, h);
+        load_states<SP, false>(a.state, row, S, 4 * s, in, h);
         float b[4], cc[4], step = 0.f, x = 0.f, z = 0.f;
         coefficients(a.in.b, n, b);
         coefficients(a.in.c, n, cc);
@@ -927,7 +948,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepArgs a) {
         for (int i = 0; i < 2; ++i) {
             h[i] = __ffma2_rn(decay<T>(both(step), a2[i]), h[i],
                               __fmul2_rn(both(step * x), make_float2(b[2 * i], b[2 * i + 1])));
-            dot = __ffma2_rn(make_float2(cc[2 * i], cc[2 * i + 1]), h[i], dot);
+            // of states that there are not nothing counts, whatever the step and x
+            dot = __ffma2_rn(make_float2(cc[2 * i], cc[2 * i + 1]),
+                             make_float2(4 * s + 2 * i < S ? h[i].x : 0.f, 4 * s + 2 * i + 1 < S ? h[i].y : 0.f), dot);
         }
         store_states(a.out, row, S, 4 * s, in, h);
         float y = dot.x + dot.y;

@@ -3,7 +3,7 @@ further than they reach."""
 import pytest
 import torch
 
-from block_ref import HALF_STEP, inside, scan
+from block_ref import HALF_STEP, inside, scan, scan_magnitudes
 from gpu_helpers import lib
 from test_gpu_ffn import ADD, gpu, make
 
@@ -125,3 +125,36 @@ def test_infinite_gradients_without_skip(dtype):
     bad[:] = False
     bad[:8, 3] = True
     assert (dx[bad] == INF).all() and torch.equal(dx[~bad], clean[0][0].cpu()[~bad])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("S", [1, 2, 3, 5, 8, 17, 24, 33, 50])
+def test_infinities_with_any_number_of_states(dtype, S):
+    """The lanes of a channel have places for more states than these: nothing comes of those, also where an
+    input or a step (softplus of an infinite logit) is infinite; and the gradients are finite where the
+    definition's are."""
+    gdn = lib()
+    T, D = 42, 6
+    p = scan_inputs(dtype, T, D, S, skip=True)
+    p["x"][0, 7, 3], p["x"][0, 9, 4], p["dt"][0, 20, 1] = INF, -INF, INF
+    y, ht = gdn.state_space_scan_fwd(**on_gpu(p))
+    zeros = torch.zeros(1, D, S)
+    want, state = definition(p, zeros, T)
+    assert int(want.isinf().sum()) == 35 + 33 + 22 and not torch.isnan(want).any()
+    infinite = want.isinf()
+    assert torch.equal(y[0].cpu().isinf(), infinite) and not torch.isnan(y).any()
+    assert torch.equal(y[0].cpu().double()[infinite], want[infinite])
+    assert torch.equal(ht.cpu().double()[state.isinf()], state[state.isinf()]) and not torch.isnan(ht).any()
+    for t in (7, 9, 20):
+        token = {k: v[:, t].contiguous() if v.dim() == 3 else v for k, v in p.items()}
+        h = torch.ones(1, D, S).cuda()
+        y1 = gdn.state_space_step(state=h, **on_gpu(token))
+        want, state = definition({k: v[:, t:t + 1] if v.dim() == 3 else v for k, v in p.items()}, zeros + 1, 1)
+        assert torch.equal(y1.cpu().isinf(), want.isinf()) and not torch.isnan(y1).any()
+        assert torch.equal(h.cpu().isinf(), state.isinf()) and not torch.isnan(h).any()
+    dy, dht = torch.ones(1, T, D, dtype=dtype), torch.ones(1, D, S)
+    flat = {k: v.double().reshape(-1, v.shape[-1]) if v.dim() == 3 else v.double() for k, v in p.items()}
+    want = scan_magnitudes(**flat, h0=zeros.double(), dy=dy[0].double(), dht=dht.double(), seqs=[(0, T)], signed=True)
+    out = gdn.state_space_scan_bwd(dy.cuda(), dht=dht.cuda(), **on_gpu(p))
+    for k, t in zip(("dx", "ddt", "da", "db", "dc", "dskip", "dz", "ddt_bias", "dh0"), out):
+        assert torch.isfinite(t.reshape(want[k].shape).cpu()[want[k].isfinite()]).all(), k
