@@ -573,7 +573,9 @@ __global__ void __launch_bounds__(256) join_kernel(JoinArgs a) {
         for (int k = 0; k < kAhead; ++k)
             if (j + k < count) {
                 pairs[at(j + k) * states + i] = v;
-                v = fmaf(ex2(st[k] * a2), v, e[k]);
+                // a part's decay may underflow where no token's does: an infinite state stays one
+                const float decay = ex2(st[k] * a2);
+                v = decay == 0.f && isinf(v) ? v + e[k] : fmaf(decay, v, e[k]);
             }
     }
     if (back && a.dh0 && count > 0) a.dh0[n * states + i] = v;

@@ -158,3 +158,25 @@ def test_infinities_with_any_number_of_states(dtype, S):
     out = gdn.state_space_scan_bwd(dy.cuda(), dht=dht.cuda(), **on_gpu(p))
     for k, t in zip(("dx", "ddt", "da", "db", "dc", "dskip", "dz", "ddt_bias", "dh0"), out):
         assert torch.isfinite(t.reshape(want[k].shape).cpu()[want[k].isfinite()]).all(), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_an_infinite_state_of_a_sequence_cut_into_parts(dtype):
+    """A part's decay underflows (32 steps of 1.5 times a = -2 and less), which no token's does: the state
+    stays infinite to the end."""
+    gdn = lib()
+    T, D, S = 3000, 6, 5
+    p = scan_inputs(dtype, T, D, S, skip=True)
+    p["a"] = -2 - torch.rand(D, S, generator=torch.Generator().manual_seed(1))
+    p["dt"], p["dt_bias"] = torch.full((1, T, D), 1.5, dtype=dtype), None
+    n = gdn._abi_layer.ENTRIES["gdn_ssm_fwd"]
+    assert n.workspace_size(n.pack(*[0] * 10, 1, T, D, S, 1, 1 if dtype == BF else 0, 0, 0)) > 256
+    clean, ht0 = gdn.state_space_scan_fwd(**on_gpu(p))
+    p["x"][0, 500, 3], p["x"][0, 2, 4] = INF, -INF
+    y, ht = gdn.state_space_scan_fwd(**on_gpu(p))
+    want, state = definition(p, torch.zeros(1, D, S), T)
+    assert int(want.isinf().sum()) == 2500 + 2998 and int(state.isinf().sum()) == 2 * S
+    keep = want.isfinite()
+    assert torch.equal(y[0].cpu()[keep], clean[0].cpu()[keep]) and torch.equal(y[0].cpu().double()[~keep], want[~keep])
+    keep = state.isfinite()
+    assert torch.equal(ht.cpu()[keep], ht0.cpu()[keep]) and torch.equal(ht.cpu().double()[~keep], state[~keep])
