@@ -724,7 +724,9 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
                 for (int c = 0; c < 2; ++c) m.saved[q][c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
             }
         }
-        for (int q = subs - 1; q >= 0; --q) {
+        // TAIL: the sequence ends inside the sub-segment
+        const auto gradients = [&](int q, auto tail) {
+            constexpr bool TAIL = decltype(tail)::value;
             SubStates h = {{hs[0][0], hs[0][1]}, {hs[1][0], hs[1][1]}}, e[kSub], p[kSub];
             if (q > 0)
 #pragma unroll
@@ -746,6 +748,13 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
                         h[c][i] = __ffma2_rn(both(c ? du.w : du.z), i ? make_float2(b.z, b.w) : make_float2(b.x, b.y), p[k][c][i]);
                     }
             }
+            // past the last token nothing: an infinite state times the step there, 0, would be NaN in da
+            if (TAIL)
+#pragma unroll
+                for (int k = 1; k < kSub; ++k)
+                    if (q * kSub + k >= len)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) p[k][c][0] = p[k][c][1] = both(0.f);
             // <c, h>, <e, b> and <e a, p> of this lane's states, [token][channel]
             float hc[2 * kSub], eb[2 * kSub], ep[2 * kSub];
             float *red = &m.red[q & 1][warp][0][0];
@@ -818,7 +827,10 @@ __global__ void __launch_bounds__(Segment<LP>::NT, kBwdThreads / Segment<LP>::NT
                 for (int w = 0; w < G::WARPS; ++w) v += (&m.red[q & 1][w][0][0])[k];
                 m.acc[q * kSub * G::V + k] = v;
             }
-        }
+        };
+        int q = subs - 1;
+        if (len % kSub != 0) gradients(q--, std::true_type());
+        for (; q >= 0; --q) gradients(q, std::false_type());
 #pragma unroll
         for (int c = 0; c < 2; ++c) store_states(a.start, row + c, S, 4 * s, ch + c < D, da[c]);
         __syncthreads();                           // every channel's sums are there

@@ -180,3 +180,18 @@ def test_an_infinite_state_of_a_sequence_cut_into_parts(dtype):
     assert torch.equal(y[0].cpu()[keep], clean[0].cpu()[keep]) and torch.equal(y[0].cpu().double()[~keep], want[~keep])
     keep = state.isfinite()
     assert torch.equal(ht.cpu()[keep], ht0.cpu()[keep]) and torch.equal(ht.cpu().double()[~keep], state[~keep])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T", [1, 33, 42, 63])
+def test_the_last_input_infinite(dtype, T):
+    """Nothing comes after it: a's gradient, which takes the states before each token, stays finite."""
+    gdn = lib()
+    D, S = 6, 16
+    p = scan_inputs(dtype, T, D, S, skip=False)
+    dy, dht, h0 = torch.ones(1, T, D, dtype=dtype).cuda(), torch.ones(1, D, S).cuda(), torch.ones(1, D, S).cuda()
+    clean = gdn.state_space_scan_bwd(dy, dht=dht, initial_state=h0, **on_gpu(p))
+    p["x"][0, T - 1, 3] = INF
+    out = gdn.state_space_scan_bwd(dy, dht=dht, initial_state=h0, **on_gpu(p))
+    for k, i in (("dx", 0), ("da", 2), ("dh0", 8)):
+        assert torch.equal(out[i], clean[i]), k
