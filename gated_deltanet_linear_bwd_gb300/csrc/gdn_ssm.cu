@@ -37,10 +37,11 @@ constexpr int kSub = 4;                            // tokens whose decays it hol
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The decays 2^y.  What matters is a small error that leans neither way, as a slow state multiplies
-// thousands of decays near 1 together.  The hardware's exponential leans down by 0.5e-8 .. 3e-8 of
-// itself there: a constant added to y, free in the product's instruction, takes 1.2e-8 of that away
-// (a step of 0 still gives exactly 1).  fp32 tensors take for |y| < 1/32 the polynomial 1 + y q(y), q
-// through (2^y - 1) / y at the three Chebyshev points of -1/32 .. 1/32 (1.1e-7 of y).
+// thousands of decays near 1 together.  The hardware's exponential leans down by 0.5e-8 .. 3.3e-8 of
+// itself there, 1.8e-8 on average over steps spread by their logarithm: a constant added to y, free in
+// the product's instruction, takes 1.2e-8 of that away (a step of 0 still gives exactly 1).  fp32 tensors
+// take for |y| < 1/32 the polynomial 1 + y q(y), q through (2^y - 1) / y at the three Chebyshev points of
+// -1/32 .. 1/32 (1.1e-7 of y).
 template <typename T>
 __device__ __forceinline__ float2 decay(float2 step, float2 a2) {
     if (sizeof(T) == 2) {
