@@ -469,8 +469,6 @@ int vec_of(int D, int most) {
     return v;
 }
 
-constexpr int kSms = 152;          // of the GPU that the choices below are made for
-
 // Tokens of a run: as few as keep the GPU's threads (`threads` to an SM) in one wave, but enough that
 // the W - 1 inputs read before a run, and its weights, are little beside it.
 int run_of(long long tokens, int D, int vec, int threads, int least) {
@@ -557,11 +555,10 @@ cudaError_t run_step(const gdn_conv_step_args *a, int sms, cudaStream_t q) {
     });
 }
 
-// Channels to a thread: 8 bytes in the forward pass, 4 (fp32 8) in the backward pass, which holds some
-// 20 numbers for each, and up to 16 for single tokens.
+// Channels to a thread: 8 bytes in the forward pass and of single tokens, 4 (fp32 8) in the backward pass,
+// which holds some 20 numbers for each.
 int fwd_vec(int dtype, int D) { return vec_of(D, dtype == GDN_BF16 ? 4 : 2); }
 int bwd_vec(int D) { return vec_of(D, 2); }
-int step_vec(int dtype, int D) { return vec_of(D, dtype == GDN_BF16 ? 4 : 2); }
 
 int tokens_of(int B, int T) { return B * T; }
 
@@ -667,7 +664,7 @@ gdn_status gdn_conv_step(const gdn_conv_step_args *a, void *stream) {
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     cudaStream_t q = (cudaStream_t)stream;
     prof_before("conv_step", q);
-    const cudaError_t e = conv::by_type(a->dtype, conv::step_vec(a->dtype, a->D), [&](auto *t, auto v) {
+    const cudaError_t e = conv::by_type(a->dtype, conv::fwd_vec(a->dtype, a->D), [&](auto *t, auto v) {
         return conv::run_step<std::remove_pointer_t<decltype(t)>, decltype(v)::value>(a, dev.sms, q);
     });
     prof_after(q);

@@ -702,7 +702,7 @@ gdn_status check(int M, int K, int F, int dtype, int activation) {
         return fail(GDN_ERR_UNSUPPORTED, "activation %d is not GDN_ACT_SILU or GDN_ACT_GELU", activation);
     return GDN_OK;
 }
-// Bytes of `count` [M, F] tensors, each from a 256-byte boundary on.
+// Bytes of an [M, F] tensor, to the next one's 256-byte boundary.
 size_t hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
 
 }  // namespace

@@ -57,6 +57,10 @@ gdn_status mx_quantize(const gdn_mx_quantize_args *a, uint32_t *work, int words,
 // by one, stays an int.
 constexpr int kMaxExtent = (int)((1ll << 31) - (1 << 16));
 
+// SMs of the GPU that work is cut for where the size of a workspace depends on it: that is told without
+// a device.
+constexpr int kSms = 152;
+
 inline bool misaligned(const void *p) { return ((uintptr_t)p & 15u) != 0; }
 
 }  // namespace gdn

@@ -750,8 +750,6 @@ struct Tiles {
     static constexpr int kBwdWarps = 4, kBwdRows = kHalf ? 16 : 8, kBwdStages = 4;
 };
 
-constexpr int kSms = 152;          // of the GPU that the choices below are made for
-
 // CTAs that share a sequence: doubled while the grid leaves slots of the GPU (two
 // CTAs per SM) empty and the sequences have a tile for each; of a packed batch, whose
 // longest sequence may be the last to end, up to twice that (us of 16 x (512 .. 8192) tokens

@@ -1006,8 +1006,6 @@ auto by_alignment(bool whole, F f) {
     return whole ? f(std::true_type()) : f(std::false_type());
 }
 
-constexpr int kSms = 152;          // of the GPU that the choices below are made for
-
 gdn_status check(int B, int T, int D, int S, int N, int dtype, bool packed) {
     if (B < 1 || T < 0 || D < 1 || S < 1)
         return fail(GDN_ERR_INVALID_ARG, "bad sizes B=%d T=%d D=%d S=%d", B, T, D, S);
