@@ -3,9 +3,10 @@ further than they reach."""
 import pytest
 import torch
 
-from block_ref import HALF_STEP, inside, scan, scan_magnitudes
+from block_ref import HALF_STEP, convolution, inside, scan, scan_magnitudes
 from gpu_helpers import lib
 from test_gpu_ffn import ADD, gpu, make
+from test_gpu_scan import ONCE, TOKEN
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +196,70 @@ def test_the_last_input_infinite(dtype, T):
     out = gdn.state_space_scan_bwd(dy, dht=dht, initial_state=h0, **on_gpu(p))
     for k, i in (("dx", 0), ("da", 2), ("dh0", 8)):
         assert torch.equal(out[i], clean[i]), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("S", [5, 16])
+def test_masked_steps(dtype, S):
+    """A logit of -inf is a step of zero: the states pass such tokens as they are, whatever their finite x, and
+    the gradients are those of the sequence without them."""
+    gdn = lib()
+    T, D = 50, 10
+    p = scan_inputs(dtype, T, D, S, skip=True)
+    for k in ("b", "c"):
+        p[k] = p[k] - 0.5
+    masked = torch.zeros(T, dtype=torch.bool)
+    masked[[0, 3, 4, 5, 17, 31, 32, 48, 49]] = True
+    p["dt"][0, masked] = -INF
+    p["x"][0, masked] = 1e30
+    h0, dht = torch.ones(1, D, S).cuda(), torch.ones(1, D, S).cuda()
+    dy = torch.randn(1, T, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    dy[0, masked] = 0
+    few = {k: t[:, ~masked].contiguous() if t.dim() == 3 else t for k, t in p.items()}
+    y, ht = gdn.state_space_scan_fwd(initial_state=h0, **on_gpu(p))
+    y2, ht2 = gdn.state_space_scan_fwd(initial_state=h0, **on_gpu(few))
+    assert torch.equal(ht, ht2) and torch.equal(y[:, ~masked], y2) and torch.isfinite(y).all()
+    out = gdn.state_space_scan_bwd(dy.cuda(), dht=dht, initial_state=h0, **on_gpu(p))
+    assert not out[0][0, masked].any() and not out[1][0, masked].any()
+    flat = {k: t.double().reshape(-1, t.shape[-1]) if t.dim() == 3 else t.double() for k, t in few.items()}
+    want, size = (scan_magnitudes(**flat, h0=h0.cpu().double(), dy=dy[0, ~masked].double(), dht=dht.cpu().double(),
+                                  seqs=[(0, len(dy[0, ~masked]))], signed=signed) for signed in (True, False))
+    for k, g in zip(("dx", "ddt", "da", "db", "dc", "dskip", "dz", "ddt_bias", "dh0"), out):
+        g = g[:, ~masked] if g.dim() == 3 and k != "dh0" else g
+        # as test_gpu_scan's check: a result's rounding, and what its terms lose token by token
+        room = HALF_STEP[g.dtype] * want[k].abs() * (1 + ONCE) + (ONCE + TOKEN * (T + 1) + T * 2.0 ** -24) * size[k]
+        inside(k, g.reshape(want[k].shape), want[k], room)
+
+
+# ------------------------------------------------------------------ convolution
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("D", [7, 264])
+def test_an_infinity_stays_under_its_taps(dtype, silu, D):
+    gdn = lib()
+    gen = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=gen)
+    T, W, cu = 40, 4, torch.tensor([0, 9, 40], dtype=torch.int32).cuda()
+    x, w, b, dy = r(1, T, D).to(dtype), r(D, W).to(dtype), r(D).to(dtype), r(1, T, D).to(dtype).cuda()
+    act = "silu" if silu else None
+    run = lambda: (gdn.causal_convolution_fwd(x.cuda(), w.cuda(), b.cuda(), cu_seqlens=cu, activation=act),
+                   gdn.causal_convolution_bwd(dy, x.cuda(), w.cuda(), b.cuda(), cu_seqlens=cu, activation=act))
+    (y0, h0), (dx0, dw0, db0, dh0) = run()
+    x[0, 7, 3], x[0, 20, 5] = INF, -INF
+    (y1, h1), (dx1, dw1, db1, dh1) = run()
+    want, _, state = convolution(x[0].double(), w.double(), b.double(), torch.zeros(2, W - 1, D, dtype=torch.float64),
+                                 [(0, 9), (9, 40)], silu)
+    y0, y1, dx0, dx1 = (t[0].cpu() for t in (y0, y1, dx0, dx1))
+    keep = want.isfinite()
+    assert int((~keep).sum()) == 2 + 4 and torch.equal(y1[keep], y0[keep])
+    assert torch.equal(torch.isnan(y1), torch.isnan(want)) and torch.equal(y1[y1.isinf()].double(), want[want.isinf()])
+    assert torch.equal(h1.cpu().double(), state)
+    # dx of the tokens whose outputs the infinity reaches (with silu, whose slope there is NaN), and its channels'
+    # sums
+    reach = torch.zeros(T, D, dtype=torch.bool)
+    if silu:
+        reach[4:9, 3], reach[17:24, 5] = True, True
+    assert torch.equal(dx1[~reach], dx0[~reach]) and not torch.isfinite(dx1[reach]).any()
+    others = torch.tensor([d for d in range(D) if d not in (3, 5)])
+    assert torch.equal(dw1[others], dw0[others]) and torch.equal(db1[others], db0[others]) and torch.equal(dh1, dh0)
+    assert not torch.isfinite(dw1[5]).any()
