@@ -660,6 +660,8 @@ gdn_status gdn_conv_step(const gdn_conv_step_args *a, void *stream) {
     if (misaligned(a->x) || misaligned(a->weight) || misaligned(a->bias) || misaligned(a->state) ||
         misaligned(a->y) || misaligned(a->out_state))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    if (shifted(a->state, a->out_state, (size_t)a->N * (a->W - 1) * a->D * (a->dtype == GDN_BF16 ? 2 : 4)))
+        return fail(GDN_ERR_INVALID_ARG, "out_state overlaps state without being it");
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     cudaStream_t q = (cudaStream_t)stream;

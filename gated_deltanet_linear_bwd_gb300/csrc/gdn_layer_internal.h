@@ -62,5 +62,11 @@ constexpr int kMaxExtent = (int)((1ll << 31) - (1 << 16));
 constexpr int kSms = 152;
 
 inline bool misaligned(const void *p) { return ((uintptr_t)p & 15u) != 0; }
+// Two ranges of so many bytes that share some of them, and are not the same: a step's new states would
+// overwrite old ones that are still to be read.
+inline bool shifted(const void *a, const void *b, size_t bytes) {
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return p != q && (p < q ? q - p : p - q) < bytes;
+}
 
 }  // namespace gdn

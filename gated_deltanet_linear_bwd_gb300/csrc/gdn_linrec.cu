@@ -1024,6 +1024,8 @@ gdn_status gdn_linrec_step(const gdn_linrec_step_args *a, void *stream) {
     if (misaligned(a->x) || misaligned(a->g) || misaligned(a->gate_scale) || misaligned(a->state) ||
         misaligned(a->h) || misaligned(a->out_state))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    if (shifted(a->state, a->out_state, (size_t)a->N * a->D * 4))
+        return fail(GDN_ERR_INVALID_ARG, "out_state overlaps state without being it");
     LayerDevice dev;
     const gdn_status st = layer_device(&dev);
     if (st != GDN_OK) return st;

@@ -1268,6 +1268,8 @@ gdn_status gdn_ssm_step(const gdn_ssm_step_args *a, void *stream) {
         misaligned(a->skip) || misaligned(a->z) || misaligned(a->dt_bias) || misaligned(a->state) ||
         misaligned(a->y) || misaligned(a->out_state))
         return fail(GDN_ERR_INVALID_ARG, "every tensor must be 16-byte aligned");
+    if (shifted(a->state, a->out_state, (size_t)a->N * a->D * a->S * 4))
+        return fail(GDN_ERR_INVALID_ARG, "out_state overlaps state without being it");
     LayerDevice dev;
     if ((st = layer_device(&dev)) != GDN_OK) return st;
     cudaStream_t q = (cudaStream_t)stream;

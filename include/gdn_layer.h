@@ -69,7 +69,7 @@ typedef struct gdn_linrec_step_args {
     int32_t N, D;
     int32_t dtype;
     void *h;                    /* [N, D], dtype                                     */
-    float *out_state;           /* [N, D]: may be `state` itself                     */
+    float *out_state;           /* [N, D]: may be `state` itself, not part of it     */
 } gdn_linrec_step_args;
 
 /* Bytes of workspace for these arguments: 256 (then none is read, and it may be NULL) or
@@ -250,7 +250,8 @@ typedef struct gdn_conv_step_args {
     int32_t N, D, W;
     int32_t dtype, activation;
     void *y;                    /* [N, D], dtype                                     */
-    void *out_state;            /* [N, W - 1, D], dtype: may be `state` itself       */
+    void *out_state;            /* [N, W - 1, D], dtype: may be `state` itself, not
+                                   part of it                                        */
 } gdn_conv_step_args;
 gdn_status gdn_conv_step(const gdn_conv_step_args *args, void *stream);
 
@@ -318,7 +319,7 @@ typedef struct gdn_ssm_step_args {
     int32_t N, D, S;
     int32_t dtype;
     void *y;                    /* [N, D], dtype                                     */
-    float *out_state;           /* [N, D, S]: may be `state` itself                  */
+    float *out_state;           /* [N, D, S]: may be `state` itself, not part of it  */
 } gdn_ssm_step_args;
 
 /* Bytes of workspace, as gdn_linrec_fwd_workspace_size. */
