@@ -15,9 +15,11 @@
 // segments of 32 tokens, whose start states and end gradients one joined walk gives.
 //
 // A token and channel of 16 states is 16 exponentials and 64 multiply-adds (1.7 ps of the GPU's
-// either), and about 120 instructions in all (3.2 ps): bound by instruction issue, 61% busy.  Packed 16
-// x (256 .. 4096) tokens x 4096 gated bf16 600 us (4.2 ps), 32768 x 2048 in parts 533; 4 x 4096 x 2048
-// backward 1035, of which the segments' gradients are 746; the memory's floors are 172, 81 and 70.
+// either), and 122 instructions in all (3.2 ps): bound by instruction issue, 63% of whose slots the 16
+// warps of an SM fill.  Packed 16 x (256 .. 4096) tokens x 4096 gated bf16 600 us (4.2 ps), 32768 x 2048
+// in parts 538; 4 x 4096 x 2048 backward 1035, of which the segments' gradients (466 instructions) are
+// 744; the memory's floors are 172, 81 and 70.  Whether sequences are cut goes by their mean length: of
+// a packed batch of one of 32768 tokens and fifteen of 100, x 2048, all are walked whole (5.2 ms).
 #include <algorithm>
 #include <type_traits>
 
@@ -598,7 +600,7 @@ struct BwdArgs {
 
 // A lane has four states of two channels here, LP lanes a pair of channels: the decays and decayed
 // states of a sub-segment's tokens are 64 registers.  4 x 4096 x 2048 x 16 gated bf16, this kernel alone:
-// segments of 64 tokens in sub-segments of 8 (128 registers, 8 warps to an SM) 846 us, so (12 warps) 746.
+// segments of 64 tokens in sub-segments of 8 (128 registers, 8 warps to an SM) 846 us, so (12 warps) 744.
 template <int LP>
 struct Segment {
     static constexpr int CP = LP <= 4 ? 32 : 128 / LP, CH = 2 * CP, NT = CP * LP, WARPS = NT / 32;
