@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kThreads = 128, kCols = 8 * kThreads;  // eight columns to a thread
 constexpr int kRows = 64;                            // whose v are in shared memory at once
-constexpr int kCtas = kSms * 4;                       // that are enough to fill the GPU
+constexpr int kCtas = kSms * 4;                      // that are enough to fill the GPU
 
 struct RowsArgs {
     const __nv_bfloat16 *w, *w2;   // [R, C]; w2: the rows from R on
